@@ -37,14 +37,16 @@ __all__ = [
     "reduce_sum", "reduce_rows", "reduce_sum_fixed_order", "reduce_rows_fixed_order",
     "reduce_sum_exact", "reduce_sum_noalloc", "fixed_to_int", "workspace_bytes", "launch_plan", "ArmxError", "Config",
     "PlanInfo", "LIB_PATH",
-    "OP_SUM", "OP_ROWS", "OP_FIXED", "OP_ROWS_FIXED", "OP_EXACT",
+    "rms_norm_rows", "rms_norm_rows_int8", "rms_norm_rows_backward", "quantize_rows_int8",
+    "matmul_int8", "RmsNorm", "RmsNormInt8", "RmsNormGrads", "RowCodes",
+    "OP_SUM", "OP_ROWS", "OP_FIXED", "OP_ROWS_FIXED", "OP_EXACT", "OP_RMS_BACKWARD",
     "FLAG_PLAIN", "FLAG_CACHED_LOADS", "FLAG_ONE_CHAIN", "FLAG_TWO_PASS", "FLAG_MMA_LEVELS",
     "FLAG_MMA_LEAVES", "FLAG_ALL_ONES", "FLAG_INT_LIMBS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libarmx.so")
 
-OP_SUM, OP_ROWS, OP_FIXED, OP_ROWS_FIXED, OP_EXACT = 0, 1, 2, 3, 4
+OP_SUM, OP_ROWS, OP_FIXED, OP_ROWS_FIXED, OP_EXACT, OP_RMS_BACKWARD = 0, 1, 2, 3, 4, 5
 FLAG_PLAIN, FLAG_CACHED_LOADS, FLAG_ONE_CHAIN, FLAG_TWO_PASS = 0x1, 0x2, 0x4, 0x8
 FLAG_MMA_LEVELS = 0x10
 FLAG_MMA_LEAVES = 0x20
@@ -359,3 +361,8 @@ def reduce_rows_fixed_order(x: torch.Tensor, *, out: torch.Tensor | None = None,
     gives each row the order with MFMA leaves of reduce_sum_fixed_order."""
     return _rows_call(lib.reduce_rows_fixed_order, OP_ROWS_FIXED, x, out, workspace,
                       _config(**cfg), "reduce_rows_fixed_order")
+
+
+from .layer import (  # noqa: E402  (needs the names above)
+    RmsNorm, RmsNormGrads, RmsNormInt8, RowCodes, matmul_int8, quantize_rows_int8,
+    rms_norm_rows, rms_norm_rows_backward, rms_norm_rows_int8)

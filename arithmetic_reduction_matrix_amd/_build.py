@@ -26,8 +26,9 @@ PROBE_SOURCES = ["read_probe.hip"]
 
 ARCH = "gfx950"
 HIP_SOURCES = ["sum_kernels.hip", "fixed_kernels.hip", "rows_kernels.hip", "exact_kernels.hip",
-               "rows_fixed_kernels.hip", "levels_kernels.hip", "short_rows_kernels.hip"]
-HOST_SOURCES = ["api.cpp", "plan.cpp"]
+               "rows_fixed_kernels.hip", "levels_kernels.hip", "short_rows_kernels.hip",
+               "norm_kernels.hip", "matmul_int8_kernels.hip"]
+HOST_SOURCES = ["api.cpp", "api_layer.cpp", "plan.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -9,12 +9,17 @@
 
 #include "armx.h"
 #include "launch.h"
+#include "layer.h"
 #include "plan.h"
 
 namespace {
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cu_count[kMaxDevices];
+
+}  // namespace
+
+namespace armx {
 
 // Compute units of the current device (cached); 256 if no device is usable.
 int current_cu_count() {
@@ -29,6 +34,12 @@ int current_cu_count() {
   g_cu_count[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
+
+}  // namespace armx
+
+namespace {
+
+using armx::current_cu_count;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -105,6 +116,15 @@ hipError_t launch_row_plans(const armx::RowPlans& plans, const void* x, float* o
   if (e != hipSuccess || plans.tail_rows == 0) return e;
   const uint16_t* tx = static_cast<const uint16_t*>(x) + head * plans.main.ld;
   return launch(plans.tail, tx, out + head, ws, stream);
+}
+
+// The plan of rms_norm_rows_backward, which takes no configuration but events.
+int plan_backward(size_t rows, size_t cols, const armx_config* cfg, armx::NormBackwardPlan* p) {
+  if (cfg && (cfg->block_threads || cfg->chain_r || cfg->grid_blocks || cfg->flags))
+    return ARMX_ERR_CONFIG;
+  if (rows > armx::kMaxN || cols >= (uint64_t(1) << 31)) return ARMX_ERR_SHAPE;
+  *p = armx::plan_norm_backward(rows, cols, rows && cols ? current_cu_count() : 256);
+  return ARMX_OK;
 }
 
 void log_row_plans(const char* entry, const armx::RowPlans& plans) {
@@ -205,6 +225,10 @@ int reduce_rows_fixed_order(const void* x, size_t rows, size_t cols, size_t ld, 
 
 size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols, const armx_config* cfg) {
   armx::Plan plan;
+  if (op == ARMX_OP_RMS_BACKWARD) {
+    armx::NormBackwardPlan p;
+    return plan_backward(n_or_rows, cols, cfg, &p) == ARMX_OK ? p.ws_bytes : size_t(-1);
+  }
   if (op != ARMX_OP_SUM && op != ARMX_OP_ROWS && op != ARMX_OP_FIXED &&
       op != ARMX_OP_ROWS_FIXED && op != ARMX_OP_EXACT)
     return size_t(-1);
@@ -226,6 +250,20 @@ size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols, const armx_co
 int armx_launch_plan(int op, size_t n_or_rows, size_t cols, const armx_config* cfg,
                      armx_plan_info* info) {
   if (!info) return ARMX_ERR_NULL;
+  if (op == ARMX_OP_RMS_BACKWARD) {
+    armx::NormBackwardPlan p;
+    const int st = plan_backward(n_or_rows, cols, cfg, &p);
+    if (st != ARMX_OK) return st;
+    armx_plan_info r{};
+    r.workspace_bytes = p.ws_bytes;
+    r.grid_blocks = int(p.blocks);
+    r.block_threads = p.blocks ? p.block : 0;
+    r.chain_r = p.blocks ? p.shape.chunks : 0;
+    r.waves_per_cu = double(p.blocks) * double(p.block / 64) / double(current_cu_count());
+    r.launches = cols == 0 ? 0 : p.blocks > 1 ? 2 : 1;
+    *info = r;
+    return ARMX_OK;
+  }
   if (op != ARMX_OP_SUM && op != ARMX_OP_ROWS && op != ARMX_OP_FIXED &&
       op != ARMX_OP_ROWS_FIXED && op != ARMX_OP_EXACT)
     return ARMX_ERR_CONFIG;

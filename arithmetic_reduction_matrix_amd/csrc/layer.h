@@ -1,0 +1,89 @@
+// Arguments and launch shapes of the layer entry points (row norms, 8-bit
+// codes, the product of codes), shared by their C entry points and launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "armx.h"
+
+namespace armx {
+
+// 16-byte loads: 8 values of a 16-bit type.
+constexpr uint32_t kRowVec = 8;
+
+// How a row of `cols` values lies on threads: `threads` per row, each with
+// `chunks` 16-byte loads in registers (chunk j of thread t is the row's chunk
+// j * threads + t).  chunks 0: the row does not fit, and is walked in a loop,
+// twice.  A function of cols only, so a row's bits depend on nothing else.
+struct RowShape {
+  int threads;
+  int chunks;
+};
+
+RowShape row_shape(uint64_t cols);
+constexpr int kRowBlock = 256;  // threads per block of rows of at most that many
+
+struct NormArgs {
+  const uint16_t* x = nullptr;
+  const uint16_t* residual = nullptr;  // may be null
+  const uint16_t* weight = nullptr;    // null: quantise only
+  uint16_t* out = nullptr;             // 16-bit result, or
+  int8_t* codes = nullptr;             // codes and scales
+  float* scales = nullptr;
+  uint16_t* sum_out = nullptr;  // may be null
+  float* inv_rms = nullptr;     // may be null
+  uint64_t rows = 0, cols = 0;
+  uint64_t ldx = 0, ldr = 0, ldo = 0, lds = 0, ldc = 0;
+  float eps = 0;
+  int type = ARMX_F16;
+};
+
+struct NormBackwardArgs {
+  const uint16_t* dy = nullptr;
+  const uint16_t* h = nullptr;
+  const uint16_t* weight = nullptr;
+  const float* inv_rms = nullptr;
+  const uint16_t* dsum = nullptr;  // may be null
+  uint16_t* dx = nullptr;
+  float* dweight = nullptr;
+  float* partials = nullptr;  // blocks x pitch, when there is more than one block
+  uint64_t rows = 0, cols = 0;
+  uint64_t ldy = 0, ldh = 0, ldd = 0, ldx = 0;
+  int type = ARMX_F16;
+};
+
+struct NormBackwardPlan {
+  RowShape shape{};
+  int block = 0;        // threads per block
+  uint64_t blocks = 0;  // each sums dweight over its own rows
+  uint64_t pitch = 0;   // floats between the blocks' partial sums
+  size_t ws_bytes = 0;
+};
+
+NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count);
+
+struct MatmulArgs {
+  const int8_t* a = nullptr;
+  const int8_t* b = nullptr;
+  const float* a_scales = nullptr;
+  const float* b_scales = nullptr;
+  const void* bias = nullptr;  // may be null
+  void* out = nullptr;
+  uint64_t m = 0, n = 0, k = 0, lda = 0, ldb = 0, ldo = 0;
+  int out_type = ARMX_F16;
+};
+
+// Each launches on the current device and stream with the call's events.
+hipError_t launch_norm(const NormArgs& args, const armx_config* cfg, hipStream_t stream);
+hipError_t launch_norm_backward(const NormBackwardArgs& args, const NormBackwardPlan& plan,
+                                const armx_config* cfg, hipStream_t stream);
+hipError_t launch_matmul_int8(const MatmulArgs& args, int cu_count, const armx_config* cfg,
+                              hipStream_t stream);
+
+// Compute units of the current device (api.cpp).
+int current_cu_count();
+
+}  // namespace armx

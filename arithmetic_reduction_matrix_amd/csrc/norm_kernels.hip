@@ -1,0 +1,681 @@
+// Root-mean-square norm of rows with the residual's addition (16-bit or 8-bit
+// result), rows as 8-bit codes, and the norm's backward pass.
+//
+// Every kernel reads and writes each value once: a row lies in the registers
+// of the threads that share it (row_shape), the row's sum of squares and its
+// largest magnitude are combined across lanes and wavefronts, and the result
+// is formed from the registers.  The bound is HBM.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.hpp"
+#include "launch.h"
+#include "layer.h"
+
+namespace armx {
+
+RowShape row_shape(uint64_t cols) {
+  const uint64_t n = (cols + kRowVec - 1) / kRowVec;  // 16-byte chunks
+  if (n <= 8) return {8, 1};
+  if (n <= 16) return {16, 1};
+  if (n <= 32) return {32, 1};
+  if (n <= 64) return {64, 1};
+  if (n <= 128) return {64, 2};
+  if (n <= 256) return {256, 1};
+  if (n <= 512) return {256, 2};
+  if (n <= 1024) return {256, 4};
+  if (n <= 2048) return {512, 4};
+  if (n <= 4096) return {1024, 4};
+  return {1024, 0};
+}
+
+namespace {
+
+using namespace dev;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// ---- the two 16-bit types -------------------------------------------------------
+
+template <int TYPE>
+__device__ __forceinline__ void widen8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (TYPE == ARMX_F16) {
+      f[2 * i] = lo_f32(v[i]);
+      f[2 * i + 1] = hi_f32(v[i]);
+    } else {
+      f[2 * i] = __builtin_bit_cast(float, v[i] << 16);
+      f[2 * i + 1] = __builtin_bit_cast(float, v[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// two values rounded to nearest even, in one word
+template <int TYPE>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  if constexpr (TYPE == ARMX_F16) {
+    return __builtin_bit_cast(uint32_t, half2v{_Float16(a), _Float16(b)});
+  } else {
+    return __builtin_bit_cast(uint32_t, bf16x2{__bf16(a), __bf16(b)});
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = narrow2<TYPE>(f[2 * i], f[2 * i + 1]);
+  return v;
+}
+
+// ---- row pieces -------------------------------------------------------------------
+
+// Chunk `c` (8 values) of a row of `cols` values; values past the row are 0.
+__device__ __forceinline__ u32x4 load_chunk8(const uint16_t* row, uint32_t c, uint32_t cols) {
+  return load8_masked(row, uint64_t(c) * 8, cols, 0u);
+}
+
+__device__ __forceinline__ void store_chunk8(uint16_t* row, uint32_t c, uint32_t cols, u32x4 v) {
+  const uint64_t e = uint64_t(c) * 8;
+  if (e + 8 <= cols) {
+    *reinterpret_cast<u32x4*>(row + e) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i < cols) row[e + i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+}
+
+__device__ __forceinline__ void store_codes8(int8_t* row, uint32_t c, uint32_t cols, u32x2 v) {
+  const uint64_t e = uint64_t(c) * 8;
+  if (e + 8 <= cols) {
+    *reinterpret_cast<u32x2*>(row + e) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i < cols) row[e + i] = int8_t(v[i / 4] >> (8 * (i % 4)));
+}
+
+// ---- combines across the threads of a row ------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Largest of aligned lane groups of 2^levels, in every lane (lane_tree's moves).
+__device__ __forceinline__ uint32_t lane_max(uint32_t v, int levels) {
+  if (levels >= 1) v = max_u32(v, dpp_u32<kDppXor1>(v));
+  if (levels >= 2) v = max_u32(v, dpp_u32<kDppXor2>(v));
+  if (levels >= 3) v = max_u32(v, dpp_u32<kDppHalfMirror>(v));
+  if (levels >= 4) v = max_u32(v, dpp_u32<kDppMirror>(v));
+  if (levels >= 5) {
+    auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max_u32(p[0], p[1]);
+  }
+  if (levels >= 6) {
+    auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max_u32(p[0], p[1]);
+  }
+  return v;
+}
+
+constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
+
+// The row's sum of squares and largest magnitude (bits), in each of its
+// threads.  TPR > 64: over the block's wavefronts through LDS, added in
+// wavefront order by every thread alike.
+template <int TPR>
+struct RowCombine {
+  static constexpr int kWaves = TPR > 64 ? TPR / 64 : 1;
+  struct Lds {
+    float s[kWaves];
+    uint32_t m[kWaves];
+  };
+  // `turn` alternates between the two halves of `lds` from row to row, so one
+  // barrier per row is enough
+  __device__ __forceinline__ static void run(float& s, uint32_t& m, Lds* lds, int turn) {
+    constexpr int levels = log2_of(TPR > 64 ? 64 : TPR);
+    s = lane_tree(s, levels);
+    m = lane_max(m, levels);
+    if constexpr (TPR > 64) {
+      Lds& l = lds[turn];
+      if (lane_id() == 0) {
+        l.s[wave_id()] = s;
+        l.m[wave_id()] = m;
+      }
+      __syncthreads();
+      s = 0.0f;
+      m = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        s += l.s[w];
+        m = max_u32(m, l.m[w]);
+      }
+    }
+  }
+};
+
+// ---- codes ----------------------------------------------------------------------------
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// What a row's codes are made with, from its largest |p|.
+struct CodeScale {
+  float up;      // exact power of two that keeps 127 / top finite and p normal
+  float factor;  // 127 / (top * up); 0 for a row of zeros or not finite
+  float top;     // top * up
+  bool finite;
+  __device__ __forceinline__ explicit CodeScale(uint32_t top_bits) {
+    const float t = __builtin_bit_cast(float, top_bits);
+    finite = top_bits < kInfBits;
+    up = t < 0x1p-64f ? 0x1p60f : 1.0f;
+    top = t * up;
+    factor = finite && t > 0.0f ? 127.0f / top : 0.0f;
+  }
+};
+
+// Codes of 8 products: round half to even of 127 p / top, of the exact
+// quotient.  t = p * factor is off by under 127 * 2^-23 < 2^-16 (the quotient
+// and the product round by 2^-24 each), so it rounds as the exact quotient
+// does unless it is within 2^-14 of a half; there 254 |p| is compared with the
+// odd multiple of top, both exact in binary64 (24 + 8 bits).  Adding 1.5 2^23
+// rounds t to a whole number whose code is the sum's low byte.
+__device__ __forceinline__ u32x2 codes8(const float (&p)[8], const CodeScale& cs) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t q[8];
+  bool near = false;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = (p[i] * cs.up) * cs.factor;
+    const float r = t[i] + kMagic;
+    q[i] = __builtin_bit_cast(uint32_t, r);
+    near |= __builtin_fabsf(t[i] - (r - kMagic)) > 0.5f - 0x1p-14f;
+  }
+  if (__builtin_expect(near, 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = __builtin_fabsf(t[i]);
+      const float k = __builtin_floorf(a);
+      if (__builtin_fabsf(a - k - 0.5f) <= 0x1p-14f) {
+        const double lhs = 254.0 * double(__builtin_fabsf(p[i] * cs.up));
+        const double border = double(2.0f * k + 1.0f) * double(cs.top);
+        int c = int(k);
+        if (lhs > border || (lhs == border && (c & 1))) ++c;
+        q[i] = uint32_t(t[i] < 0.0f ? -c : c);
+      }
+    }
+  }
+  u32x2 v;
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    v[w] = (q[4 * w] & 255u) | (q[4 * w + 1] & 255u) << 8 | (q[4 * w + 2] & 255u) << 16 |
+           q[4 * w + 3] << 24;
+  if (!cs.finite) v = u32x2{0u, 0u};
+  return v;
+}
+
+__device__ __forceinline__ float code_scale(uint32_t top_bits, float inv) {
+  if (top_bits >= kInfBits) return __builtin_nanf("");
+  return __builtin_bit_cast(float, top_bits) * inv / 127.0f;
+}
+
+__device__ __forceinline__ float inv_rms_of(float sum, uint64_t cols, float eps) {
+  return 1.0f / __builtin_sqrtf(sum / float(cols) + eps);
+}
+
+// ---- forward --------------------------------------------------------------------------
+
+// OUT: what the kernel writes.
+constexpr int kOut16 = 0;     // the norm in 16 bits
+constexpr int kOutCodes = 1;  // the norm in codes
+constexpr int kOutQuant = 2;  // the input in codes
+
+// h = x + residual for chunk c of a row, as stored (one rounding)
+template <int TYPE, bool RES>
+__device__ __forceinline__ u32x4 load_sum(const uint16_t* xr, const uint16_t* rr, uint32_t c,
+                                          uint32_t cols) {
+  const u32x4 x = load_chunk8(xr, c, cols);
+  if constexpr (!RES) {
+    return x;
+  } else {
+    const u32x4 r = load_chunk8(rr, c, cols);
+    float a[8], b[8];
+    widen8<TYPE>(x, a);
+    widen8<TYPE>(r, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] += b[i];
+    return narrow8<TYPE>(a);
+  }
+}
+
+// A chunk's share of the sum of squares and of the largest |p|.
+template <int TYPE, int OUT>
+__device__ __forceinline__ void measure_chunk(u32x4 h, u32x4 w, float& s, uint32_t& m) {
+  float f[8];
+  widen8<TYPE>(h, f);
+  if constexpr (OUT != kOutQuant) {
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a = __builtin_fmaf(f[2 * i], f[2 * i], a);
+      b = __builtin_fmaf(f[2 * i + 1], f[2 * i + 1], b);
+    }
+    s += a + b;
+  }
+  if constexpr (OUT == kOutCodes) {
+    float g[8];
+    widen8<TYPE>(w, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= g[i];
+  }
+  if constexpr (OUT != kOut16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_u32(m, __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu);
+  }
+}
+
+template <int TYPE, int OUT>
+__device__ __forceinline__ void finish_chunk(const NormArgs& k, uint64_t row, uint32_t c, u32x4 h,
+                                             u32x4 w, float inv, const CodeScale& cs) {
+  float f[8], g[8];
+  widen8<TYPE>(h, f);
+  if constexpr (OUT != kOutQuant) widen8<TYPE>(w, g);
+  const uint32_t cols = uint32_t(k.cols);
+  if constexpr (OUT == kOut16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
+    store_chunk8(k.out + row * k.ldo, c, cols, narrow8<TYPE>(f));
+  } else {
+    if constexpr (OUT == kOutCodes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= g[i];
+    }
+    store_codes8(k.codes + row * k.ldc, c, cols, codes8(f, cs));
+  }
+}
+
+template <int OUT>
+__device__ __forceinline__ void finish_row(const NormArgs& k, uint64_t row, float inv,
+                                           uint32_t top) {
+  if constexpr (OUT == kOut16) {
+    if (k.inv_rms) k.inv_rms[row] = inv;
+  } else {
+    k.scales[row] = code_scale(top, inv);
+  }
+}
+
+// Rows in registers: TPR threads per row, C chunks each; a block of at least
+// kRowBlock threads takes block / TPR rows at a time.
+template <int TYPE, int OUT, bool RES, int TPR, int C>
+__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel(NormArgs k) {
+  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
+  constexpr int kRows = kBlock / TPR;
+  __shared__ typename RowCombine<TPR>::Lds lds[2];
+  const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
+  const uint32_t chunks = (cols + 7) / 8;
+  u32x4 w[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) w[j] = u32x4{0, 0, 0, 0};
+  if constexpr (OUT != kOutQuant) {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (j * TPR + t < chunks) w[j] = load_chunk8(k.weight, j * TPR + t, cols);
+  }
+  int turn = 0;
+  // every thread of a block makes the same number of rounds (barriers)
+  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows;
+       base += uint64_t(gridDim.x) * kRows, turn ^= 1) {
+    const uint64_t row = base + threadIdx.x / TPR;
+    const bool live = row < k.rows;
+    u32x4 h[C];
+    float s = 0.0f;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+      h[j] = u32x4{0, 0, 0, 0};
+      if (live && c < chunks)
+        h[j] = load_sum<TYPE, RES>(k.x + row * k.ldx, k.residual + row * k.ldr, c, cols);
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+      if (RES && k.sum_out && live && c < chunks)
+        store_chunk8(k.sum_out + row * k.lds, c, cols, h[j]);
+      measure_chunk<TYPE, OUT>(h[j], w[j], s, m);
+    }
+    RowCombine<TPR>::run(s, m, lds, turn);
+    const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
+    const CodeScale cs(m);
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+      if (c < chunks) finish_chunk<TYPE, OUT>(k, row, c, h[j], w[j], inv, cs);
+    }
+    if (t == 0) finish_row<OUT>(k, row, inv, m);
+  }
+}
+
+// Rows too long for the registers: one block per row, walked twice.  The
+// second walk forms h again from what the first read, or reads it from
+// sum_out (where each thread wrote its own chunks), so that outputs may stand
+// where inputs did.
+template <int TYPE, int OUT, bool RES>
+__global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
+  __shared__ typename RowCombine<1024>::Lds lds[2];
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x, turn ^= 1) {
+    const uint16_t* xr = k.x + row * k.ldx;
+    const uint16_t* rr = k.residual + row * k.ldr;
+    float s = 0.0f;
+    uint32_t m = 0;
+    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
+      const u32x4 h = load_sum<TYPE, RES>(xr, rr, c, cols);
+      if (RES && k.sum_out) store_chunk8(k.sum_out + row * k.lds, c, cols, h);
+      const u32x4 w = OUT == kOutCodes ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
+      measure_chunk<TYPE, OUT>(h, w, s, m);
+    }
+    RowCombine<1024>::run(s, m, lds, turn);
+    const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
+    const CodeScale cs(m);
+    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
+      const u32x4 h = RES && k.sum_out ? load_chunk8(k.sum_out + row * k.lds, c, cols)
+                                       : load_sum<TYPE, RES>(xr, rr, c, cols);
+      const u32x4 w = OUT != kOutQuant ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
+      finish_chunk<TYPE, OUT>(k, row, c, h, w, inv, cs);
+    }
+    if (threadIdx.x == 0) finish_row<OUT>(k, row, inv, m);
+  }
+}
+
+constexpr uint64_t kMaxGrid = 0x7FFFFFFF / 1024;  // the runtime counts threads in 32 bits
+
+hipError_t launch_rows_kernel(const void* fn, uint64_t blocks, int threads, void** args,
+                              const armx_config* cfg, hipStream_t stream, bool first = true,
+                              bool last = true) {
+  return launch_kernel(fn, dim3(unsigned(blocks)), dim3(unsigned(threads)), args, 0, stream,
+                       cfg && first ? static_cast<hipEvent_t>(cfg->start_event) : nullptr,
+                       cfg && last ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
+}
+
+template <int TYPE, int OUT, bool RES>
+hipError_t launch_norm_typed(const NormArgs& a, const armx_config* cfg, hipStream_t stream) {
+  const RowShape s = row_shape(a.cols);
+  const void* fn = nullptr;
+#define ARMX_NORM_CASE(T, C) \
+  if (s.threads == T && s.chunks == C) \
+    fn = reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, T, C>)
+  ARMX_NORM_CASE(8, 1);
+  ARMX_NORM_CASE(16, 1);
+  ARMX_NORM_CASE(32, 1);
+  ARMX_NORM_CASE(64, 1);
+  ARMX_NORM_CASE(64, 2);
+  ARMX_NORM_CASE(256, 1);
+  ARMX_NORM_CASE(256, 2);
+  ARMX_NORM_CASE(256, 4);
+  ARMX_NORM_CASE(512, 4);
+  ARMX_NORM_CASE(1024, 4);
+#undef ARMX_NORM_CASE
+  if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_loop_kernel<TYPE, OUT, RES>);
+  const int block = s.threads > kRowBlock ? s.threads : kRowBlock;
+  const uint64_t per = uint64_t(block / s.threads);
+  uint64_t blocks = (a.rows + per - 1) / per;
+  if (blocks > kMaxGrid) blocks = kMaxGrid;
+  NormArgs copy = a;
+  void* args[] = {&copy};
+  return launch_rows_kernel(fn, blocks, block, args, cfg, stream);
+}
+
+template <int TYPE>
+hipError_t launch_norm_out(const NormArgs& a, const armx_config* cfg, hipStream_t stream) {
+  if (!a.weight) return launch_norm_typed<TYPE, kOutQuant, false>(a, cfg, stream);
+  if (a.codes)
+    return a.residual ? launch_norm_typed<TYPE, kOutCodes, true>(a, cfg, stream)
+                      : launch_norm_typed<TYPE, kOutCodes, false>(a, cfg, stream);
+  return a.residual ? launch_norm_typed<TYPE, kOut16, true>(a, cfg, stream)
+                    : launch_norm_typed<TYPE, kOut16, false>(a, cfg, stream);
+}
+
+// ---- backward ---------------------------------------------------------------------------
+
+// Block b takes the row groups b, b + blocks, ...; every thread keeps the
+// dweight sums of its own columns in registers over the block's rows.  A block
+// of several rows at a time adds its row groups' sums through LDS, in order.
+template <int TYPE, bool DSUM, int TPR, int C>
+__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backward_kernel(
+    NormBackwardArgs k, float* dst, uint64_t pitch) {
+  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
+  constexpr int kRows = kBlock / TPR;
+  __shared__ typename RowCombine<TPR>::Lds lds[2];
+  __shared__ float part[kRows > 1 ? kRows * TPR * C * 8 : 1];
+  const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
+  const uint32_t chunks = (cols + 7) / 8;
+  u32x4 w[C];
+  float acc[C][8];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    w[j] = u32x4{0, 0, 0, 0};
+    if (j * TPR + t < chunks) w[j] = load_chunk8(k.weight, j * TPR + t, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
+  }
+  int turn = 0;
+  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows;
+       base += uint64_t(gridDim.x) * kRows, turn ^= 1) {
+    const uint64_t row = base + threadIdx.x / TPR;
+    const bool live = row < k.rows;
+    u32x4 dy[C], h[C], ds[C];
+    float dot = 0.0f;
+    const float inv = live ? k.inv_rms[row] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+      dy[j] = h[j] = ds[j] = u32x4{0, 0, 0, 0};
+      if (live && c < chunks) {
+        dy[j] = load_chunk8(k.dy + row * k.ldy, c, cols);
+        h[j] = load_chunk8(k.h + row * k.ldh, c, cols);
+        if constexpr (DSUM) ds[j] = load_chunk8(k.dsum + row * k.ldd, c, cols);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      float fy[8], fh[8], fw[8];
+      widen8<TYPE>(dy[j], fy);
+      widen8<TYPE>(h[j], fh);
+      widen8<TYPE>(w[j], fw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
+        if (live) acc[j][i] = __builtin_fmaf(fy[i], fh[i] * inv, acc[j][i]);
+      }
+    }
+    uint32_t unused = 0;
+    RowCombine<TPR>::run(dot, unused, lds, turn);
+    if (!live) continue;
+    const float f = inv * inv * (dot / float(k.cols));
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+      if (c >= chunks) continue;
+      float fy[8], fh[8], fw[8], fd[8];
+      widen8<TYPE>(dy[j], fy);
+      widen8<TYPE>(h[j], fh);
+      widen8<TYPE>(w[j], fw);
+      if constexpr (DSUM) widen8<TYPE>(ds[j], fd);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
+        if constexpr (DSUM) fy[i] += fd[i];
+      }
+      store_chunk8(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+    }
+  }
+  if constexpr (kRows > 1) {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        part[(threadIdx.x / TPR) * (TPR * C * 8) + (j * TPR + t) * 8 + i] = acc[j][i];
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < cols; e += kBlock) {
+      float v = part[e];
+      for (int r = 1; r < kRows; ++r) v += part[r * (TPR * C * 8) + e];
+      dst[uint64_t(blockIdx.x) * pitch + e] = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t c = j * TPR + t;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c * 8 + i < cols) dst[uint64_t(blockIdx.x) * pitch + c * 8 + i] = acc[j][i];
+    }
+  }
+}
+
+// Rows too long for the registers: two walks per row, the block's dweight sums
+// kept in its own row of `dst` (each thread reads and writes its own columns).
+template <int TYPE, bool DSUM>
+__global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardArgs k, float* dst,
+                                                                  uint64_t pitch) {
+  __shared__ typename RowCombine<1024>::Lds lds[2];
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+  float* sums = dst + uint64_t(blockIdx.x) * pitch;
+  for (uint32_t c = threadIdx.x; c < chunks; c += 1024)
+    for (uint32_t i = 0; i < 8; ++i)
+      if (c * 8 + i < cols) sums[c * 8 + i] = 0.0f;
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x, turn ^= 1) {
+    const uint16_t* yr = k.dy + row * k.ldy;
+    const uint16_t* hr = k.h + row * k.ldh;
+    const float inv = k.inv_rms[row];
+    float dot = 0.0f;
+    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
+      float fy[8], fh[8], fw[8];
+      widen8<TYPE>(load_chunk8(yr, c, cols), fy);
+      widen8<TYPE>(load_chunk8(hr, c, cols), fh);
+      widen8<TYPE>(load_chunk8(k.weight, c, cols), fw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
+    }
+    uint32_t unused = 0;
+    RowCombine<1024>::run(dot, unused, lds, turn);
+    const float f = inv * inv * (dot / float(k.cols));
+    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
+      float fy[8], fh[8], fw[8], fd[8];
+      widen8<TYPE>(load_chunk8(yr, c, cols), fy);
+      widen8<TYPE>(load_chunk8(hr, c, cols), fh);
+      widen8<TYPE>(load_chunk8(k.weight, c, cols), fw);
+      if constexpr (DSUM) widen8<TYPE>(load_chunk8(k.dsum + row * k.ldd, c, cols), fd);
+      for (uint32_t i = 0; i < 8; ++i)
+        if (c * 8 + i < cols) sums[c * 8 + i] = __builtin_fmaf(fy[i], fh[i] * inv, sums[c * 8 + i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
+        if constexpr (DSUM) fy[i] += fd[i];
+      }
+      store_chunk8(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+    }
+  }
+}
+
+// dweight[c] = the sum of the blocks' partial sums, in block order within each
+// of 8 interleaved parts, then the parts in order.
+constexpr int kJoinCols = 32, kJoinParts = 8;
+__global__ __launch_bounds__(kJoinCols* kJoinParts) void norm_join_kernel(const float* partials,
+                                                                          uint64_t blocks,
+                                                                          uint64_t pitch,
+                                                                          uint64_t cols,
+                                                                          float* dweight) {
+  __shared__ float part[kJoinParts][kJoinCols];
+  const uint32_t tc = threadIdx.x % kJoinCols, tp = threadIdx.x / kJoinCols;
+  const uint64_t c = uint64_t(blockIdx.x) * kJoinCols + tc;
+  float v = 0.0f;
+  if (c < cols)
+    for (uint64_t b = tp; b < blocks; b += kJoinParts) v += partials[b * pitch + c];
+  part[tp][tc] = v;
+  __syncthreads();
+  if (tp == 0 && c < cols) {
+    for (int p = 1; p < kJoinParts; ++p) v += part[p][tc];
+    dweight[c] = v;
+  }
+}
+
+template <int TYPE, bool DSUM>
+hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPlan& plan,
+                                 const armx_config* cfg, hipStream_t stream) {
+  const RowShape s = plan.shape;
+  const void* fn = nullptr;
+#define ARMX_NORM_CASE(T, C) \
+  if (s.threads == T && s.chunks == C) \
+    fn = reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, T, C>)
+  ARMX_NORM_CASE(8, 1);
+  ARMX_NORM_CASE(16, 1);
+  ARMX_NORM_CASE(32, 1);
+  ARMX_NORM_CASE(64, 1);
+  ARMX_NORM_CASE(64, 2);
+  ARMX_NORM_CASE(256, 1);
+  ARMX_NORM_CASE(256, 2);
+  ARMX_NORM_CASE(256, 4);
+  ARMX_NORM_CASE(512, 4);
+  ARMX_NORM_CASE(1024, 4);
+#undef ARMX_NORM_CASE
+  if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_backward_loop_kernel<TYPE, DSUM>);
+  NormBackwardArgs copy = a;
+  const bool join = plan.blocks > 1;
+  float* dst = join ? a.partials : a.dweight;
+  uint64_t pitch = join ? plan.pitch : 0;
+  void* args[] = {&copy, &dst, &pitch};
+  hipError_t e = launch_rows_kernel(fn, plan.blocks, plan.block, args, cfg, stream, true, !join);
+  if (e != hipSuccess || !join) return e;
+  const float* partials = a.partials;
+  uint64_t blocks = plan.blocks, cols = a.cols;
+  float* dweight = a.dweight;
+  void* join_args[] = {&partials, &blocks, &pitch, &cols, &dweight};
+  return launch_rows_kernel(reinterpret_cast<const void*>(&norm_join_kernel),
+                            (cols + kJoinCols - 1) / kJoinCols, kJoinCols * kJoinParts, join_args,
+                            cfg, stream, false, true);
+}
+
+}  // namespace
+
+NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) {
+  NormBackwardPlan p;
+  p.shape = row_shape(cols);
+  p.block = p.shape.threads > kRowBlock ? p.shape.threads : kRowBlock;
+  if (rows == 0 || cols == 0) return p;
+  const uint64_t per = uint64_t(p.block / p.shape.threads);
+  const uint64_t groups = (rows + per - 1) / per;
+  const uint64_t most = uint64_t(cu_count) * (1024 / uint64_t(p.block));
+  p.blocks = groups < most ? groups : most;
+  p.pitch = (cols + 63) / 64 * 64;
+  if (p.blocks > 1) p.ws_bytes = size_t(p.blocks * p.pitch * sizeof(float));
+  return p;
+}
+
+hipError_t launch_norm(const NormArgs& args, const armx_config* cfg, hipStream_t stream) {
+  return args.type == ARMX_F16 ? launch_norm_out<ARMX_F16>(args, cfg, stream)
+                               : launch_norm_out<ARMX_BF16>(args, cfg, stream);
+}
+
+hipError_t launch_norm_backward(const NormBackwardArgs& a, const NormBackwardPlan& plan,
+                                const armx_config* cfg, hipStream_t stream) {
+  if (a.type == ARMX_F16)
+    return a.dsum ? launch_backward_typed<ARMX_F16, true>(a, plan, cfg, stream)
+                  : launch_backward_typed<ARMX_F16, false>(a, plan, cfg, stream);
+  return a.dsum ? launch_backward_typed<ARMX_BF16, true>(a, plan, cfg, stream)
+                : launch_backward_typed<ARMX_BF16, false>(a, plan, cfg, stream);
+}
+
+}  // namespace armx

@@ -377,18 +377,158 @@ int reduce_sum_exact(const void* x, size_t n, float* out, int64_t* out_fixed, vo
 int reduce_sum_noalloc(const void* x, size_t n, float* out, const armx_config* cfg,
                        void* stream);
 
+/* ---- rows of a layer: norms, 8-bit codes, and their product ----------------
+ *
+ * What stands on both sides of a matrix product in a transformer layer: the
+ * root-mean-square norm of rows with the residual's addition (forward and
+ * backward), rows turned into 8-bit codes with one scale per row, and the
+ * product of such codes.  The conventions above hold, and:
+ * - `type` is an armx_type.  Inputs and 16-bit outputs of one call share it.
+ * - Matrices are row-major with a pitch of their own (ld*, in elements, at
+ *   least the row's length).  Rows of 16-bit values start at multiples of 16
+ *   bytes (pointer 16-byte aligned, pitch a multiple of 8 when there is more
+ *   than one row); rows of codes too (pitch a multiple of 16).  Pitch padding
+ *   is never written, and never read but where matmul_int8 says so.
+ * - `cfg` may give the two events only; every other field must be zero
+ *   (ARMX_ERR_CONFIG).
+ * - A row's result depends on that row's values (and weight, scales and bias)
+ *   and on the row's length only, not on how many rows there are or where it
+ *   stands (batch invariance); dweight, a sum over rows, depends on the row
+ *   count and the device's compute-unit count too.  Nothing depends on timing.
+ * - Row counts of 0 write nothing.  At most 2^40 elements from a matrix's
+ *   first to its last, rows of fewer than 2^31, codes as matmul_int8 says.
+ */
+typedef enum armx_type {
+  ARMX_F16 = 0,  /* IEEE binary16 */
+  ARMX_BF16 = 1, /* bfloat16      */
+  ARMX_F32 = 2   /* IEEE binary32 */
+} armx_type;
+
+/*
+ * rms_norm_rows -- root-mean-square norm of every row, after the residual's
+ * addition:
+ *   h[r][c]   = x[r][c] + residual[r][c], rounded once to `type`
+ *               (x itself when residual is NULL)
+ *   inv[r]    = 1 / sqrt(sum over c of h[r][c]^2 / cols + eps)
+ *   out[r][c] = (h[r][c] * inv[r]) * weight[c], rounded once to `type`
+ * with sums, inv and products in binary32.
+ *
+ * x, residual  device, rows x cols, ARMX_F16 or ARMX_BF16; residual may be NULL.
+ * weight       device, cols values of `type`, 16-byte aligned.
+ * eps          at least 0.
+ * out          device, rows x cols.
+ * sum_out      device, receives h; may be NULL (h is not written) and must be
+ *              without a residual.
+ * inv_rms      device, rows binary32 (inv, for the backward pass), or NULL.
+ * out or sum_out may be x or residual themselves (same pointer and pitch);
+ * nothing else may overlap.  A sum of squares past binary32's range counts as
+ * an infinity (inv 0); a NaN or an infinity in a row makes NaNs in that row.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other
+ * than the two, or an eps that is negative or NaN, is ARMX_ERR_CONFIG.
+ */
+int rms_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
+                  const void* weight, int type, size_t rows, size_t cols, float eps, void* out,
+                  size_t ldo, void* sum_out, size_t lds, float* inv_rms,
+                  const armx_config* cfg, void* stream);
+
+/*
+ * rms_norm_rows_int8 -- the same norm with its result in 8-bit codes:
+ *   p[r][c]     = h[r][c] * weight[c] in binary32
+ *   codes[r][c] = 127 p[r][c] / max over c of |p[r][c]|, rounded half to even
+ *   scales[r]   = (max over c of |p[r][c]|) * inv[r] / 127 in binary32
+ * so that codes * scales stands for the norm.  The rounding of codes is that
+ * of the exact quotient, so the codes are the same on every device and do
+ * not depend on the order of any sum.  A row of zeros (or cols == 0) has codes
+ * and scale 0; a row in which some p is a NaN or an infinity has codes 0 and
+ * scale NaN.
+ *
+ * x, residual, weight, type, eps, sum_out as for rms_norm_rows.
+ * codes   device, rows x cols int8, 16-byte aligned rows, -127 .. 127.
+ * scales  device, rows binary32.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}.
+ */
+int rms_norm_rows_int8(const void* x, size_t ldx, const void* residual, size_t ldr,
+                       const void* weight, int type, size_t rows, size_t cols, float eps,
+                       int8_t* codes, size_t ldc, float* scales, void* sum_out, size_t lds,
+                       const armx_config* cfg, void* stream);
+
+/*
+ * quantize_rows_int8 -- rows of a matrix as 8-bit codes with one scale each:
+ * codes and scales as in rms_norm_rows_int8 with p = x and inv = 1.  A weight
+ * matrix stored output-major becomes matmul_int8's second operand with one
+ * scale per output channel.  Returns as rms_norm_rows_int8.
+ */
+int quantize_rows_int8(const void* x, size_t ldx, int type, size_t rows, size_t cols,
+                       int8_t* codes, size_t ldc, float* scales, const armx_config* cfg,
+                       void* stream);
+
+/*
+ * rms_norm_rows_backward -- gradients of rms_norm_rows: with g = dy * weight,
+ *   dx[r][c]   = inv[r] * (g[r][c] - h[r][c] * inv[r]^2 * mean over c of (g[r][c] h[r][c]))
+ *                + dsum[r][c], rounded once to `type`
+ *   dweight[c] = sum over r of dy[r][c] * (h[r][c] * inv[r]), in binary32.
+ * dx is the gradient of x and of residual alike (h is their sum).
+ *
+ * dy       device, rows x cols, the gradient of out.
+ * h        device, rows x cols, what was normalised (sum_out, or x).
+ * inv_rms  device, rows binary32, as rms_norm_rows wrote them.
+ * dsum     device, rows x cols, the gradient that flows into sum_out from
+ *          elsewhere, or NULL.
+ * dx       device, rows x cols; may be dy or dsum themselves.
+ * dweight  device, cols binary32, 16-byte aligned; zeros when rows == 0.
+ * ws       device workspace of armx_workspace_bytes(ARMX_OP_RMS_BACKWARD, rows,
+ *          cols, NULL) bytes; it needs no zeros and none are left (it has no
+ *          counter region).  NULL when that is 0.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
+ */
+int rms_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh,
+                           const void* weight, const float* inv_rms, const void* dsum,
+                           size_t ldd, int type, size_t rows, size_t cols, void* dx,
+                           size_t ldx, float* dweight, void* ws, size_t ws_bytes,
+                           const armx_config* cfg, void* stream);
+
+/*
+ * matmul_int8 -- product of two matrices of 8-bit codes, both with rows along
+ * the sum, with a scale for each row of either:
+ *   out[i][j] = sum over t < k of a[i][t] * b[j][t], exact in 32-bit integers,
+ *               converted to binary32, times (a_scales[i] * b_scales[j]),
+ *               plus bias[j], each step one binary32 rounding, then rounded
+ *               once to out_type.
+ * The integer sum is exact, so out[i][j] does not depend on tiles, on m, n or
+ * on any split of k: the product is batch invariant by construction.
+ *
+ * a         device, m x k int8 (any value, -128 too), rows 16-byte aligned.
+ * b         device, n x k int8 (a linear layer's weight, one output channel
+ *           per row), rows 16-byte aligned.
+ *           Every row's first 16 ceil(k / 16) bytes must be readable, the last
+ *           row's too; what stands past k is not used.
+ * a_scales  device, m binary32; b_scales device, n binary32.
+ * bias      device, n values of out_type, or NULL.
+ * out       device, m x n of out_type (ARMX_F16, ARMX_BF16 or ARMX_F32), any
+ *           pitch and any alignment its type has.
+ * k         at most 131071, so that no sum of products can leave 32 bits;
+ *           k == 0 gives the bias (or 0) where both scales are finite.
+ * lda, ldb  at most 2^23; m and n at most 2^30.
+ * Needs no workspace.  Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}.
+ */
+int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t* b, size_t ldb,
+                const float* b_scales, const void* bias, size_t m, size_t n, size_t k,
+                void* out, size_t ldo, int out_type, const armx_config* cfg, void* stream);
+
 /* Operation codes for armx_workspace_bytes. */
 #define ARMX_OP_SUM 0
 #define ARMX_OP_ROWS 1
 #define ARMX_OP_FIXED 2
 #define ARMX_OP_ROWS_FIXED 3
 #define ARMX_OP_EXACT 4
+#define ARMX_OP_RMS_BACKWARD 5
 
 /*
  * armx_workspace_bytes -- bytes of workspace the matching call needs on the
  * current device with this configuration (0 if none).  `n_or_rows` is n for
- * ARMX_OP_SUM / ARMX_OP_FIXED / ARMX_OP_EXACT and rows for ARMX_OP_ROWS and
- * ARMX_OP_ROWS_FIXED; `cols` is used by those two only.  Returns (size_t)-1
+ * ARMX_OP_SUM / ARMX_OP_FIXED / ARMX_OP_EXACT and rows for ARMX_OP_ROWS,
+ * ARMX_OP_ROWS_FIXED and ARMX_OP_RMS_BACKWARD; `cols` is used by those three
+ * only (the last op's workspace has no counter region).  Returns (size_t)-1
  * for an invalid op or configuration.  Needs no GPU: without a device it
  * assumes 256 compute units.
  */
