@@ -62,114 +62,472 @@ __device__ __forceinline__ u32x4 keep_codes(u32x4 v, int keep) {
   return v;
 }
 
-// Scales, bias and rounding of 4 consecutive columns of one row, stored.
-template <int OUT>
-__device__ __forceinline__ void store_out4(const MatmulArgs& p, uint64_t i, uint64_t j, i32x4 acc,
-                                           bool wide) {
-  if (i >= p.m || j >= p.n) return;
-  const float sa = p.a_scales[i];
-  float y[4];
+// ---- scales, bias, rounding ---------------------------------------------------
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// The epilogue of one lane's C consecutive columns (a multiple of 4), whose
+// scales and bias stay in registers while its rows pass.
+template <int OUT, int C>
+struct Columns {
+  const MatmulArgs& p;
+  uint64_t j;
+  bool wide;  // all of the columns exist and every row's take whole 8- or 16-byte stores
+  float scale[C], bias[C];
+
+  __device__ __forceinline__ float bias_at(uint64_t c) const {
+    if constexpr (OUT == ARMX_F32) return static_cast<const float*>(p.bias)[c];
+    if constexpr (OUT == ARMX_F16) return float(static_cast<const _Float16*>(p.bias)[c]);
+    return float(static_cast<const __bf16*>(p.bias)[c]);
+  }
+
+  // `aligned`: rows of out start at multiples of a store
+  __device__ __forceinline__ Columns(const MatmulArgs& args, uint64_t first, bool aligned)
+      : p(args), j(first), wide(aligned && first + C <= args.n) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint64_t jc = j + c < p.n ? j + c : p.n - 1;
-    y[c] = float(acc[c]) * (sa * p.b_scales[jc]);
+    for (int c = 0; c < C; c += 4) {
+      if (j + c + 4 <= p.n) {
+        const f32x4u v = *reinterpret_cast<const f32x4u*>(p.b_scales + j + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scale[c + e] = v[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scale[c + e] = j + c + e < p.n ? p.b_scales[j + c + e] : 0.0f;
+      }
+    }
     if (p.bias) {
-      if constexpr (OUT == ARMX_F32)
-        y[c] += static_cast<const float*>(p.bias)[jc];
-      else if constexpr (OUT == ARMX_F16)
-        y[c] += float(static_cast<const _Float16*>(p.bias)[jc]);
-      else
-        y[c] += float(static_cast<const __bf16*>(p.bias)[jc]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) bias[c] = j + c < p.n ? bias_at(j + c) : 0.0f;
     }
   }
-  const bool full = wide && j + 4 <= p.n;
-  if constexpr (OUT == ARMX_F32) {
-    float* o = static_cast<float*>(p.out) + i * p.ldo + j;
-    if (full) {
-      *reinterpret_cast<floatx4*>(o) = floatx4{y[0], y[1], y[2], y[3]};
-      return;
-    }
+
+  // Row i: float(sum) * (row scale * column scale) + bias, each step one
+  // rounding, then one to the output's type.
+  __device__ __forceinline__ void store(uint64_t i, const i32x4 (&sums)[C / 4]) const {
+    if (i >= p.m) return;
+    const float sa = p.a_scales[i];
+    float y[C];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j + c < p.n) o[c] = y[c];
-  } else {
-    u32x2 v;
-    if constexpr (OUT == ARMX_F16) {
-      v[0] = __builtin_bit_cast(uint32_t, half2v{_Float16(y[0]), _Float16(y[1])});
-      v[1] = __builtin_bit_cast(uint32_t, half2v{_Float16(y[2]), _Float16(y[3])});
+    for (int c = 0; c < C; ++c) y[c] = float(sums[c / 4][c % 4]) * (sa * scale[c]);
+    if (p.bias) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) y[c] += bias[c];
+    }
+    if constexpr (OUT == ARMX_F32) {
+      float* o = static_cast<float*>(p.out) + i * p.ldo + j;
+      if (wide) {
+#pragma unroll
+        for (int c = 0; c < C; c += 4)
+          *reinterpret_cast<floatx4*>(o + c) = floatx4{y[c], y[c + 1], y[c + 2], y[c + 3]};
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (j + c < p.n) o[c] = y[c];
+      }
     } else {
-      v[0] = __builtin_bit_cast(uint32_t, bf16x2{__bf16(y[0]), __bf16(y[1])});
-      v[1] = __builtin_bit_cast(uint32_t, bf16x2{__bf16(y[2]), __bf16(y[3])});
-    }
-    uint16_t* o = static_cast<uint16_t*>(p.out) + i * p.ldo + j;
-    if (full) {
-      *reinterpret_cast<u32x2*>(o) = v;
-      return;
-    }
+      uint32_t v[C / 2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j + c < p.n) o[c] = uint16_t(v[c / 2] >> (16 * (c % 2)));
+      for (int c = 0; c < C; c += 2) {
+        if constexpr (OUT == ARMX_F16)
+          v[c / 2] = __builtin_bit_cast(uint32_t, half2v{_Float16(y[c]), _Float16(y[c + 1])});
+        else
+          v[c / 2] = __builtin_bit_cast(uint32_t, bf16x2{__bf16(y[c]), __bf16(y[c + 1])});
+      }
+      uint16_t* o = static_cast<uint16_t*>(p.out) + i * p.ldo + j;
+      if (wide) {
+        if constexpr (C % 8 == 0) {
+#pragma unroll
+          for (int c = 0; c < C / 2; c += 4)
+            *reinterpret_cast<u32x4*>(o + 2 * c) = u32x4{v[c], v[c + 1], v[c + 2], v[c + 3]};
+        } else {
+          static_assert(C == 4, "whole stores");
+          *reinterpret_cast<u32x2*>(o) = u32x2{v[0], v[1]};
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (j + c < p.n) o[c] = uint16_t(v[c / 2] >> (16 * (c % 2)));
+      }
+    }
   }
+};
+
+// Whether rows of out start at multiples of 16 bytes (the widest store).
+inline int aligned_rows(const MatmulArgs& p) {
+  const uint64_t size = p.out_type == ARMX_F32 ? 4 : 2;
+  return p.ldo * size % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
 }
 
-// 64 x 64 outputs per block, 32 x 32 per wavefront, operands straight from
-// memory to the MFMA's registers.
-template <int OUT>
-__global__ __launch_bounds__(256) void matmul_direct_kernel(MatmulArgs p, uint64_t tiles_n,
-                                                            int wide) {
-  const uint64_t ti = blockIdx.x / tiles_n, tj = blockIdx.x % tiles_n;
-  const int lane = lane_id(), w = wave_id();
-  const uint64_t i0 = ti * 64 + (w & 1) * 32, j0 = tj * 64 + (w >> 1) * 32;
+// ---- tiles staged through LDS -------------------------------------------------
+//
+// A block makes BM x BN outputs.  Its wavefronts form KS groups of WM x WN that
+// share k: a group takes every KS-th step of 128 codes and sums over its own.
+// A step's rows of a and b go from memory straight to LDS (buffer_load ... lds,
+// 16 bytes per lane, 8 rows of 128 bytes per wavefront load) into one of the
+// group's two buffers while the other is multiplied.  (Steps of 64 codes in four
+// buffers, with rows of 64 bytes, measured slower, 8192^3 450 -> 715 us: memory
+// moves lines of 128 bytes, and each was moved twice.)
+//
+// Row 4 q + e of a wavefront's operand tile y of b is its column 4 (q kNT + y) + e,
+// so that the lanes of group q end with 4 kNT consecutive columns of a row over the
+// tiles, which they store together.
+//
+// LDS rows are 128 bytes, 8 slots of 16; row r keeps its piece c in slot
+// c ^ swizzle(r), taken of the row's place in its operand tile.  A 16-byte LDS read serves 16 lanes at a time (lanes 0-3,
+// 12-15, 20-23 and 24-27 first, and so on) from 64 banks, that is from 16
+// slots: rows r and r + 1 lie in different halves of them, and the rows of
+// one parity that are read together differ in swizzle (no bank conflicts, by
+// count).  The load writes LDS in lane order, so the swizzle is made on the
+// memory side: the lane that fills slot s of row r fetches piece s ^ swizzle(r).
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
+
+constexpr int kStepK = 128;
+#define ARMX_INLINE __attribute__((always_inline))
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
+template <int BM, int BN, int WM, int WN, int KS>
+struct Tile {
+  static constexpr int kGroup = WM * WN;  // wavefronts of a group
+  static constexpr int kWaves = kGroup * KS;
+  static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
+  static constexpr int kNT = BN / WN / 16;
+  static constexpr int kLoadsA = BM / 8 / kGroup;  // wavefront loads per step
+  static constexpr int kLoadsB = BN / 8 / kGroup;
+  static constexpr int kStageBytes = (BM + BN) * kStepK;
+  static constexpr int kSumBytes = KS > 1 ? KS * BM * BN * 4 : 0;
+  static constexpr int kLdsBytes =
+      2 * KS * kStageBytes > kSumBytes ? 2 * KS * kStageBytes : kSumBytes;
+  static_assert(kLoadsA * 8 * kGroup == BM && kLoadsB * 8 * kGroup == BN, "whole loads");
+  static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
+};
+
+typedef __attribute__((address_space(3))) int8_t lds_byte;
+
+// 16 bytes per lane from `rows` into LDS at `lds` + 16 lane.  Written as asm so
+// that the compiler, which cannot tell the two buffers apart, does not wait for
+// these loads before every read of LDS; nothing comes back in registers, and
+// wait_loads() and a barrier stand between these writes and their reads.
+__device__ __forceinline__ void lds_load16(const CodeRows& rows, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(rows.rs)
+               : "memory");
+}
+
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
+  return *reinterpret_cast<const u32x4 __attribute__((address_space(3)))*>(at);
+}
+
+// vmcnt(0): this wavefront's loads into LDS have landed
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// Which tile a block makes: every XCD takes a contiguous range of ids, and ids
+// run down 4 rows of tiles before the next column, so that blocks running at
+// the same time on one XCD share operand rows in its L2.
+constexpr unsigned kTileGroup = 4;
+__device__ __forceinline__ void tile_of_block(unsigned tiles_m, unsigned tiles_n, unsigned& ti,
+                                              unsigned& tj) {
+  const unsigned id = unsigned(xcd_block_id());
+  const unsigned per = kTileGroup * tiles_n, grp = id / per, first = grp * kTileGroup;
+  const unsigned rows = tiles_m - first < kTileGroup ? tiles_m - first : kTileGroup;
+  const unsigned in = id - grp * per;
+  ti = first + in % rows;
+  tj = in / rows;
+}
+
+template <int BM, int BN, int WM, int WN, int KS, int OUT>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(MatmulArgs p,
+                                                                           unsigned tiles_m,
+                                                                           unsigned tiles_n,
+                                                                           int aligned) {
+  using T = Tile<BM, BN, WM, WN, KS>;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
+  const int lane = lane_id(), group = wave_id() / T::kGroup, w = wave_id() % T::kGroup;
+  // the buffer in use; flip - base is the other
+  uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_byte*)lds)) +
+                  uint32_t(group) * (2 * T::kStageBytes);
+  const uint32_t flip = 2 * base + T::kStageBytes;
+  unsigned ti, tj;
+  tile_of_block(tiles_m, tiles_n, ti, tj);
+  const uint64_t i0 = uint64_t(ti) * BM, j0 = uint64_t(tj) * BN;
   const CodeRows a(p.a, p.m, p.lda, p.k, i0), b(p.b, p.n, p.ldb, p.k, j0);
-  const uint32_t r = lane & 15, g = uint32_t(lane >> 4) * 16;
-  const uint32_t lda = uint32_t(p.lda), ldb = uint32_t(p.ldb), k = uint32_t(p.k);
-  i32x4 acc[2][2];
+  const uint32_t k = uint32_t(p.k);
+  // rows past the matrix are read from its last row; their outputs are not stored
+  uint32_t off_a[T::kLoadsA], off_b[T::kLoadsB];
+  const uint32_t last_a = uint32_t(p.m - 1 - i0 < BM ? p.m - 1 - i0 : BM - 1);
+  const uint32_t last_b = uint32_t(p.n - 1 - j0 < BN ? p.n - 1 - j0 : BN - 1);
+  // byte offset of the piece that this lane brings into its slot of tile row
+  // `row`, which is row `at` of an operand tile
+  auto source = [&](uint32_t row, uint32_t at, uint32_t last, uint32_t ld) ARMX_INLINE {
+    return (row < last ? row : last) * ld + ((uint32_t(lane) & 7) ^ swizzle(at)) * 16;
+  };
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int y = 0; y < 2; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
-  for (uint32_t t = 0; t < k; t += 64) {
-    u32x4 va[2], vb[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      va[x] = keep_codes(a.load((r + 16 * x) * lda + t + g), int(k) - int(t + g));
-      vb[x] = b.load((r + 16 * x) * ldb + t + g);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) acc[x][y] = mfma_i8(vb[y], va[x], acc[x][y]);
+  for (int x = 0; x < T::kLoadsA; ++x) {
+    const uint32_t row = (w * T::kLoadsA + x) * 8 + (lane >> 3);
+    off_a[x] = source(row, row, last_a, uint32_t(p.lda));
   }
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int x = 0; x < T::kLoadsB; ++x) {
+    const uint32_t row = (w * T::kLoadsB + x) * 8 + (lane >> 3);
+    off_b[x] = source(row, row / (4 * T::kNT) * 4 + row % 4, last_b, uint32_t(p.ldb));
+  }
+  // wavefront load x of the step at k0, into the buffer at `to`
+  auto stage_one = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    if (x < T::kLoadsA) {
+      lds_load16(a, to + (w * T::kLoadsA + x) * 1024, off_a[x] + k0);
+    } else {
+      x -= T::kLoadsA;
+      lds_load16(b, to + BM * kStepK + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
+    }
+  };
+  constexpr int kLoads = T::kLoadsA + T::kLoadsB;
+  auto stage = [&](uint32_t to, uint32_t k0) ARMX_INLINE {
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-      store_out4<OUT>(p, i0 + 16 * x + r, j0 + 16 * y + (lane >> 4) * 4, acc[x][y], wide != 0);
+    for (int x = 0; x < kLoads; ++x) stage_one(to, k0, x);
+  };
+  // all of the group's loads have landed and all its reads are done; a group of
+  // one wavefront has only itself to wait for
+  auto sync = [&]() ARMX_INLINE {
+    wait_loads();
+    if constexpr (T::kGroup > 1)
+      __syncthreads();
+    else
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  // operand registers of half a step (64 codes of k): lane l reads row l % 16,
+  // piece 4 half + l / 16
+  const uint32_t r = lane & 15, g = lane >> 4;
+  uint32_t at_a[2], at_b[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t slot = (4 * h + g) ^ swizzle(r);
+    at_a[h] = ((w % WM) * (BM / WM) + r) * kStepK + slot * 16;
+    at_b[h] = (BM + (w / WM) * (BN / WN) + r / 4 * (4 * T::kNT) + r % 4) * kStepK + slot * 16;
+  }
+  u32x4 fa[2][T::kMT], fb[2][T::kNT];
+  constexpr int kReads = T::kMT + T::kNT;
+  // read j of half h, in the order in which its products need them
+  auto fetch = [&](uint32_t from, int h, int j) ARMX_INLINE {
+    if (j < T::kNT)
+      fb[h][j] = lds_read16(from + at_b[h] + j * 4 * kStepK);
+    else
+      fa[h][j - T::kNT] = lds_read16(from + at_a[h] + (j - T::kNT) * 16 * kStepK);
+  };
+  auto fetch_half = [&](uint32_t from, int h) ARMX_INLINE {
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) {
+      fetch(from, h, j);
+      // in this order: the wait at the loop's head is the stricter of the two
+      // orders that reach it
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // codes past k are cut from a's operands
+  auto mask_half = [&](uint32_t k0, int h) ARMX_INLINE {
+    const int keep = int(k) - int(k0 + 64 * h + 16 * g);
+#pragma unroll
+    for (int x = 0; x < T::kMT; ++x) fa[h][x] = keep_codes(fa[h][x], keep);
+  };
+  i32x4 acc[T::kMT][T::kNT];
+#pragma unroll
+  for (int x = 0; x < T::kMT; ++x)
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
+  auto multiply_row = [&](int h, int x) ARMX_INLINE {
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y) acc[x][y] = mfma_i8(fb[h][y], fa[h][x], acc[x][y]);
+  };
+  auto multiply = [&](int h) ARMX_INLINE {
+#pragma unroll
+    for (int x = 0; x < T::kMT; ++x) multiply_row(h, x);
+  };
+  // The products of one half, with the other's operands (h) read from `from`
+  // and, with SEND, the loads of the step at k0 into `to` spread between them.
+  auto multiply_and_fetch = [&](int h, uint32_t from, auto send, uint32_t to, uint32_t k0)
+      ARMX_INLINE {
+    constexpr int kPer = (kLoads + T::kMT - 1) / T::kMT;
+    constexpr int kPerR = (kReads + T::kMT - 1) / T::kMT;
+#pragma unroll
+    for (int i = 0; i < T::kMT; ++i) {
+      if constexpr (send.value) {
+#pragma unroll
+        for (int j = i * kPer; j < (i + 1) * kPer; ++j)
+          if (j < kLoads) stage_one(to, k0, j);
+      }
+#pragma unroll
+      for (int j = i * kPerR; j < (i + 1) * kPerR; ++j)
+        if (j < kReads) fetch(from, h, j);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply_row(1 - h, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // A step but the last (its first half's operands already in registers): the
+  // second half's are read while the first is multiplied; then, after the
+  // barrier that ends all reading of this buffer and finds the other one
+  // filled, the step after next is sent for into it (SEND) and the next step's
+  // first half read under the second half's products.
+  constexpr uint32_t kStride = KS * kStepK;
+  auto step = [&](auto send, uint32_t k0) ARMX_INLINE {
+    multiply_and_fetch(1, base, No{}, 0, 0);
+    sync();
+    const uint32_t other = flip - base;
+    multiply_and_fetch(0, other, send, base, k0 + 2 * kStride);
+    base = other;
+  };
+  if (k > 0) {
+    // every group makes the same number of steps, counted by `left`, so that all
+    // meet at the barriers; one that lies past k loads nothing (the range check)
+    // and is cut to zeros
+    uint32_t k0 = uint32_t(group) * kStepK;
+    uint32_t left = (k + kStride - 1) / kStride;
+    stage(base, k0);
+    sync();
+    if (left > 1) stage(flip - base, k0 + kStride);
+    fetch_half(base, 0);
+    for (; left > 2; --left, k0 += kStride) step(Yes{}, k0);
+    if (left > 1) {
+      step(No{}, k0);
+      k0 += kStride;
+    }
+    fetch_half(base, 1);
+    mask_half(k0, 0);
+    multiply(0);
+    mask_half(k0, 1);
+    multiply(1);
+  }
+  constexpr int kCols = 4 * T::kNT;   // a lane's columns of a row
+  auto columns = [&](int wave) ARMX_INLINE {
+    return Columns<OUT, kCols>(p, j0 + (wave / WM) * (BN / WN) + kCols * g, aligned != 0);
+  };
+  if constexpr (KS == 1) {
+    const auto out = columns(w);
+#pragma unroll
+    for (int x = 0; x < T::kMT; ++x) out.store(i0 + (w % WM) * (BM / WM) + 16 * x + r, acc[x]);
+  } else {
+    // the groups' sums meet in LDS; 16 rows of a wavefront's tile at a time are
+    // added and stored by one wavefront, dealt out over all of them
+    constexpr int kRowUnits = T::kGroup * T::kMT;
+    i32x4* sums = reinterpret_cast<i32x4*>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < T::kMT; ++x)
+#pragma unroll
+      for (int y = 0; y < T::kNT; ++y)
+        sums[(((group * T::kGroup + w) * T::kMT + x) * T::kNT + y) * 64 + lane] = acc[x][y];
+    __syncthreads();
+    for (int u = group * T::kGroup + w; u < kRowUnits; u += T::kWaves) {
+      i32x4 v[T::kNT];
+#pragma unroll
+      for (int y = 0; y < T::kNT; ++y) {
+        v[y] = sums[(u * T::kNT + y) * 64 + lane];
+#pragma unroll
+        for (int q = 1; q < KS; ++q) v[y] += sums[((q * kRowUnits + u) * T::kNT + y) * 64 + lane];
+      }
+      const int uw = u / T::kMT;
+      columns(uw).store(i0 + (uw % WM) * (BM / WM) + 16 * (u % T::kMT) + r, v);
+    }
+  }
 }
 
-template <int OUT>
-hipError_t launch_typed(const MatmulArgs& p, const armx_config* cfg, hipStream_t stream) {
+template <int OUT, int BM, int BN, int WM, int WN, int KS>
+hipError_t launch_tiled(const MatmulArgs& p, const armx_config* cfg, hipStream_t stream) {
   MatmulArgs copy = p;
-  uint64_t tiles_n = (p.n + 63) / 64;
-  const uint64_t blocks = (p.m + 63) / 64 * tiles_n;
-  constexpr uint64_t quad = OUT == ARMX_F32 ? 16 : 8;
-  int wide = p.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % quad == 0;
-  void* args[] = {&copy, &tiles_n, &wide};
-  return launch_kernel(reinterpret_cast<const void*>(&matmul_direct_kernel<OUT>),
-                       dim3(unsigned(blocks)), dim3(256), args, 0, stream,
+  unsigned tiles_m = unsigned((p.m + BM - 1) / BM), tiles_n = unsigned((p.n + BN - 1) / BN);
+  int aligned = aligned_rows(p);
+  void* args[] = {&copy, &tiles_m, &tiles_n, &aligned};
+  return launch_kernel(reinterpret_cast<const void*>(&matmul_tiled_kernel<BM, BN, WM, WN, KS, OUT>),
+                       dim3(tiles_m * tiles_n), dim3(64 * WM * WN * KS), args, 0, stream,
                        cfg ? static_cast<hipEvent_t>(cfg->start_event) : nullptr,
                        cfg ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
+}
+
+// ---- which tile ---------------------------------------------------------------
+//
+// The tile whose estimated time is least.  A compute unit that makes q tiles runs
+// them in rounds of at most `resident` blocks; a round takes `fixed` (its first
+// loads, its epilogue) and, per step of KS x 128 codes, `alone` or, with several
+// blocks on the unit, `each` of them if that is more.  The constants (us) are
+// fitted to times of each tile on MI355X over 176 shapes of 1 to 8192 rows, 128 to
+// 28672 columns and lengths of 128 to 14336; the tile they choose is 1.3% behind
+// the fastest of all twenty measured on average and 15% at worst.  Each of the ten
+// pays where it is chosen (us, it and the best of the others): 256 x 256 at
+// 8192^3 416 (128 x 128: 516); 128 x 128 at 2048 x 4096 x 4096 37.5 (63);
+// its two groups at 1024 x 4096 x 14336 82 (96); 64 x 64 by 2 at 512 x 4096 x 4096
+// 15.8 (20.2), by 4 at 256 x 4096 x 14336 41.7 (47.7); 64 x 32 at 128 x 4096 x 14336
+// 27.2 (34.6); 48 x 32 at 160 x 4096 x 14336 39 (42); 32 x 32 at 64 x 4096 x 4096 6.8
+// (8.0); 16 x 32 at 32 x 4096 x 14336 18.0 (21.4); 16 x 16 at 16 x 4096 x 14336
+// 14.2 (18.0).
+struct TileTime {
+  int bm, bn, ks, resident;
+  float fixed, alone, each;
+};
+constexpr TileTime kTiles[] = {
+    {256, 256, 1, 1, 5.03f, 1.39f, 1.39f}, {128, 128, 1, 2, 2.24f, 0.71f, 0.48f},
+    {128, 128, 2, 1, 3.08f, 1.21f, 1.21f}, {64, 64, 2, 2, 1.76f, 0.61f, 0.43f},
+    {64, 64, 4, 1, 1.97f, 1.11f, 1.11f},   {64, 32, 6, 1, 1.86f, 0.86f, 0.86f},
+    {48, 32, 8, 1, 1.80f, 0.93f, 0.93f},   {32, 32, 8, 1, 1.62f, 0.81f, 0.81f},
+    {16, 32, 8, 1, 1.47f, 0.67f, 0.67f},   {16, 16, 16, 1, 1.35f, 1.02f, 1.02f},
+};
+
+inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+inline uint64_t tile_count(const TileTime& t, const MatmulArgs& p) {
+  return ceil_div(p.m, uint64_t(t.bm)) * ceil_div(p.n, uint64_t(t.bn));
+}
+
+double tile_time(const TileTime& t, const MatmulArgs& p, int cu_count) {
+  const uint64_t per_cu = ceil_div(tile_count(t, p), uint64_t(cu_count));
+  const double steps = double(ceil_div(p.k, uint64_t(t.ks) * kStepK));
+  auto round = [&](uint64_t blocks) {
+    const double together = double(blocks) * t.each;
+    return blocks == 0 ? 0.0 : t.fixed + steps * (together > t.alone ? together : t.alone);
+  };
+  return double(per_cu / t.resident) * round(t.resident) + round(per_cu % t.resident);
+}
+
+int choose_tile(const MatmulArgs& p, int cu_count) {
+  int best = -1;
+  for (int i = 0; i < int(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    if (tile_count(kTiles[i], p) > 0x7FFFFFFFu / 1024) continue;  // the grid's limit
+    if (best < 0 || tile_time(kTiles[i], p, cu_count) < tile_time(kTiles[best], p, cu_count))
+      best = i;
+  }
+  return best;
+}
+
+template <int OUT>
+hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cfg,
+                        hipStream_t stream) {
+  switch (choose_tile(p, cu_count)) {
+    case 0: return launch_tiled<OUT, 256, 256, 2, 4, 1>(p, cfg, stream);
+    case 1: return launch_tiled<OUT, 128, 128, 2, 4, 1>(p, cfg, stream);
+    case 2: return launch_tiled<OUT, 128, 128, 2, 2, 2>(p, cfg, stream);
+    case 3: return launch_tiled<OUT, 64, 64, 2, 2, 2>(p, cfg, stream);
+    case 4: return launch_tiled<OUT, 64, 64, 2, 2, 4>(p, cfg, stream);
+    case 5: return launch_tiled<OUT, 64, 32, 1, 1, 6>(p, cfg, stream);
+    case 6: return launch_tiled<OUT, 48, 32, 1, 1, 8>(p, cfg, stream);
+    case 7: return launch_tiled<OUT, 32, 32, 1, 1, 8>(p, cfg, stream);
+    case 8: return launch_tiled<OUT, 16, 32, 1, 1, 8>(p, cfg, stream);
+    case 9: return launch_tiled<OUT, 16, 16, 1, 1, 16>(p, cfg, stream);
+    default: return hipErrorInvalidValue;  // no grid holds that many tiles
+  }
 }
 
 }  // namespace
 
 hipError_t launch_matmul_int8(const MatmulArgs& args, int cu_count, const armx_config* cfg,
                               hipStream_t stream) {
-  (void)cu_count;
   switch (args.out_type) {
-    case ARMX_F16: return launch_typed<ARMX_F16>(args, cfg, stream);
-    case ARMX_BF16: return launch_typed<ARMX_BF16>(args, cfg, stream);
-    default: return launch_typed<ARMX_F32>(args, cfg, stream);
+    case ARMX_F16: return launch_typed<ARMX_F16>(args, cu_count, cfg, stream);
+    case ARMX_BF16: return launch_typed<ARMX_BF16>(args, cu_count, cfg, stream);
+    default: return launch_typed<ARMX_F32>(args, cu_count, cfg, stream);
   }
 }
 
