@@ -470,24 +470,48 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
   }
-  int turn = 0;
-  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows;
-       base += uint64_t(gridDim.x) * kRows, turn ^= 1) {
+  // One row group's values; with kAhead the next group's are on their way while
+  // this one's are combined (8192 x 4096 56.6 -> 54.3 us; at 512 threads x 4, where
+  // the registers no longer hold both, 62 -> 71).
+  struct Rows {
+    u32x4 dy[C], h[C], ds[C];
+    float inv;
+  };
+  constexpr bool kAhead = TPR * C <= 1024;
+  auto load = [&](uint64_t base) __attribute__((always_inline)) {
+    Rows v;
     const uint64_t row = base + threadIdx.x / TPR;
     const bool live = row < k.rows;
-    u32x4 dy[C], h[C], ds[C];
-    float dot = 0.0f;
-    const float inv = live ? k.inv_rms[row] : 0.0f;
+    v.inv = live ? k.inv_rms[row] : 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t c = j * TPR + t;
-      dy[j] = h[j] = ds[j] = u32x4{0, 0, 0, 0};
+      v.dy[j] = v.h[j] = v.ds[j] = u32x4{0, 0, 0, 0};
       if (live && c < chunks) {
-        dy[j] = load_chunk8(k.dy + row * k.ldy, c, cols);
-        h[j] = load_chunk8(k.h + row * k.ldh, c, cols);
-        if constexpr (DSUM) ds[j] = load_chunk8(k.dsum + row * k.ldd, c, cols);
+        v.dy[j] = load_chunk8(k.dy + row * k.ldy, c, cols);
+        v.h[j] = load_chunk8(k.h + row * k.ldh, c, cols);
+        if constexpr (DSUM) v.ds[j] = load_chunk8(k.dsum + row * k.ldd, c, cols);
       }
     }
+    return v;
+  };
+  int turn = 0;
+  const uint64_t stride = uint64_t(gridDim.x) * kRows;
+  Rows ahead;
+  if constexpr (kAhead) ahead = load(uint64_t(blockIdx.x) * kRows);
+  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows; base += stride, turn ^= 1) {
+    const uint64_t row = base + threadIdx.x / TPR;
+    const bool live = row < k.rows;
+    Rows now;
+    if constexpr (kAhead) {
+      now = ahead;
+      if (base + stride < k.rows) ahead = load(base + stride);
+    } else {
+      now = load(base);
+    }
+    const u32x4 (&dy)[C] = now.dy, (&h)[C] = now.h, (&ds)[C] = now.ds;
+    const float inv = now.inv;
+    float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       float fy[8], fh[8], fw[8];
@@ -537,9 +561,15 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t c = j * TPR + t;
+      float* d = dst + uint64_t(blockIdx.x) * pitch + c * 8;
+      if (c * 8 + 8 <= cols) {
+        reinterpret_cast<floatx4*>(d)[0] = floatx4{acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+        reinterpret_cast<floatx4*>(d)[1] = floatx4{acc[j][4], acc[j][5], acc[j][6], acc[j][7]};
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c * 8 + i < cols) dst[uint64_t(blockIdx.x) * pitch + c * 8 + i] = acc[j][i];
+        for (int i = 0; i < 8; ++i)
+          if (c * 8 + i < cols) d[i] = acc[j][i];
+      }
     }
   }
 }
@@ -590,25 +620,39 @@ __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardAr
   }
 }
 
-// dweight[c] = the sum of the blocks' partial sums, in block order within each
-// of 8 interleaved parts, then the parts in order.
-constexpr int kJoinCols = 32, kJoinParts = 8;
-__global__ __launch_bounds__(kJoinCols* kJoinParts) void norm_join_kernel(const float* partials,
-                                                                          uint64_t blocks,
-                                                                          uint64_t pitch,
-                                                                          uint64_t cols,
-                                                                          float* dweight) {
-  __shared__ float part[kJoinParts][kJoinCols];
-  const uint32_t tc = threadIdx.x % kJoinCols, tp = threadIdx.x / kJoinCols;
-  const uint64_t c = uint64_t(blockIdx.x) * kJoinCols + tc;
-  float v = 0.0f;
-  if (c < cols)
-    for (uint64_t b = tp; b < blocks; b += kJoinParts) v += partials[b * pitch + c];
+// dweight[c] = the sum of the blocks' partial sums: 4 consecutive columns per
+// thread, kJoinParts threads of a block sharing the partial sums of its columns
+// (part t takes t, t + kJoinParts, ..., eight loads in flight), whose sums are
+// then added in order.
+constexpr int kJoinCols = 32, kJoinParts = 32;
+__global__ __launch_bounds__(kJoinCols / 4 * kJoinParts) void norm_join_kernel(
+    const float* partials, uint64_t blocks, uint64_t pitch, uint64_t cols, float* dweight) {
+  constexpr int kQuads = kJoinCols / 4;
+  __shared__ floatx4 part[kJoinParts][kQuads];
+  const uint32_t tc = threadIdx.x % kQuads, tp = threadIdx.x / kQuads;
+  // the pitch is a multiple of 64, so a quad past the columns is still inside it
+  const uint64_t c = uint64_t(blockIdx.x) * kJoinCols + tc * 4;
+  const floatx4* src = reinterpret_cast<const floatx4*>(partials + c);
+  floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint64_t b = tp; b < blocks; b += 8 * kJoinParts) {
+    floatx4 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t bi = b + uint64_t(i) * kJoinParts;
+      t[i] = src[(bi < blocks ? bi : b) * (pitch / 4)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (b + uint64_t(i) * kJoinParts < blocks) v += t[i];
+  }
   part[tp][tc] = v;
   __syncthreads();
-  if (tp == 0 && c < cols) {
-    for (int p = 1; p < kJoinParts; ++p) v += part[p][tc];
-    dweight[c] = v;
+  if (tp == 0) {
+    const uint64_t last = blocks < kJoinParts ? blocks : kJoinParts;
+    for (uint64_t t = 1; t < last; ++t) v += part[t][tc];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < cols) dweight[c + i] = v[i];
   }
 }
 
@@ -644,7 +688,8 @@ hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPl
   float* dweight = a.dweight;
   void* join_args[] = {&partials, &blocks, &pitch, &cols, &dweight};
   return launch_rows_kernel(reinterpret_cast<const void*>(&norm_join_kernel),
-                            (cols + kJoinCols - 1) / kJoinCols, kJoinCols * kJoinParts, join_args,
+                            (cols + kJoinCols - 1) / kJoinCols, kJoinCols / 4 * kJoinParts,
+                            join_args,
                             cfg, stream, false, true);
 }
 
@@ -657,7 +702,11 @@ NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) 
   if (rows == 0 || cols == 0) return p;
   const uint64_t per = uint64_t(p.block / p.shape.threads);
   const uint64_t groups = (rows + per - 1) / per;
-  const uint64_t most = uint64_t(cu_count) * (1024 / uint64_t(p.block));
+  // Every block's dweight sums are written and read again, so fewer blocks move
+  // less, and too few leave loads unsent.  Measured on MI355X at 1, 2 and 4 blocks
+  // of 256 threads per compute unit (us): 8192 x 4096 55.4, 54.3, 61.2; 4096 x 8192
+  // 54.9, 58.9, 69.0; 32768 x 128 11.6, 10.7, 11.7.
+  const uint64_t most = uint64_t(cu_count) * (cols <= 4096 ? 2 : 1);
   p.blocks = groups < most ? groups : most;
   p.pitch = (cols + 63) / 64 * 64;
   if (p.blocks > 1) p.ws_bytes = size_t(p.blocks * p.pitch * sizeof(float));

@@ -67,68 +67,103 @@ for _f in (lib.rms_norm_rows, lib.rms_norm_rows_int8, lib.quantize_rows_int8,
     _f.restype = ctypes.c_int
 
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_HALVES = (torch.float16, torch.bfloat16)
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+# A call's kernel may take no longer than its Python does, so the checks below
+# read each tensor's properties once, compare dtypes by identity and devices by
+# index, and check nothing of the matrices made here.
 
 
-def _first(x, name: str, what: str, dtypes) -> None:
+def _first(x, name: str, what: str, dtypes):
+    """Shape, dtype and device index of the operand the others must match."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: {what} must be a torch.Tensor")
-    if x.dtype not in dtypes:
+    dtype = x.dtype
+    if dtype not in dtypes:
         raise TypeError(f"{name}: {what} must be {' or '.join(str(d) for d in dtypes)}, "
-                        f"got {x.dtype}")
+                        f"got {dtype}")
     if not x.is_cuda:
         raise ValueError(f"{name}: {what} must be on a GPU (HIP) device")
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected a 2-D {what}, got {x.dim()}-D")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D {what}, got {len(shape)}-D")
+    return shape, dtype, x.get_device()
 
 
-def _matrix(t, name: str, what: str, shape, dtype, device) -> tuple[int | None, int]:
+def _matrix(t, name: str, what: str, shape, dtype, dev: int) -> tuple[int | None, int]:
     """Pointer and row pitch of a matrix that must have this shape and type."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape \
-            or t.device != device:
-        raise ValueError(f"{name}: {what} must be a {tuple(shape)} {dtype} tensor on {device}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+            or t.get_device() != dev:
+        raise ValueError(f"{name}: {what} must be a {tuple(shape)} {dtype} tensor on cuda:{dev}")
     rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: rows of {what} must be contiguous (stride(1) == 1)")
-    return t.data_ptr() or None, t.stride(0) if rows > 1 else cols
+    return t.data_ptr() or None, pitch if rows > 1 else cols
 
 
-def _vector(t, name: str, what: str, n: int, dtype, device) -> int | None:
+def _vector(t, name: str, what: str, n: int, dtype, dev: int) -> int | None:
     """Pointer of n contiguous values."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != n \
-            or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: {what} must be {n} contiguous {dtype} values on {device}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != n \
+            or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be {n} contiguous {dtype} values on cuda:{dev}")
     return t.data_ptr() or None
 
 
-def _rows_like(rows: int, cols: int, multiple: int, dtype, device) -> torch.Tensor:
-    """An uninitialised matrix whose rows start at multiples of `multiple` values."""
+def _rows_like(x, rows: int, cols: int, multiple: int, dtype) -> tuple:
+    """An uninitialised matrix on x's device whose rows start at multiples of
+    `multiple` values; its pointer and pitch."""
     pitch = -(-cols // multiple) * multiple
-    m = torch.empty((rows, pitch), dtype=dtype, device=device)
-    return m if pitch == cols else m[:, :cols]
+    m = x.new_empty((rows, pitch), dtype=dtype)
+    return m if pitch == cols else m[:, :cols], m.data_ptr() or None, pitch
 
 
-def _events(start_event, stop_event):
-    if start_event is None and stop_event is None:
-        return None
-    return ctypes.byref(_config(start_event=start_event, stop_event=stop_event))
+def _call(fn, name: str, dev: int, args: tuple, start_event, stop_event) -> None:
+    """fn(*args, cfg, stream) on the current stream of device `dev`."""
+    cfg = None
+    if start_event is not None or stop_event is not None:
+        cfg = ctypes.byref(_config(start_event=start_event, stop_event=stop_event))
+    if _current_device() == dev:
+        st = fn(*args, cfg, _stream_of(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, cfg, _stream_of(dev))
+    if st:
+        _check(st, name)
 
 
 def _norm_inputs(x, weight, residual, sum_out, name):
-    _first(x, name, "x", (torch.float16, torch.bfloat16))
-    shape, dtype, dev = x.shape, x.dtype, x.device
+    shape, dtype, dev = _first(x, name, "x", _HALVES)
     xp, ldx = _matrix(x, name, "x", shape, dtype, dev)
     wp = _vector(weight, name, "weight", shape[1], dtype, dev)
     if residual is None:
         if sum_out is not None:
             raise ValueError(f"{name}: sum_out goes with a residual")
-        return xp, ldx, wp, None, 0, None, None, 0
+        return shape, dtype, dev, xp, ldx, wp, None, 0, None, None, 0
     rp, ldr = _matrix(residual, name, "residual", shape, dtype, dev)
     if sum_out is None:
-        sum_out = _rows_like(*shape, 8, dtype, dev)
-    sp, lds = _matrix(sum_out, name, "sum_out", shape, dtype, dev)
-    return xp, ldx, wp, rp, ldr, sum_out, sp, lds
+        sum_out, sp, lds = _rows_like(x, *shape, 8, dtype)
+    else:
+        sp, lds = _matrix(sum_out, name, "sum_out", shape, dtype, dev)
+    return shape, dtype, dev, xp, ldx, wp, rp, ldr, sum_out, sp, lds
+
+
+def _codes_out(x, shape, out, scales, name, dev):
+    """Codes and scales with their pointers and the codes' pitch, made if not given."""
+    rows, cols = shape
+    if out is None:
+        out, op, ldo = _rows_like(x, rows, cols, 16, torch.int8)
+    else:
+        op, ldo = _matrix(out, name, "out", shape, torch.int8, dev)
+    if scales is None:
+        scales = x.new_empty(rows, dtype=torch.float32)
+        cp = scales.data_ptr() or None
+    else:
+        cp = _vector(scales, name, "scales", rows, torch.float32, dev)
+    return out, op, ldo, scales, cp
 
 
 def rms_norm_rows(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None,
@@ -142,18 +177,19 @@ def rms_norm_rows(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tens
     ``rms_norm_rows_backward`` takes.  ``out`` and ``sum_out`` may be ``x`` or
     ``residual`` themselves."""
     name = "rms_norm_rows"
-    xp, ldx, wp, rp, ldr, sum_out, sp, lds = _norm_inputs(x, weight, residual, sum_out, name)
-    rows, cols = x.shape
-    dev = x.device
+    shape, dtype, dev, xp, ldx, wp, rp, ldr, sum_out, sp, lds = _norm_inputs(
+        x, weight, residual, sum_out, name)
+    rows, cols = shape
     if out is None:
-        out = _rows_like(rows, cols, 8, x.dtype, dev)
-    op, ldo = _matrix(out, name, "out", x.shape, x.dtype, dev)
-    inv = torch.empty(rows, dtype=torch.float32, device=dev) if keep_inv_rms else None
-    with _on_device(dev):
-        st = lib.rms_norm_rows(xp, ldx, rp, ldr, wp, _TYPES[x.dtype], rows, cols, eps, op, ldo,
-                               sp, lds, inv.data_ptr() or None if keep_inv_rms else None,
-                               _events(start_event, stop_event), _stream_of(dev.index))
-    _check(st, name)
+        out, op, ldo = _rows_like(x, rows, cols, 8, dtype)
+    else:
+        op, ldo = _matrix(out, name, "out", shape, dtype, dev)
+    inv = ip = None
+    if keep_inv_rms:
+        inv = x.new_empty(rows, dtype=torch.float32)
+        ip = inv.data_ptr() or None
+    _call(lib.rms_norm_rows, name, dev, (xp, ldx, rp, ldr, wp, _TYPES[dtype], rows, cols, eps, op,
+                                         ldo, sp, lds, ip), start_event, stop_event)
     return RmsNorm(out, sum_out, inv)
 
 
@@ -166,20 +202,12 @@ def rms_norm_rows_int8(x: torch.Tensor, weight: torch.Tensor, *,
     (``codes * scales[:, None]`` stands for the norm), as ``matmul_int8`` takes
     them.  ``out`` receives the codes."""
     name = "rms_norm_rows_int8"
-    xp, ldx, wp, rp, ldr, sum_out, sp, lds = _norm_inputs(x, weight, residual, sum_out, name)
-    rows, cols = x.shape
-    dev = x.device
-    if out is None:
-        out = _rows_like(rows, cols, 16, torch.int8, dev)
-    op, ldo = _matrix(out, name, "out", x.shape, torch.int8, dev)
-    if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    cp = _vector(scales, name, "scales", rows, torch.float32, dev)
-    with _on_device(dev):
-        st = lib.rms_norm_rows_int8(xp, ldx, rp, ldr, wp, _TYPES[x.dtype], rows, cols, eps, op,
-                                    ldo, cp, sp, lds, _events(start_event, stop_event),
-                                    _stream_of(dev.index))
-    _check(st, name)
+    shape, dtype, dev, xp, ldx, wp, rp, ldr, sum_out, sp, lds = _norm_inputs(
+        x, weight, residual, sum_out, name)
+    out, op, ldo, scales, cp = _codes_out(x, shape, out, scales, name, dev)
+    _call(lib.rms_norm_rows_int8, name, dev,
+          (xp, ldx, rp, ldr, wp, _TYPES[dtype], *shape, eps, op, ldo, cp, sp, lds), start_event,
+          stop_event)
     return RmsNormInt8(out, scales, sum_out)
 
 
@@ -191,20 +219,11 @@ def quantize_rows_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
     max|x| / 127.  A linear layer's weight (one output channel per row) becomes
     ``matmul_int8``'s second operand."""
     name = "quantize_rows_int8"
-    _first(x, name, "x", (torch.float16, torch.bfloat16))
-    rows, cols = x.shape
-    dev = x.device
-    xp, ldx = _matrix(x, name, "x", x.shape, x.dtype, dev)
-    if out is None:
-        out = _rows_like(rows, cols, 16, torch.int8, dev)
-    op, ldo = _matrix(out, name, "out", x.shape, torch.int8, dev)
-    if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    cp = _vector(scales, name, "scales", rows, torch.float32, dev)
-    with _on_device(dev):
-        st = lib.quantize_rows_int8(xp, ldx, _TYPES[x.dtype], rows, cols, op, ldo, cp,
-                                    _events(start_event, stop_event), _stream_of(dev.index))
-    _check(st, name)
+    shape, dtype, dev = _first(x, name, "x", _HALVES)
+    xp, ldx = _matrix(x, name, "x", shape, dtype, dev)
+    out, op, ldo, scales, cp = _codes_out(x, shape, out, scales, name, dev)
+    _call(lib.quantize_rows_int8, name, dev, (xp, ldx, _TYPES[dtype], *shape, op, ldo, cp),
+          start_event, stop_event)
     return RowCodes(out, scales)
 
 
@@ -221,8 +240,7 @@ def rms_norm_rows_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     dweight (float32).  ``out`` receives dx and may be ``dy`` or ``dsum``.
     Without ``workspace`` one is taken from the allocator for this call."""
     name = "rms_norm_rows_backward"
-    _first(dy, name, "dy", (torch.float16, torch.bfloat16))
-    shape, dtype, dev = dy.shape, dy.dtype, dy.device
+    shape, dtype, dev = _first(dy, name, "dy", _HALVES)
     rows, cols = shape
     yp, ldy = _matrix(dy, name, "dy", shape, dtype, dev)
     hp, ldh = _matrix(h, name, "h", shape, dtype, dev)
@@ -230,32 +248,37 @@ def rms_norm_rows_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     ip = _vector(inv_rms, name, "inv_rms", rows, torch.float32, dev)
     dp, ldd = (None, 0) if dsum is None else _matrix(dsum, name, "dsum", shape, dtype, dev)
     if out is None:
-        out = _rows_like(rows, cols, 8, dtype, dev)
-    op, ldo = _matrix(out, name, "out", shape, dtype, dev)
+        out, op, ldo = _rows_like(dy, rows, cols, 8, dtype)
+    else:
+        op, ldo = _matrix(out, name, "out", shape, dtype, dev)
     if dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
-    gp = _vector(dweight, name, "dweight", cols, torch.float32, dev)
-    with _on_device(dev):
-        if workspace is None:
+        dweight = dy.new_empty(cols, dtype=torch.float32)
+        gp = dweight.data_ptr() or None
+    else:
+        gp = _vector(dweight, name, "dweight", cols, torch.float32, dev)
+    if workspace is None:
+        with _on_device(dy.device):
             need = lib.armx_workspace_bytes(OP_RMS_BACKWARD, rows, cols, None)
-            # from the allocator, which knows streams and graph captures: it
-            # needs no zeros, so nothing is gained by keeping one
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"{name}: workspace must be a contiguous tensor on {dev}")
-        ws, ws_bytes = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        st = lib.rms_norm_rows_backward(yp, ldy, hp, ldh, wp, ip, dp, ldd, _TYPES[dtype], rows,
-                                        cols, op, ldo, gp, ws, ws_bytes,
-                                        _events(start_event, stop_event), _stream_of(dev.index))
-    _check(st, name)
+        # from the allocator, which knows streams and graph captures: it needs
+        # no zeros, so nothing is gained by keeping one
+        workspace = dy.new_empty(need, dtype=torch.uint8) if need else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be a contiguous tensor on cuda:{dev}")
+    ws, ws_bytes = (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call(lib.rms_norm_rows_backward, name, dev,
+          (yp, ldy, hp, ldh, wp, ip, dp, ldd, _TYPES[dtype], rows, cols, op, ldo, gp, ws,
+           ws_bytes), start_event, stop_event)
     return RmsNormGrads(out, dweight)
 
 
-def _code_rows(t, name: str, what: str, rows: int, k: int, dev) -> tuple[int | None, int]:
+def _code_rows(t, name: str, what: str, shape, k: int, dev: int) -> tuple[int | None, int]:
     """Pointer and pitch of a matrix of codes whose rows can be read in pieces
     of 16 to their end."""
-    p, ld = _matrix(t, name, what, (rows, k), torch.int8, dev)
+    rows = shape[0]
+    if shape[1] != k:
+        raise ValueError(f"{name}: {what} must have rows of {k} codes, as a has")
+    p, ld = _matrix(t, name, what, shape, torch.int8, dev)
     if k % 16 and rows and (ld % 16 == 0 or rows == 1):   # else the call reports the pitch
         end = t.storage_offset() + (rows - 1) * ld + -(-k // 16) * 16
         if end > t.untyped_storage().nbytes():
@@ -274,28 +297,25 @@ def matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     ``bias`` has it too).  The sum over k (at most 131071) is exact, so a
     result depends on its row and column only."""
     name = "matmul_int8"
-    _first(a, name, "a", (torch.int8,))
-    _first(b, name, "b", (torch.int8,))
-    dev = a.device
-    m, k = a.shape
-    n = b.shape[0]
-    ap, lda = _code_rows(a, name, "a", m, k, dev)
-    bp, ldb = _code_rows(b, name, "b", n, k, dev)
+    shape, _, dev = _first(a, name, "a", (torch.int8,))
+    m, k = shape
+    ap, lda = _code_rows(a, name, "a", shape, k, dev)
+    shape, _, _ = _first(b, name, "b", (torch.int8,))
+    n = shape[0]
+    bp, ldb = _code_rows(b, name, "b", shape, k, dev)
     asp = _vector(a_scales, name, "a_scales", m, torch.float32, dev)
     bsp = _vector(b_scales, name, "b_scales", n, torch.float32, dev)
-    if out is None:
-        if dtype not in _TYPES:
-            raise TypeError(f"{name}: dtype must be float16, bfloat16 or float32, got {dtype}")
-        out = torch.empty((m, n), dtype=dtype, device=dev)
-        op, ldo = out.data_ptr() or None, n
-    else:
+    if out is not None:
         dtype = out.dtype if isinstance(out, torch.Tensor) else None
-        if dtype not in _TYPES:
-            raise TypeError(f"{name}: out must be a float16, bfloat16 or float32 tensor")
+    type_ = _TYPES.get(dtype)
+    if type_ is None:
+        raise TypeError(f"{name}: the result is float16, bfloat16 or float32, not {dtype}")
+    if out is None:
+        out, ldo = a.new_empty((m, n), dtype=dtype), n
+        op = out.data_ptr() or None
+    else:
         op, ldo = _matrix(out, name, "out", (m, n), dtype, dev)
     biasp = None if bias is None else _vector(bias, name, "bias", n, dtype, dev)
-    with _on_device(dev):
-        st = lib.matmul_int8(ap, lda, asp, bp, ldb, bsp, biasp, m, n, k, op, ldo, _TYPES[dtype],
-                             _events(start_event, stop_event), _stream_of(dev.index))
-    _check(st, name)
+    _call(lib.matmul_int8, name, dev, (ap, lda, asp, bp, ldb, bsp, biasp, m, n, k, op, ldo, type_),
+          start_event, stop_event)
     return out
