@@ -21,10 +21,10 @@ RowShape row_shape(uint64_t cols) {
   if (n <= 16) return {16, 1};
   if (n <= 32) return {32, 1};
   if (n <= 64) return {64, 1};
-  if (n <= 128) return {64, 2};
+  if (n <= 128) return {128, 1};
   if (n <= 256) return {256, 1};
-  if (n <= 512) return {256, 2};
-  if (n <= 1024) return {256, 4};
+  if (n <= 512) return {512, 1};
+  if (n <= 1024) return {512, 2};
   if (n <= 2048) return {512, 4};
   if (n <= 4096) return {1024, 4};
   return {1024, 0};
@@ -79,10 +79,15 @@ __device__ __forceinline__ u32x4 load_chunk8(const uint16_t* row, uint32_t c, ui
   return load8_masked(row, uint64_t(c) * 8, cols, 0u);
 }
 
+// STREAM: past the caches (kStreamValues).
+template <bool STREAM>
 __device__ __forceinline__ void store_chunk8(uint16_t* row, uint32_t c, uint32_t cols, u32x4 v) {
   const uint64_t e = uint64_t(c) * 8;
   if (e + 8 <= cols) {
-    *reinterpret_cast<u32x4*>(row + e) = v;
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row + e));
+    else
+      *reinterpret_cast<u32x4*>(row + e) = v;
     return;
   }
 #pragma unroll
@@ -90,15 +95,46 @@ __device__ __forceinline__ void store_chunk8(uint16_t* row, uint32_t c, uint32_t
     if (e + i < cols) row[e + i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
 }
 
+template <bool STREAM>
 __device__ __forceinline__ void store_codes8(int8_t* row, uint32_t c, uint32_t cols, u32x2 v) {
   const uint64_t e = uint64_t(c) * 8;
   if (e + 8 <= cols) {
-    *reinterpret_cast<u32x2*>(row + e) = v;
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x2*>(row + e));
+    else
+      *reinterpret_cast<u32x2*>(row + e) = v;
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (e + i < cols) row[e + i] = int8_t(v[i / 4] >> (8 * (i % 4)));
+}
+
+// A wavefront's row as a range-checked buffer of the 32-bit words that hold its
+// values: a load of a chunk past them returns zeros with no memory access, so the
+// loads of a row's chunks stand in no branch and are all in flight together (a
+// branch around a load makes the compiler wait where its paths join: 37 rows of
+// 5001 values, norm to codes, 6.8 -> XX us).  With an odd count the last word
+// holds one value past the row; trim() clears it.
+constexpr int kRawBuffer = 0x00020000;
+struct RowWords {
+  __amdgpu_buffer_rsrc_t rs;
+  // `row` must be the same in all lanes of the wavefront; cols 0: nothing is read
+  __device__ __forceinline__ RowWords(const uint16_t* row, uint32_t cols)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(row), 0,
+                                             int((cols + 1) / 2 * 4), kRawBuffer)) {}
+  __device__ __forceinline__ u32x4 load(uint32_t c) const {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, c * 16, 0, 0));
+  }
+};
+
+__device__ __forceinline__ u32x4 trim(u32x4 v, uint32_t c, uint32_t cols) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t e = c * 8 + 2 * i;   // the word's first value
+    if (e + 1 == cols) v[i] &= 0xFFFFu;
+  }
+  return v;
 }
 
 // ---- combines across the threads of a row ------------------------------------------
@@ -169,48 +205,70 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 
 // What a row's codes are made with, from its largest |p|.
 struct CodeScale {
-  float up;      // exact power of two that keeps 127 / top finite and p normal
-  float factor;  // 127 / (top * up); 0 for a row of zeros or not finite
-  float top;     // top * up
+  float up;       // exact power of two that keeps the quotients finite and p normal
+  float top;      // largest |p| * up
+  float inverse;  // 1 / top, and
+  float factor;   // 127 / top; 0 for a row of zeros or one that is not finite
   bool finite;
   __device__ __forceinline__ explicit CodeScale(uint32_t top_bits) {
     const float t = __builtin_bit_cast(float, top_bits);
     finite = top_bits < kInfBits;
-    up = t < 0x1p-64f ? 0x1p60f : 1.0f;
+    up = t < 0x1p-64f ? 0x1p60f : t > 0x1p64f ? 0x1p-60f : 1.0f;
     top = t * up;
-    factor = finite && t > 0.0f ? 127.0f / top : 0.0f;
+    const bool some = finite && t > 0.0f;
+    inverse = some ? 1.0f / top : 0.0f;
+    factor = some ? 127.0f / top : 0.0f;
   }
 };
 
-// Codes of 8 products: round half to even of 127 p / top, of the exact
-// quotient.  t = p * factor is off by under 127 * 2^-23 < 2^-16 (the quotient
-// and the product round by 2^-24 each), so it rounds as the exact quotient
-// does unless it is within 2^-14 of a half; there 254 |p| is compared with the
-// odd multiple of top, both exact in binary64 (24 + 8 bits).  Adding 1.5 2^23
-// rounds t to a whole number whose code is the sum's low byte.
+// Codes of 8 products: round half to even of 127 p / top, of the exact quotient
+// v.  t = p * factor is off by less than 2^-23 |v| (the quotient and the product
+// round by 2^-24 each); adding 1.5 2^23 rounds it to a whole number whose code is
+// the sum's low byte.
+//
+// NARROW (p of at most 11 bits, a value of a 16-bit type): a v that is no half lies
+// at least 2^-9 |v| / 127 from one, since 2 * 127 p and every odd multiple of top
+// are whole multiples of the smaller's last bit; only true halves, which are common
+// (one value in some tens where top has few bits), need care.  One correction,
+// t + (127 p - t top) / top with the difference exact, gives them exactly.
+//
+// Otherwise t rounds as v does unless it is within 2^-14 of a half.  There 254 |p|
+// is compared with the odd multiple m of top: hi + lo = m top and e = 254 |p| - hi
+// are exact (fma; the difference loses its first 13 bits), so e against lo decides.
+template <bool NARROW>
 __device__ __forceinline__ u32x2 codes8(const float (&p)[8], const CodeScale& cs) {
   constexpr float kMagic = 12582912.0f;
   uint32_t q[8];
-  bool near = false;
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t[i] = (p[i] * cs.up) * cs.factor;
-    const float r = t[i] + kMagic;
-    q[i] = __builtin_bit_cast(uint32_t, r);
-    near |= __builtin_fabsf(t[i] - (r - kMagic)) > 0.5f - 0x1p-14f;
-  }
-  if (__builtin_expect(near, 0)) {
+  if constexpr (NARROW) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = __builtin_fabsf(t[i]);
-      const float k = __builtin_floorf(a);
-      if (__builtin_fabsf(a - k - 0.5f) <= 0x1p-14f) {
-        const double lhs = 254.0 * double(__builtin_fabsf(p[i] * cs.up));
-        const double border = double(2.0f * k + 1.0f) * double(cs.top);
-        int c = int(k);
-        if (lhs > border || (lhs == border && (c & 1))) ++c;
-        q[i] = uint32_t(t[i] < 0.0f ? -c : c);
+      const float s = p[i] * cs.up, n = 127.0f * s;
+      float t = s * cs.factor;
+      t = __builtin_fmaf(__builtin_fmaf(-t, cs.top, n), cs.inverse, t);
+      q[i] = __builtin_bit_cast(uint32_t, t + kMagic);
+    }
+  } else {
+    bool near = false;
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t[i] = (p[i] * cs.up) * cs.factor;
+      const float r = t[i] + kMagic;
+      q[i] = __builtin_bit_cast(uint32_t, r);
+      near |= __builtin_fabsf(t[i] - (r - kMagic)) > 0.5f - 0x1p-14f;
+    }
+    if (__builtin_expect(near, 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = __builtin_fabsf(t[i]), k = __builtin_floorf(a);
+        const float m = 2.0f * k + 1.0f, hi = m * cs.top;
+        const float lo = __builtin_fmaf(m, cs.top, -hi);
+        const float e = __builtin_fmaf(254.0f, __builtin_fabsf(p[i] * cs.up), -hi);
+        if (__builtin_fabsf(a - k - 0.5f) <= 0x1p-14f) {
+          int c = int(k);
+          if (e > lo || (e == lo && (c & 1))) ++c;
+          q[i] = uint32_t(t[i] < 0.0f ? -c : c);
+        }
       }
     }
   }
@@ -239,21 +297,61 @@ constexpr int kOut16 = 0;     // the norm in 16 bits
 constexpr int kOutCodes = 1;  // the norm in codes
 constexpr int kOutQuant = 2;  // the input in codes
 
-// h = x + residual for chunk c of a row, as stored (one rounding)
+// h = x + residual, as stored (one rounding)
+template <int TYPE>
+__device__ __forceinline__ u32x4 sum8(u32x4 x, u32x4 r) {
+  float a[8], b[8];
+  widen8<TYPE>(x, a);
+  widen8<TYPE>(r, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] += b[i];
+  return narrow8<TYPE>(a);
+}
+
 template <int TYPE, bool RES>
 __device__ __forceinline__ u32x4 load_sum(const uint16_t* xr, const uint16_t* rr, uint32_t c,
                                           uint32_t cols) {
   const u32x4 x = load_chunk8(xr, c, cols);
-  if constexpr (!RES) {
-    return x;
-  } else {
-    const u32x4 r = load_chunk8(rr, c, cols);
-    float a[8], b[8];
-    widen8<TYPE>(x, a);
-    widen8<TYPE>(r, b);
+  if constexpr (!RES) return x;
+  return sum8<TYPE>(x, load_chunk8(rr, c, cols));
+}
+
+// Chunks t, t + TPR, ... of a row that TPR threads share: p is the first row of
+// the block's, ld its pitch, `live` whether this thread's row exists.
+template <int TPR, int C>
+__device__ __forceinline__ void load_row(const uint16_t* p, uint64_t ld, bool live, uint32_t t,
+                                         uint32_t cols, u32x4 (&v)[C]) {
+  if constexpr (TPR >= 64) {
+    const uint64_t r = uint64_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x / TPR)));
+    const uint32_t count = __builtin_amdgcn_readfirstlane(live ? int(cols) : 0);
+    const RowWords row(p + (count ? r * ld : 0), count);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] += b[i];
-    return narrow8<TYPE>(a);
+    for (int j = 0; j < C; ++j) v[j] = row.load(j * TPR + t);
+    if (cols & 1) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = trim(v[j], j * TPR + t, cols);
+    }
+  } else {
+    const uint32_t chunks = (cols + 7) / 8;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      v[j] = u32x4{0, 0, 0, 0};
+      if (live && j * TPR + t < chunks)
+        v[j] = load_chunk8(p + (threadIdx.x / TPR) * ld, j * TPR + t, cols);
+    }
+  }
+}
+
+// The weight's chunks of a thread.
+template <int TPR, int C>
+__device__ __forceinline__ void load_weight(const uint16_t* w, uint32_t t, uint32_t cols,
+                                            u32x4 (&v)[C]) {
+  const RowWords row(w, cols);
+#pragma unroll
+  for (int j = 0; j < C; ++j) v[j] = row.load(j * TPR + t);
+  if (cols & 1) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = trim(v[j], j * TPR + t, cols);
   }
 }
 
@@ -283,7 +381,7 @@ __device__ __forceinline__ void measure_chunk(u32x4 h, u32x4 w, float& s, uint32
   }
 }
 
-template <int TYPE, int OUT>
+template <int TYPE, int OUT, bool STREAM>
 __device__ __forceinline__ void finish_chunk(const NormArgs& k, uint64_t row, uint32_t c, u32x4 h,
                                              u32x4 w, float inv, const CodeScale& cs) {
   float f[8], g[8];
@@ -293,13 +391,13 @@ __device__ __forceinline__ void finish_chunk(const NormArgs& k, uint64_t row, ui
   if constexpr (OUT == kOut16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
-    store_chunk8(k.out + row * k.ldo, c, cols, narrow8<TYPE>(f));
+    store_chunk8<STREAM>(k.out + row * k.ldo, c, cols, narrow8<TYPE>(f));
   } else {
     if constexpr (OUT == kOutCodes) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= g[i];
     }
-    store_codes8(k.codes + row * k.ldc, c, cols, codes8(f, cs));
+    store_codes8<STREAM>(k.codes + row * k.ldc, c, cols, codes8<OUT == kOutQuant>(f, cs));
   }
 }
 
@@ -315,7 +413,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& k, uint64_t row, floa
 
 // Rows in registers: TPR threads per row, C chunks each; a block of at least
 // kRowBlock threads takes block / TPR rows at a time.
-template <int TYPE, int OUT, bool RES, int TPR, int C>
+template <int TYPE, int OUT, bool RES, bool STREAM, int TPR, int C>
 __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel(NormArgs k) {
   constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
   constexpr int kRows = kBlock / TPR;
@@ -325,11 +423,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
   u32x4 w[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) w[j] = u32x4{0, 0, 0, 0};
-  if constexpr (OUT != kOutQuant) {
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (j * TPR + t < chunks) w[j] = load_chunk8(k.weight, j * TPR + t, cols);
-  }
+  if constexpr (OUT != kOutQuant) load_weight<TPR>(k.weight, t, cols, w);
   int turn = 0;
   // every thread of a block makes the same number of rounds (barriers)
   for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows;
@@ -339,18 +433,18 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
     u32x4 h[C];
     float s = 0.0f;
     uint32_t m = 0;
+    load_row<TPR>(k.x + base * k.ldx, k.ldx, live, t, cols, h);
+    if constexpr (RES) {
+      u32x4 res[C];
+      load_row<TPR>(k.residual + base * k.ldr, k.ldr, live, t, cols, res);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
-      h[j] = u32x4{0, 0, 0, 0};
-      if (live && c < chunks)
-        h[j] = load_sum<TYPE, RES>(k.x + row * k.ldx, k.residual + row * k.ldr, c, cols);
+      for (int j = 0; j < C; ++j) h[j] = sum8<TYPE>(h[j], res[j]);
     }
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t c = j * TPR + t;
       if (RES && k.sum_out && live && c < chunks)
-        store_chunk8(k.sum_out + row * k.lds, c, cols, h[j]);
+        store_chunk8<STREAM>(k.sum_out + row * k.lds, c, cols, h[j]);
       measure_chunk<TYPE, OUT>(h[j], w[j], s, m);
     }
     RowCombine<TPR>::run(s, m, lds, turn);
@@ -360,7 +454,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t c = j * TPR + t;
-      if (c < chunks) finish_chunk<TYPE, OUT>(k, row, c, h[j], w[j], inv, cs);
+      if (c < chunks) finish_chunk<TYPE, OUT, STREAM>(k, row, c, h[j], w[j], inv, cs);
     }
     if (t == 0) finish_row<OUT>(k, row, inv, m);
   }
@@ -382,7 +476,7 @@ __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
     uint32_t m = 0;
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
       const u32x4 h = load_sum<TYPE, RES>(xr, rr, c, cols);
-      if (RES && k.sum_out) store_chunk8(k.sum_out + row * k.lds, c, cols, h);
+      if (RES && k.sum_out) store_chunk8<false>(k.sum_out + row * k.lds, c, cols, h);
       const u32x4 w = OUT == kOutCodes ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
       measure_chunk<TYPE, OUT>(h, w, s, m);
     }
@@ -393,7 +487,7 @@ __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
       const u32x4 h = RES && k.sum_out ? load_chunk8(k.sum_out + row * k.lds, c, cols)
                                        : load_sum<TYPE, RES>(xr, rr, c, cols);
       const u32x4 w = OUT != kOutQuant ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
-      finish_chunk<TYPE, OUT>(k, row, c, h, w, inv, cs);
+      finish_chunk<TYPE, OUT, false>(k, row, c, h, w, inv, cs);
     }
     if (threadIdx.x == 0) finish_row<OUT>(k, row, inv, m);
   }
@@ -412,18 +506,20 @@ hipError_t launch_rows_kernel(const void* fn, uint64_t blocks, int threads, void
 template <int TYPE, int OUT, bool RES>
 hipError_t launch_norm_typed(const NormArgs& a, const armx_config* cfg, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
+  const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
 #define ARMX_NORM_CASE(T, C) \
   if (s.threads == T && s.chunks == C) \
-    fn = reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, T, C>)
+    fn = stream_out ? reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, true, T, C>) \
+                    : reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, false, T, C>)
   ARMX_NORM_CASE(8, 1);
   ARMX_NORM_CASE(16, 1);
   ARMX_NORM_CASE(32, 1);
   ARMX_NORM_CASE(64, 1);
-  ARMX_NORM_CASE(64, 2);
+  ARMX_NORM_CASE(128, 1);
   ARMX_NORM_CASE(256, 1);
-  ARMX_NORM_CASE(256, 2);
-  ARMX_NORM_CASE(256, 4);
+  ARMX_NORM_CASE(512, 1);
+  ARMX_NORM_CASE(512, 2);
   ARMX_NORM_CASE(512, 4);
   ARMX_NORM_CASE(1024, 4);
 #undef ARMX_NORM_CASE
@@ -452,7 +548,7 @@ hipError_t launch_norm_out(const NormArgs& a, const armx_config* cfg, hipStream_
 // Block b takes the row groups b, b + blocks, ...; every thread keeps the
 // dweight sums of its own columns in registers over the block's rows.  A block
 // of several rows at a time adds its row groups' sums through LDS, in order.
-template <int TYPE, bool DSUM, int TPR, int C>
+template <int TYPE, bool DSUM, bool STREAM, int TPR, int C>
 __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backward_kernel(
     NormBackwardArgs k, float* dst, uint64_t pitch) {
   constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
@@ -465,11 +561,10 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
   float acc[C][8];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    w[j] = u32x4{0, 0, 0, 0};
-    if (j * TPR + t < chunks) w[j] = load_chunk8(k.weight, j * TPR + t, cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
   }
+  load_weight<TPR>(k.weight, t, cols, w);
   // One row group's values; with kAhead the next group's are on their way while
   // this one's are combined (8192 x 4096 56.6 -> 54.3 us; at 512 threads x 4, where
   // the registers no longer hold both, 62 -> 71).
@@ -483,16 +578,9 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
     const uint64_t row = base + threadIdx.x / TPR;
     const bool live = row < k.rows;
     v.inv = live ? k.inv_rms[row] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
-      v.dy[j] = v.h[j] = v.ds[j] = u32x4{0, 0, 0, 0};
-      if (live && c < chunks) {
-        v.dy[j] = load_chunk8(k.dy + row * k.ldy, c, cols);
-        v.h[j] = load_chunk8(k.h + row * k.ldh, c, cols);
-        if constexpr (DSUM) v.ds[j] = load_chunk8(k.dsum + row * k.ldd, c, cols);
-      }
-    }
+    load_row<TPR>(k.dy + base * k.ldy, k.ldy, live, t, cols, v.dy);
+    load_row<TPR>(k.h + base * k.ldh, k.ldh, live, t, cols, v.h);
+    if constexpr (DSUM) load_row<TPR>(k.dsum + base * k.ldd, k.ldd, live, t, cols, v.ds);
     return v;
   };
   int turn = 0;
@@ -542,7 +630,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
         fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
         if constexpr (DSUM) fy[i] += fd[i];
       }
-      store_chunk8(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+      store_chunk8<STREAM>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
     }
   }
   if constexpr (kRows > 1) {
@@ -615,7 +703,7 @@ __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardAr
         fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
         if constexpr (DSUM) fy[i] += fd[i];
       }
-      store_chunk8(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+      store_chunk8<false>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
     }
   }
 }
@@ -660,18 +748,21 @@ template <int TYPE, bool DSUM>
 hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPlan& plan,
                                  const armx_config* cfg, hipStream_t stream) {
   const RowShape s = plan.shape;
+  const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
 #define ARMX_NORM_CASE(T, C) \
   if (s.threads == T && s.chunks == C) \
-    fn = reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, T, C>)
+    fn = stream_out                                                                            \
+             ? reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, true, T, C>)    \
+             : reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, false, T, C>)
   ARMX_NORM_CASE(8, 1);
   ARMX_NORM_CASE(16, 1);
   ARMX_NORM_CASE(32, 1);
   ARMX_NORM_CASE(64, 1);
-  ARMX_NORM_CASE(64, 2);
+  ARMX_NORM_CASE(128, 1);
   ARMX_NORM_CASE(256, 1);
-  ARMX_NORM_CASE(256, 2);
-  ARMX_NORM_CASE(256, 4);
+  ARMX_NORM_CASE(512, 1);
+  ARMX_NORM_CASE(512, 2);
   ARMX_NORM_CASE(512, 4);
   ARMX_NORM_CASE(1024, 4);
 #undef ARMX_NORM_CASE
@@ -706,7 +797,7 @@ NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) 
   // less, and too few leave loads unsent.  Measured on MI355X at 1, 2 and 4 blocks
   // of 256 threads per compute unit (us): 8192 x 4096 55.4, 54.3, 61.2; 4096 x 8192
   // 54.9, 58.9, 69.0; 32768 x 128 11.6, 10.7, 11.7.
-  const uint64_t most = uint64_t(cu_count) * (cols <= 4096 ? 2 : 1);
+  const uint64_t most = uint64_t(cu_count) * (cols <= 2048 ? 2 : 1);
   p.blocks = groups < most ? groups : most;
   p.pitch = (cols + 63) / 64 * 64;
   if (p.blocks > 1) p.ws_bytes = size_t(p.blocks * p.pitch * sizeof(float));
