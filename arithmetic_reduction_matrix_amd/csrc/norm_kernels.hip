@@ -166,14 +166,14 @@ __device__ __forceinline__ uint32_t lane_max(uint32_t v, int levels) {
 constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 
 // The row's sum of squares and largest magnitude (bits), in each of its
-// threads.  TPR > 64: over the block's wavefronts through LDS, added in
-// wavefront order by every thread alike.
-template <int TPR>
+// threads.  TPR > 64: over the row's wavefronts through LDS, added in wavefront
+// order by every thread alike; the block's ROWS rows each have a place.
+template <int TPR, int ROWS>
 struct RowCombine {
   static constexpr int kWaves = TPR > 64 ? TPR / 64 : 1;
   struct Lds {
-    float s[kWaves];
-    uint32_t m[kWaves];
+    float s[ROWS][kWaves];
+    uint32_t m[ROWS][kWaves];
   };
   // `turn` alternates between the two halves of `lds` from row to row, so one
   // barrier per row is enough
@@ -183,17 +183,18 @@ struct RowCombine {
     m = lane_max(m, levels);
     if constexpr (TPR > 64) {
       Lds& l = lds[turn];
+      const int row = wave_id() / kWaves;
       if (lane_id() == 0) {
-        l.s[wave_id()] = s;
-        l.m[wave_id()] = m;
+        l.s[row][wave_id() % kWaves] = s;
+        l.m[row][wave_id() % kWaves] = m;
       }
       __syncthreads();
       s = 0.0f;
       m = 0;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        s += l.s[w];
-        m = max_u32(m, l.m[w]);
+        s += l.s[row][w];
+        m = max_u32(m, l.m[row][w]);
       }
     }
   }
@@ -417,7 +418,7 @@ template <int TYPE, int OUT, bool RES, bool STREAM, int TPR, int C>
 __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel(NormArgs k) {
   constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
   constexpr int kRows = kBlock / TPR;
-  __shared__ typename RowCombine<TPR>::Lds lds[2];
+  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
   const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
   const uint32_t chunks = (cols + 7) / 8;
   u32x4 w[C];
@@ -447,7 +448,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
         store_chunk8<STREAM>(k.sum_out + row * k.lds, c, cols, h[j]);
       measure_chunk<TYPE, OUT>(h[j], w[j], s, m);
     }
-    RowCombine<TPR>::run(s, m, lds, turn);
+    RowCombine<TPR, kRows>::run(s, m, lds, turn);
     const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
     const CodeScale cs(m);
     if (!live) continue;
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
 // where inputs did.
 template <int TYPE, int OUT, bool RES>
 __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
-  __shared__ typename RowCombine<1024>::Lds lds[2];
+  __shared__ typename RowCombine<1024, 1>::Lds lds[2];
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   int turn = 0;
   for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x, turn ^= 1) {
@@ -480,7 +481,7 @@ __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
       const u32x4 w = OUT == kOutCodes ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
       measure_chunk<TYPE, OUT>(h, w, s, m);
     }
-    RowCombine<1024>::run(s, m, lds, turn);
+    RowCombine<1024, 1>::run(s, m, lds, turn);
     const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
     const CodeScale cs(m);
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
@@ -553,7 +554,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
     NormBackwardArgs k, float* dst, uint64_t pitch) {
   constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
   constexpr int kRows = kBlock / TPR;
-  __shared__ typename RowCombine<TPR>::Lds lds[2];
+  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
   __shared__ float part[kRows > 1 ? kRows * TPR * C * 8 : 1];
   const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
   const uint32_t chunks = (cols + 7) / 8;
@@ -613,7 +614,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
       }
     }
     uint32_t unused = 0;
-    RowCombine<TPR>::run(dot, unused, lds, turn);
+    RowCombine<TPR, kRows>::run(dot, unused, lds, turn);
     if (!live) continue;
     const float f = inv * inv * (dot / float(k.cols));
 #pragma unroll
@@ -667,7 +668,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
 template <int TYPE, bool DSUM>
 __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardArgs k, float* dst,
                                                                   uint64_t pitch) {
-  __shared__ typename RowCombine<1024>::Lds lds[2];
+  __shared__ typename RowCombine<1024, 1>::Lds lds[2];
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   float* sums = dst + uint64_t(blockIdx.x) * pitch;
   for (uint32_t c = threadIdx.x; c < chunks; c += 1024)
@@ -688,7 +689,7 @@ __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardAr
       for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
     }
     uint32_t unused = 0;
-    RowCombine<1024>::run(dot, unused, lds, turn);
+    RowCombine<1024, 1>::run(dot, unused, lds, turn);
     const float f = inv * inv * (dot / float(k.cols));
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
       float fy[8], fh[8], fw[8], fd[8];
