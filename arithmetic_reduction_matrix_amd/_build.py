@@ -1,17 +1,21 @@
-"""Builds libarmx.so (the HIP kernels and the C entry points) for gfx950, and
-libarmx_probe.so (a plain read stream, for measurement only).
+"""Builds libarmx.so (the HIP kernels and the C entry points) for gfx950,
+_binding.so (the layer entry points for PyTorch tensors), and libarmx_probe.so (a
+plain read stream, for measurement only).
 
-Run ``python arithmetic_reduction_matrix_amd/_build.py`` or call ``build()`` (it needs
-only the standard library, so it runs whether or not a library is built).
+Run ``python arithmetic_reduction_matrix_amd/_build.py`` or call ``build()`` (it imports
+only the standard library, so it runs whether or not a library is built; the
+binding is compiled against the headers of the installed PyTorch).
 Every source is compiled each time; objects go to ``_build/`` next to this
 file and the library is written to ``libarmx.so`` in this package.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +27,9 @@ LIB = os.path.join(PKG, "libarmx.so")
 # measurement only: the plain read stream the reductions are compared with
 PROBE_LIB = os.path.join(PKG, "libarmx_probe.so")
 PROBE_SOURCES = ["read_probe.hip"]
+# the layer entry points for PyTorch tensors (a CPython module)
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCES = ["binding.cpp"]
 
 ARCH = "gfx950"
 HIP_SOURCES = ["sum_kernels.hip", "fixed_kernels.hip", "rows_kernels.hip", "exact_kernels.hip",
@@ -58,6 +65,14 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
+def _torch_dir() -> str:
+    """Where PyTorch is installed (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch is not installed")
+    return list(spec.submodule_search_locations)[0]
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compiles every source and links libarmx.so; returns its path."""
     hipcc = _hipcc()
@@ -78,11 +93,28 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         obj = os.path.join(BUILD, src + ".o")
         probe_objs.append(obj)
         cmds.append([hipcc, *COMMON, *DEVICE, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj])
+    binding_objs = []
+    torch_dir = _torch_dir()
+    include = [os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    for src in BINDING_SOURCES:
+        obj = os.path.join(BUILD, src + ".o")
+        binding_objs.append(obj)
+        # first in the list: it takes longest
+        cmds.insert(0, [hipcc, *COMMON, *(f"-isystem{d}" for d in include), "-DUSE_ROCM", "-c",
+                        os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         list(pool.map(lambda c: _run(c, verbose), cmds))
-    for out, parts in ((LIB, objs), (PROBE_LIB, probe_objs)):
+    torch_lib = os.path.join(torch_dir, "lib")
+    for out, parts, more in (
+            (LIB, objs, []), (PROBE_LIB, probe_objs, []),
+            (BINDING, binding_objs,
+             [f"-L{PKG}", "-l:libarmx.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch",
+              "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])):
         tmp = out + ".tmp"
-        _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *parts, "-o", tmp], verbose)
+        _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *parts, *more, "-o", tmp],
+             verbose)
         os.replace(tmp, out)
     return LIB
 

@@ -114,7 +114,7 @@ __device__ __forceinline__ void store_codes8(int8_t* row, uint32_t c, uint32_t c
 // values: a load of a chunk past them returns zeros with no memory access, so the
 // loads of a row's chunks stand in no branch and are all in flight together (a
 // branch around a load makes the compiler wait where its paths join: 37 rows of
-// 5001 values, norm to codes, 6.8 -> XX us).  With an odd count the last word
+// 5001 values, norm to codes, 6.8 -> 6.6 us).  With an odd count the last word
 // holds one value past the row; trim() clears it.
 constexpr int kRawBuffer = 0x00020000;
 struct RowWords {

@@ -388,7 +388,8 @@ int reduce_sum_noalloc(const void* x, size_t n, float* out, const armx_config* c
  *   least the row's length).  Rows of 16-bit values start at multiples of 16
  *   bytes (pointer 16-byte aligned, pitch a multiple of 8 when there is more
  *   than one row); rows of codes too (pitch a multiple of 16).  Pitch padding
- *   is never written, and never read but where matmul_int8 says so.
+ *   is never written; of what follows a row's last value, reads may cover the
+ *   rest of its 4-byte word and what matmul_int8 says, and never use it.
  * - `cfg` may give the two events only; every other field must be zero
  *   (ARMX_ERR_CONFIG).
  * - A row's result depends on that row's values (and weight, scales and bias)
