@@ -165,7 +165,7 @@ inline int aligned_rows(const MatmulArgs& p) {
 // share k: a group takes every KS-th step of 128 codes and sums over its own.
 // A step's rows of a and b go from memory straight to LDS (buffer_load ... lds,
 // 16 bytes per lane, 8 rows of 128 bytes per wavefront load) into one of the
-// group's two buffers while the other is multiplied.  (Steps of 64 codes in four
+// group's NS buffers, NS - 1 steps ahead of the one that is multiplied.  (Steps of 64 codes in four
 // buffers, with rows of 64 bytes, measured slower, 8192^3 450 -> 715 us: memory
 // moves lines of 128 bytes, and each was moved twice.)
 //
@@ -184,14 +184,14 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
 
 constexpr int kStepK = 128;
 #define ARMX_INLINE __attribute__((always_inline))
-struct Yes {
-  static constexpr bool value = true;
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
-struct No {
-  static constexpr bool value = false;
-};
+using Yes = Int<1>;
+using No = Int<0>;
 
-template <int BM, int BN, int WM, int WN, int KS>
+template <int BM, int BN, int WM, int WN, int KS, int NS>
 struct Tile {
   static constexpr int kGroup = WM * WN;  // wavefronts of a group
   static constexpr int kWaves = kGroup * KS;
@@ -201,10 +201,11 @@ struct Tile {
   static constexpr int kLoadsB = BN / 8 / kGroup;
   static constexpr int kStageBytes = (BM + BN) * kStepK;
   static constexpr int kSumBytes = KS > 1 ? KS * BM * BN * 4 : 0;
-  static constexpr int kLdsBytes =
-      2 * KS * kStageBytes > kSumBytes ? 2 * KS * kStageBytes : kSumBytes;
+  static constexpr int kRingBytes = NS * kStageBytes;   // a group's buffers
+  static constexpr int kLdsBytes = KS * kRingBytes > kSumBytes ? KS * kRingBytes : kSumBytes;
   static_assert(kLoadsA * 8 * kGroup == BM && kLoadsB * 8 * kGroup == BN, "whole loads");
   static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
+  static_assert(NS >= 2 && NS <= 4, "the last steps are written out");
 };
 
 typedef __attribute__((address_space(3))) int8_t lds_byte;
@@ -224,8 +225,12 @@ __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
   return *reinterpret_cast<const u32x4 __attribute__((address_space(3)))*>(at);
 }
 
-// vmcnt(0): this wavefront's loads into LDS have landed
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// vmcnt(N): all but this wavefront's last N loads into LDS have landed
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the count's six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
 
 // Which tile a block makes: every XCD takes a contiguous range of ids, and ids
 // run down 4 rows of tiles before the next column, so that blocks running at
@@ -241,18 +246,21 @@ __device__ __forceinline__ void tile_of_block(unsigned tiles_m, unsigned tiles_n
   tj = in / rows;
 }
 
-template <int BM, int BN, int WM, int WN, int KS, int OUT>
+template <int BM, int BN, int WM, int WN, int KS, int NS, int OUT>
 __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(MatmulArgs p,
                                                                            unsigned tiles_m,
                                                                            unsigned tiles_n,
                                                                            int aligned) {
-  using T = Tile<BM, BN, WM, WN, KS>;
+  using T = Tile<BM, BN, WM, WN, KS, NS>;
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   const int lane = lane_id(), group = wave_id() / T::kGroup, w = wave_id() % T::kGroup;
-  // the buffer in use; flip - base is the other
-  uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_byte*)lds)) +
-                  uint32_t(group) * (2 * T::kStageBytes);
-  const uint32_t flip = 2 * base + T::kStageBytes;
+  // the group's ring of buffers, and the one in use
+  const uint32_t ring = uint32_t(reinterpret_cast<uintptr_t>((lds_byte*)lds)) +
+                        uint32_t(group) * T::kRingBytes;
+  uint32_t base = ring;
+  auto next = [&](uint32_t at) ARMX_INLINE {
+    return at == ring + (NS - 1) * T::kStageBytes ? ring : at + T::kStageBytes;
+  };
   unsigned ti, tj;
   tile_of_block(tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * BM, j0 = uint64_t(tj) * BN;
@@ -291,10 +299,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) stage_one(to, k0, x);
   };
-  // all of the group's loads have landed and all its reads are done; a group of
-  // one wavefront has only itself to wait for
-  auto sync = [&]() ARMX_INLINE {
-    wait_loads();
+  // all but the group's last `steps` steps of loads have landed and all its reads are
+  // done; a group of one wavefront has only itself to wait for
+  auto sync = [&](auto steps) ARMX_INLINE {
+    wait_loads<decltype(steps)::value * kLoads>();
     if constexpr (T::kGroup > 1)
       __syncthreads();
     else
@@ -370,15 +378,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
   };
   // A step but the last (its first half's operands already in registers): the
   // second half's are read while the first is multiplied; then, after the
-  // barrier that ends all reading of this buffer and finds the other one
-  // filled, the step after next is sent for into it (SEND) and the next step's
-  // first half read under the second half's products.
+  // barrier that ends all reading of this buffer and finds the next one filled
+  // (`out`: steps sent for behind that one), the step NS on is sent for into it
+  // (SEND) and the next step's first half read under the second half's products.
   constexpr uint32_t kStride = KS * kStepK;
-  auto step = [&](auto send, uint32_t k0) ARMX_INLINE {
+  auto step = [&](auto send, auto out, uint32_t k0) ARMX_INLINE {
     multiply_and_fetch(1, base, No{}, 0, 0);
-    sync();
-    const uint32_t other = flip - base;
-    multiply_and_fetch(0, other, send, base, k0 + 2 * kStride);
+    sync(out);
+    const uint32_t other = next(base);
+    multiply_and_fetch(0, other, send, base, k0 + NS * kStride);
     base = other;
   };
   if (k > 0) {
@@ -387,13 +395,29 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
     // and is cut to zeros
     uint32_t k0 = uint32_t(group) * kStepK;
     uint32_t left = (k + kStride - 1) / kStride;
-    stage(base, k0);
-    sync();
-    if (left > 1) stage(flip - base, k0 + kStride);
+    if (left >= NS) {
+#pragma unroll
+      for (int t = 0; t < NS; ++t) stage(ring + t * T::kStageBytes, k0 + t * kStride);
+      sync(Int<NS - 1>{});
+    } else {
+      for (uint32_t t = 0; t < left; ++t) stage(ring + t * T::kStageBytes, k0 + t * kStride);
+      sync(No{});
+    }
     fetch_half(base, 0);
-    for (; left > 2; --left, k0 += kStride) step(Yes{}, k0);
+    for (; left > NS; --left, k0 += kStride) step(Yes{}, Int<NS - 2>{}, k0);
+    // the last NS steps; what is still out shrinks with them
+    if constexpr (NS > 3)
+      if (left > 3) {
+        step(No{}, Int<NS - 2>{}, k0);
+        --left, k0 += kStride;
+      }
+    if constexpr (NS > 2)
+      if (left > 2) {
+        step(No{}, Int<1>{}, k0);
+        --left, k0 += kStride;
+      }
     if (left > 1) {
-      step(No{}, k0);
+      step(No{}, No{}, k0);
       k0 += kStride;
     }
     fetch_half(base, 1);
@@ -436,13 +460,13 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
   }
 }
 
-template <int OUT, int BM, int BN, int WM, int WN, int KS>
+template <int OUT, int BM, int BN, int WM, int WN, int KS, int NS>
 hipError_t launch_tiled(const MatmulArgs& p, const armx_config* cfg, hipStream_t stream) {
   MatmulArgs copy = p;
   unsigned tiles_m = unsigned((p.m + BM - 1) / BM), tiles_n = unsigned((p.n + BN - 1) / BN);
   int aligned = aligned_rows(p);
   void* args[] = {&copy, &tiles_m, &tiles_n, &aligned};
-  return launch_kernel(reinterpret_cast<const void*>(&matmul_tiled_kernel<BM, BN, WM, WN, KS, OUT>),
+  return launch_kernel(reinterpret_cast<const void*>(&matmul_tiled_kernel<BM, BN, WM, WN, KS, NS, OUT>),
                        dim3(tiles_m * tiles_n), dim3(64 * WM * WN * KS), args, 0, stream,
                        cfg ? static_cast<hipEvent_t>(cfg->start_event) : nullptr,
                        cfg ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
@@ -454,26 +478,28 @@ hipError_t launch_tiled(const MatmulArgs& p, const armx_config* cfg, hipStream_t
 // them in rounds of at most `resident` blocks; a round takes `fixed` (its first
 // loads, its epilogue) and, per step of KS x 128 codes, `alone` or, with several
 // blocks on the unit, `each` of them if that is more.  The constants (us) are
-// fitted to times of each tile on MI355X over 176 shapes of 1 to 8192 rows, 128 to
+// fitted to times of each tile on MI355X over 192 shapes of 1 to 8192 rows, 128 to
 // 28672 columns and lengths of 128 to 14336; the tile they choose is 1.3% behind
-// the fastest of all twenty measured on average and 15% at worst.  Each of the ten
+// the fastest of all 29 measured on average and 17% at worst.  Each of the eleven
 // pays where it is chosen (us, it and the best of the others): 256 x 256 at
-// 8192^3 416 (128 x 128: 516); 128 x 128 at 2048 x 4096 x 4096 37.5 (63);
-// its two groups at 1024 x 4096 x 14336 82 (96); 64 x 64 by 2 at 512 x 4096 x 4096
-// 15.8 (20.2), by 4 at 256 x 4096 x 14336 41.7 (47.7); 64 x 32 at 128 x 4096 x 14336
-// 27.2 (34.6); 48 x 32 at 160 x 4096 x 14336 39 (42); 32 x 32 at 64 x 4096 x 4096 6.8
-// (8.0); 16 x 32 at 32 x 4096 x 14336 18.0 (21.4); 16 x 16 at 16 x 4096 x 14336
-// 14.2 (18.0).
+// 4096 x 4096 x 14336 177 (208); 192 x 192 at 2048 x 4096 x 14336 103 (108);
+// 128 x 256 at 512 x 14336 x 4096 36.8 (39.0); 192 x 128 at 1500 x 4096 x 14336 83
+// (97); 128 x 128 at 1024 x 4096 x 14336 68.5 (79.4); 64 x 128 at 512 x 4096 x 14336
+// 51.9 (58.9); 64 x 64 at 256 x 4096 x 14336 35.6 (45.6); 64 x 32 at
+// 128 x 4096 x 14336 26.3 (35.6); 32 x 32 at 48 x 4096 x 14336 19.2 (25.0);
+// 16 x 32 at 16 x 8192 x 8192 15.1 (15.7 and more); 16 x 16 at 16 x 4096 x 14336
+// 13.7 (18.4).
 struct TileTime {
   int bm, bn, ks, resident;
   float fixed, alone, each;
 };
 constexpr TileTime kTiles[] = {
-    {256, 256, 1, 1, 5.03f, 1.39f, 1.39f}, {128, 128, 1, 2, 2.24f, 0.71f, 0.48f},
-    {128, 128, 2, 1, 3.08f, 1.21f, 1.21f}, {64, 64, 2, 2, 1.76f, 0.61f, 0.43f},
-    {64, 64, 4, 1, 1.97f, 1.11f, 1.11f},   {64, 32, 6, 1, 1.86f, 0.86f, 0.86f},
-    {48, 32, 8, 1, 1.80f, 0.93f, 0.93f},   {32, 32, 8, 1, 1.62f, 0.81f, 0.81f},
-    {16, 32, 8, 1, 1.47f, 0.67f, 0.67f},   {16, 16, 16, 1, 1.35f, 1.02f, 1.02f},
+    {256, 256, 1, 1, 3.04f, 1.50f, 1.50f}, {192, 192, 1, 1, 4.80f, 0.84f, 0.84f},
+    {128, 256, 1, 1, 3.46f, 0.86f, 0.86f}, {192, 128, 1, 1, 3.01f, 0.65f, 0.65f},
+    {128, 128, 1, 1, 2.58f, 0.52f, 0.52f}, {64, 128, 1, 2, 2.22f, 0.11f, 0.33f},
+    {64, 64, 1, 2, 1.93f, 0.09f, 0.19f},   {64, 32, 4, 1, 1.89f, 0.56f, 0.56f},
+    {32, 32, 4, 1, 1.69f, 0.39f, 0.39f},   {16, 32, 8, 1, 1.42f, 0.70f, 0.70f},
+    {16, 16, 8, 1, 1.28f, 0.46f, 0.46f},
 };
 
 inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
@@ -506,16 +532,17 @@ template <int OUT>
 hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cfg,
                         hipStream_t stream) {
   switch (choose_tile(p, cu_count)) {
-    case 0: return launch_tiled<OUT, 256, 256, 2, 4, 1>(p, cfg, stream);
-    case 1: return launch_tiled<OUT, 128, 128, 2, 4, 1>(p, cfg, stream);
-    case 2: return launch_tiled<OUT, 128, 128, 2, 2, 2>(p, cfg, stream);
-    case 3: return launch_tiled<OUT, 64, 64, 2, 2, 2>(p, cfg, stream);
-    case 4: return launch_tiled<OUT, 64, 64, 2, 2, 4>(p, cfg, stream);
-    case 5: return launch_tiled<OUT, 64, 32, 1, 1, 6>(p, cfg, stream);
-    case 6: return launch_tiled<OUT, 48, 32, 1, 1, 8>(p, cfg, stream);
-    case 7: return launch_tiled<OUT, 32, 32, 1, 1, 8>(p, cfg, stream);
-    case 8: return launch_tiled<OUT, 16, 32, 1, 1, 8>(p, cfg, stream);
-    case 9: return launch_tiled<OUT, 16, 16, 1, 1, 16>(p, cfg, stream);
+    case 0: return launch_tiled<OUT, 256, 256, 2, 4, 1, 2>(p, cfg, stream);
+    case 1: return launch_tiled<OUT, 192, 192, 4, 2, 1, 3>(p, cfg, stream);
+    case 2: return launch_tiled<OUT, 128, 256, 2, 4, 1, 3>(p, cfg, stream);
+    case 3: return launch_tiled<OUT, 192, 128, 4, 2, 1, 3>(p, cfg, stream);
+    case 4: return launch_tiled<OUT, 128, 128, 2, 4, 1, 3>(p, cfg, stream);
+    case 5: return launch_tiled<OUT, 64, 128, 2, 4, 1, 3>(p, cfg, stream);
+    case 6: return launch_tiled<OUT, 64, 64, 2, 2, 1, 4>(p, cfg, stream);
+    case 7: return launch_tiled<OUT, 64, 32, 1, 1, 4, 3>(p, cfg, stream);
+    case 8: return launch_tiled<OUT, 32, 32, 1, 1, 4, 4>(p, cfg, stream);
+    case 9: return launch_tiled<OUT, 16, 32, 1, 1, 8, 2>(p, cfg, stream);
+    case 10: return launch_tiled<OUT, 16, 16, 1, 1, 8, 4>(p, cfg, stream);
     default: return hipErrorInvalidValue;  // no grid holds that many tiles
   }
 }
