@@ -260,7 +260,7 @@ int armx_launch_plan(int op, size_t n_or_rows, size_t cols, const armx_config* c
     r.block_threads = p.blocks ? p.block : 0;
     r.chain_r = p.blocks ? p.shape.chunks : 0;
     r.waves_per_cu = double(p.blocks) * double(p.block / 64) / double(current_cu_count());
-    r.launches = cols == 0 ? 0 : p.blocks > 1 ? 2 : 1;
+    r.launches = cols == 0 ? 0 : p.ws_bytes ? 2 : 1;
     *info = r;
     return ARMX_OK;
   }

@@ -64,7 +64,8 @@ struct NormBackwardArgs {
 struct NormBackwardPlan {
   RowShape shape{};
   int block = 0;        // threads per block
-  uint64_t blocks = 0;  // each sums dweight over its own rows
+  bool apart = false;   // some blocks sum dweight's columns, the others make dx
+  uint64_t blocks = 0;  // otherwise each sums dweight over its own rows
   uint64_t pitch = 0;   // floats between the blocks' partial sums
   size_t ws_bytes = 0;
 };

@@ -504,6 +504,20 @@ hipError_t launch_rows_kernel(const void* fn, uint64_t blocks, int threads, void
                        cfg && last ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
 }
 
+#define ARMX_EACH_SHAPE_BELOW_1024(CASE) \
+  CASE(8, 1);                 \
+  CASE(16, 1);                \
+  CASE(32, 1);                \
+  CASE(64, 1);                \
+  CASE(128, 1);               \
+  CASE(256, 1);               \
+  CASE(512, 1);               \
+  CASE(512, 2);               \
+  CASE(512, 4)
+#define ARMX_EACH_SHAPE(CASE)       \
+  ARMX_EACH_SHAPE_BELOW_1024(CASE); \
+  CASE(1024, 4)
+
 template <int TYPE, int OUT, bool RES>
 hipError_t launch_norm_typed(const NormArgs& a, const armx_config* cfg, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
@@ -513,16 +527,7 @@ hipError_t launch_norm_typed(const NormArgs& a, const armx_config* cfg, hipStrea
   if (s.threads == T && s.chunks == C) \
     fn = stream_out ? reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, true, T, C>) \
                     : reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, false, T, C>)
-  ARMX_NORM_CASE(8, 1);
-  ARMX_NORM_CASE(16, 1);
-  ARMX_NORM_CASE(32, 1);
-  ARMX_NORM_CASE(64, 1);
-  ARMX_NORM_CASE(128, 1);
-  ARMX_NORM_CASE(256, 1);
-  ARMX_NORM_CASE(512, 1);
-  ARMX_NORM_CASE(512, 2);
-  ARMX_NORM_CASE(512, 4);
-  ARMX_NORM_CASE(1024, 4);
+  ARMX_EACH_SHAPE(ARMX_NORM_CASE);
 #undef ARMX_NORM_CASE
   if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_loop_kernel<TYPE, OUT, RES>);
   const int block = s.threads > kRowBlock ? s.threads : kRowBlock;
@@ -545,6 +550,32 @@ hipError_t launch_norm_out(const NormArgs& a, const armx_config* cfg, hipStream_
 }
 
 // ---- backward ---------------------------------------------------------------------------
+
+// dx of the chunks of a row that a thread holds.
+template <int TYPE, bool DSUM, bool STREAM, int TPR, int C>
+__device__ __forceinline__ void store_grads(const NormBackwardArgs& k, uint64_t row, uint32_t t,
+                                            float inv, float dot, const u32x4 (&dy)[C],
+                                            const u32x4 (&h)[C], const u32x4 (&ds)[C],
+                                            const u32x4 (&w)[C]) {
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+  const float f = inv * inv * (dot / float(k.cols));
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const uint32_t c = j * TPR + t;
+    if (c >= chunks) continue;
+    float fy[8], fh[8], fw[8], fd[8];
+    widen8<TYPE>(dy[j], fy);
+    widen8<TYPE>(h[j], fh);
+    widen8<TYPE>(w[j], fw);
+    if constexpr (DSUM) widen8<TYPE>(ds[j], fd);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
+      if constexpr (DSUM) fy[i] += fd[i];
+    }
+    store_chunk8<STREAM>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+  }
+}
 
 // Block b takes the row groups b, b + blocks, ...; every thread keeps the
 // dweight sums of its own columns in registers over the block's rows.  A block
@@ -616,23 +647,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
     uint32_t unused = 0;
     RowCombine<TPR, kRows>::run(dot, unused, lds, turn);
     if (!live) continue;
-    const float f = inv * inv * (dot / float(k.cols));
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
-      if (c >= chunks) continue;
-      float fy[8], fh[8], fw[8], fd[8];
-      widen8<TYPE>(dy[j], fy);
-      widen8<TYPE>(h[j], fh);
-      widen8<TYPE>(w[j], fw);
-      if constexpr (DSUM) widen8<TYPE>(ds[j], fd);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
-        if constexpr (DSUM) fy[i] += fd[i];
-      }
-      store_chunk8<STREAM>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
-    }
+    store_grads<TYPE, DSUM, STREAM, TPR>(k, row, t, inv, dot, dy, h, ds, w);
   }
   if constexpr (kRows > 1) {
 #pragma unroll
@@ -709,6 +724,100 @@ __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardAr
   }
 }
 
+// dx and dweight apart, in one launch without a workspace: the first `col_blocks`
+// blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
+// and the others make the dx of their row groups.
+template <int TYPE, bool DSUM, int TPR, int C>
+__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backward_apart_kernel(
+    NormBackwardArgs k, unsigned col_blocks) {
+  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
+  constexpr int kRows = kBlock / TPR;
+  constexpr int kWaves = kBlock / 64;
+  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
+  __shared__ float part[kWaves][64];
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+  if (blockIdx.x >= col_blocks) {
+    const uint32_t t = threadIdx.x % TPR;
+    u32x4 w[C];
+    load_weight<TPR>(k.weight, t, cols, w);
+    int turn = 0;
+    const uint64_t stride = uint64_t(gridDim.x - col_blocks) * kRows;
+    for (uint64_t base = uint64_t(blockIdx.x - col_blocks) * kRows; base < k.rows;
+         base += stride, turn ^= 1) {
+      const uint64_t row = base + threadIdx.x / TPR;
+      const bool live = row < k.rows;
+      u32x4 dy[C], h[C], ds[C];
+      load_row<TPR>(k.dy + base * k.ldy, k.ldy, live, t, cols, dy);
+      load_row<TPR>(k.h + base * k.ldh, k.ldh, live, t, cols, h);
+      if constexpr (DSUM) load_row<TPR>(k.dsum + base * k.ldd, k.ldd, live, t, cols, ds);
+      const float inv = live ? k.inv_rms[row] : 0.0f;
+      float dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        float fy[8], fh[8], fw[8];
+        widen8<TYPE>(dy[j], fy);
+        widen8<TYPE>(h[j], fh);
+        widen8<TYPE>(w[j], fw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
+      }
+      uint32_t unused = 0;
+      RowCombine<TPR, kRows>::run(dot, unused, lds, turn);
+      if (live) store_grads<TYPE, DSUM, false, TPR>(k, row, t, inv, dot, dy, h, ds, w);
+    }
+    return;
+  }
+  // 8 lanes take a row's 64 columns, 8 rows to a wavefront; rows in steps of the
+  // block's, four in flight
+  const uint32_t c = blockIdx.x * 8 + (threadIdx.x & 7);
+  const bool whole = (blockIdx.x + 1) * 64 <= cols;   // the same for the block
+  constexpr uint32_t kStep = kBlock / 8;
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](u32x4 y, u32x4 x, float inv) __attribute__((always_inline)) {
+    float fy[8], fh[8];
+    widen8<TYPE>(y, fy);
+    widen8<TYPE>(x, fh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(fy[i], fh[i] * inv, acc[i]);
+  };
+  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += 4 * kStep) {
+    u32x4 y[4], x[4];
+    float inv[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // a row past the last is read as this thread's first, and not added
+      const uint64_t rq = r + q * kStep < k.rows ? r + q * kStep : r;
+      inv[q] = k.inv_rms[rq];
+      if (whole) {
+        y[q] = *reinterpret_cast<const u32x4*>(k.dy + rq * k.ldy + uint64_t(c) * 8);
+        x[q] = *reinterpret_cast<const u32x4*>(k.h + rq * k.ldh + uint64_t(c) * 8);
+      } else {
+        y[q] = c < chunks ? load_chunk8(k.dy + rq * k.ldy, c, cols) : u32x4{0, 0, 0, 0};
+        x[q] = c < chunks ? load_chunk8(k.h + rq * k.ldh, c, cols) : u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (r + q * kStep < k.rows) add(y[q], x[q], inv[q]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {   // over the wavefront's 8 rows: lanes 8, 16 and 32 apart
+    float v = acc[i];
+    v += dpp<kDppRor8>(v);
+    v = add_xor16(v);
+    v = add_xor32(v);
+    if (lane_id() < 8) part[wave_id()][lane_id() * 8 + i] = v;
+  }
+  __syncthreads();
+  const uint32_t e = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && e < cols) {
+    float v = part[0][threadIdx.x];
+#pragma unroll
+    for (int q = 1; q < kWaves; ++q) v += part[q][threadIdx.x];
+    k.dweight[e] = v;
+  }
+}
+
 // dweight[c] = the sum of the blocks' partial sums: 4 consecutive columns per
 // thread, kJoinParts threads of a block sharing the partial sums of its columns
 // (part t takes t, t + kJoinParts, ..., eight loads in flight), whose sums are
@@ -745,27 +854,50 @@ __global__ __launch_bounds__(kJoinCols / 4 * kJoinParts) void norm_join_kernel(
   }
 }
 
+// Whether two matrices of a call may share memory (their extents meet).
+bool meet(const void* a, uint64_t lda, const void* b, uint64_t ldb, uint64_t rows, uint64_t cols) {
+  const char* pa = static_cast<const char*>(a);
+  const char* pb = static_cast<const char*>(b);
+  return pa < pb + 2 * ((rows - 1) * ldb + cols) && pb < pa + 2 * ((rows - 1) * lda + cols);
+}
+
+template <int TYPE, bool DSUM>
+hipError_t launch_backward_apart(const NormBackwardArgs& a, const NormBackwardPlan& plan,
+                                 const armx_config* cfg, hipStream_t stream) {
+  const RowShape s = plan.shape;
+  const void* fn = nullptr;
+#define ARMX_NORM_CASE(T, C)              \
+  if (s.threads == T && s.chunks == C)    \
+    fn = reinterpret_cast<const void*>(&norm_backward_apart_kernel<TYPE, DSUM, T, C>)
+  ARMX_EACH_SHAPE(ARMX_NORM_CASE);
+#undef ARMX_NORM_CASE
+  NormBackwardArgs copy = a;
+  unsigned col_blocks = unsigned((a.cols + 63) / 64);
+  void* args[] = {&copy, &col_blocks};
+  const uint64_t row_blocks = plan.blocks - col_blocks;
+  // dx where dy is: every column's sums before any row's gradient
+  if (!meet(a.dx, a.ldx, a.dy, a.ldy, a.rows, a.cols))
+    return launch_rows_kernel(fn, plan.blocks, plan.block, args, cfg, stream);
+  const hipError_t e =
+      launch_rows_kernel(fn, col_blocks, plan.block, args, cfg, stream, true, false);
+  if (e != hipSuccess) return e;
+  col_blocks = 0;
+  return launch_rows_kernel(fn, row_blocks, plan.block, args, cfg, stream, false, true);
+}
+
 template <int TYPE, bool DSUM>
 hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPlan& plan,
                                  const armx_config* cfg, hipStream_t stream) {
+  if (plan.apart) return launch_backward_apart<TYPE, DSUM>(a, plan, cfg, stream);
   const RowShape s = plan.shape;
   const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
-#define ARMX_NORM_CASE(T, C) \
-  if (s.threads == T && s.chunks == C) \
+#define ARMX_NORM_CASE(T, C)                                                                   \
+  if (s.threads == T && s.chunks == C)                                                         \
     fn = stream_out                                                                            \
              ? reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, true, T, C>)    \
              : reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, false, T, C>)
-  ARMX_NORM_CASE(8, 1);
-  ARMX_NORM_CASE(16, 1);
-  ARMX_NORM_CASE(32, 1);
-  ARMX_NORM_CASE(64, 1);
-  ARMX_NORM_CASE(128, 1);
-  ARMX_NORM_CASE(256, 1);
-  ARMX_NORM_CASE(512, 1);
-  ARMX_NORM_CASE(512, 2);
-  ARMX_NORM_CASE(512, 4);
-  ARMX_NORM_CASE(1024, 4);
+  ARMX_EACH_SHAPE_BELOW_1024(ARMX_NORM_CASE);
 #undef ARMX_NORM_CASE
   if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_backward_loop_kernel<TYPE, DSUM>);
   NormBackwardArgs copy = a;
@@ -781,8 +913,7 @@ hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPl
   void* join_args[] = {&partials, &blocks, &pitch, &cols, &dweight};
   return launch_rows_kernel(reinterpret_cast<const void*>(&norm_join_kernel),
                             (cols + kJoinCols - 1) / kJoinCols, kJoinCols / 4 * kJoinParts,
-                            join_args,
-                            cfg, stream, false, true);
+                            join_args, cfg, stream, false, true);
 }
 
 }  // namespace
@@ -794,6 +925,18 @@ NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) 
   if (rows == 0 || cols == 0) return p;
   const uint64_t per = uint64_t(p.block / p.shape.threads);
   const uint64_t groups = (rows + per - 1) / per;
+  // Few rows: the column blocks read them in at most four rounds, from the caches
+  // (us, partial sums / columns apart: 512 x 1024 8.1 / 5.3, 1024 x 8192 17.9 / 15.9,
+  // 2048 x 4096 16.9 / 16.8, 2048 x 1024 9.6 / 21.7, 1024 x 16384 36.3 / 36.5).
+  // 1024 threads of four chunks each, of any number of rows: their registers do not
+  // hold the partial sums too (512 x 32768 106 / 39).
+  p.apart = (p.shape.chunks > 0 && rows <= 2 * uint64_t(p.block) &&
+             rows * cols <= uint64_t(1) << 23) ||
+            (p.shape.threads == 1024 && p.shape.chunks > 0);
+  if (p.apart) {
+    p.blocks = (cols + 63) / 64 + (groups < kMaxGrid / 2 ? groups : kMaxGrid / 2);
+    return p;
+  }
   // Every block's dweight sums are written and read again, so fewer blocks move
   // less, and too few leave loads unsent.  Measured on MI355X at 1, 2 and 4 blocks
   // of 256 threads per compute unit (us): 8192 x 4096 55.4, 54.3, 61.2; 4096 x 8192

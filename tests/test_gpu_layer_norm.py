@@ -87,7 +87,9 @@ def test_norms_and_codes(cols, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (2, 64), (3, 8), (1000, 64), (4099, 136),
-                                       (513, 2056), (300, 8192), (70000, 16), (33, 33000)])
+                                       (513, 2056), (300, 8192), (70000, 16), (33, 33000),
+                                       (512, 1001), (513, 1024), (1024, 2049), (1025, 4100),
+                                       (1200, 7000), (300, 16384), (520, 16390), (90, 32768)])
 @pytest.mark.parametrize("dsum", [False, True])
 def test_backward(rows, cols, dtype, dsum):
     rng = np.random.default_rng(rows + cols)

@@ -100,12 +100,20 @@ def test_backward_refusals():
 def test_backward_workspace_and_plan():
     assert armx.workspace_bytes(armx.OP_RMS_BACKWARD, 0, 4096) == 0
     assert armx.workspace_bytes(armx.OP_RMS_BACKWARD, 1, 4096) == 0
-    for rows, cols in ((2, 4096), (5000, 100), (8192, 4096), (77, 40000)):
+    # few rows, and rows of 16385 to 32768 values: dweight's columns in blocks of
+    # their own, one launch, no workspace; otherwise every block's partial sums and
+    # a launch that joins them
+    for rows, cols, apart in ((2, 4096, True), (1024, 4096, True), (1025, 4096, False),
+                              (512, 128, True), (513, 128, False), (1024, 8200, False),
+                              (5000, 20000, True), (5000, 100, False), (8192, 4096, False),
+                              (77, 40000, False)):
         p = armx.launch_plan(armx.OP_RMS_BACKWARD, rows, cols)
         pitch = (cols + 63) // 64 * 64
         blocks = p["grid_blocks"]
-        assert p["workspace_bytes"] == (4 * blocks * pitch if blocks > 1 else 0)
-        assert p["launches"] == (2 if blocks > 1 else 1)
+        assert p["workspace_bytes"] == (0 if apart else 4 * blocks * pitch), (rows, cols)
+        assert p["launches"] == (1 if apart else 2)
+        if apart:
+            assert blocks > pitch // 64
         assert p["workspace_bytes"] == armx.workspace_bytes(armx.OP_RMS_BACKWARD, rows, cols)
     with pytest.raises(armx.ArmxError):
         armx.workspace_bytes(armx.OP_RMS_BACKWARD, 4, 64, chain_r=2)
