@@ -320,17 +320,29 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
   }
   u32x4 fa[2][T::kMT], fb[2][T::kNT];
   constexpr int kReads = T::kMT + T::kNT;
+  // Where this lane reads half h of the buffer at `from`; opaque to the compiler, so
+  // that it keeps two addresses and puts the rest into the reads' offsets (left to
+  // itself it adds up an address for every read).
+  struct Place {
+    uint32_t a, b;
+  };
+  auto place = [&](uint32_t from, int h) ARMX_INLINE {
+    Place at{from + at_a[h], from + at_b[h]};
+    asm("" : "+v"(at.a), "+v"(at.b));
+    return at;
+  };
   // read j of half h, in the order in which its products need them
-  auto fetch = [&](uint32_t from, int h, int j) ARMX_INLINE {
+  auto fetch = [&](Place at, int h, int j) ARMX_INLINE {
     if (j < T::kNT)
-      fb[h][j] = lds_read16(from + at_b[h] + j * 4 * kStepK);
+      fb[h][j] = lds_read16(at.b + j * 4 * kStepK);
     else
-      fa[h][j - T::kNT] = lds_read16(from + at_a[h] + (j - T::kNT) * 16 * kStepK);
+      fa[h][j - T::kNT] = lds_read16(at.a + (j - T::kNT) * 16 * kStepK);
   };
   auto fetch_half = [&](uint32_t from, int h) ARMX_INLINE {
+    const Place at = place(from, h);
 #pragma unroll
     for (int j = 0; j < kReads; ++j) {
-      fetch(from, h, j);
+      fetch(at, h, j);
       // in this order: the wait at the loop's head is the stricter of the two
       // orders that reach it
       __builtin_amdgcn_sched_barrier(0);
@@ -361,6 +373,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
       ARMX_INLINE {
     constexpr int kPer = (kLoads + T::kMT - 1) / T::kMT;
     constexpr int kPerR = (kReads + T::kMT - 1) / T::kMT;
+    const Place at = place(from, h);
 #pragma unroll
     for (int i = 0; i < T::kMT; ++i) {
       if constexpr (send.value) {
@@ -370,7 +383,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void matmul_tiled_kernel(Matm
       }
 #pragma unroll
       for (int j = i * kPerR; j < (i + 1) * kPerR; ++j)
-        if (j < kReads) fetch(from, h, j);
+        if (j < kReads) fetch(at, h, j);
       __builtin_amdgcn_sched_barrier(0);
       multiply_row(1 - h, i);
       __builtin_amdgcn_sched_barrier(0);
