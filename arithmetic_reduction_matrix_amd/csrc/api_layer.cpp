@@ -15,7 +15,7 @@
 namespace {
 
 constexpr uint64_t kMaxElements = uint64_t(1) << 40;
-constexpr uint64_t kMaxCols = uint64_t(1) << 31;     // exclusive
+constexpr uint64_t kMaxCols = uint64_t(1) << 30;     // exclusive: 32-bit byte offsets
 constexpr uint64_t kMaxProductK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr uint64_t kMaxProductLd = uint64_t(1) << 23;
 constexpr uint64_t kMaxProductRows = uint64_t(1) << 30;

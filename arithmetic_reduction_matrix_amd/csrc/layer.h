@@ -14,17 +14,18 @@ namespace armx {
 // 16-byte loads: 8 values of a 16-bit type.
 constexpr uint32_t kRowVec = 8;
 
-// How a row of `cols` values lies on threads: `threads` per row, each with
-// `chunks` 16-byte loads in registers (chunk j of thread t is the row's chunk
-// j * threads + t).  chunks 0: the row does not fit, and is walked in a loop,
-// twice.  A function of cols only, so a row's bits depend on nothing else.
+// How a row of `cols` values lies on threads: `threads` per row (8, 16, 32, or
+// whole wavefronts), each with `chunks` 16-byte loads in registers (chunk j of
+// thread t is the row's chunk j * threads + t).  chunks 0: the row does not fit,
+// and is walked in a loop, twice.  A function of cols only, so a row's bits depend
+// on nothing else.
 struct RowShape {
   int threads;
   int chunks;
 };
 
 RowShape row_shape(uint64_t cols);
-constexpr int kRowBlock = 256;  // threads per block of rows of at most that many
+constexpr int kRowBlock = 256;  // threads per block of rows of at most a wavefront
 
 // Results of at least this many values are written past the caches: they are more
 // than the 32 MiB of L2 would keep for a reader, and written so they take less of
@@ -55,7 +56,7 @@ struct NormBackwardArgs {
   const uint16_t* dsum = nullptr;  // may be null
   uint16_t* dx = nullptr;
   float* dweight = nullptr;
-  float* partials = nullptr;  // blocks x pitch, when there is more than one block
+  float* partials = nullptr;  // blocks x pitch, when the plan has a workspace
   uint64_t rows = 0, cols = 0;
   uint64_t ldy = 0, ldh = 0, ldd = 0, ldx = 0;
   int type = ARMX_F16;

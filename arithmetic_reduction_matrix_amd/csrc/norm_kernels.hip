@@ -15,19 +15,17 @@
 
 namespace armx {
 
+// Whole wavefronts for rows of more than 64 chunks, no more of them than hold the
+// row: idle ones keep loads from being in flight (codes of 13421 x 2500 on 512
+// threads per row 31.2 us, on 320 25.0).
 RowShape row_shape(uint64_t cols) {
   const uint64_t n = (cols + kRowVec - 1) / kRowVec;  // 16-byte chunks
   if (n <= 8) return {8, 1};
   if (n <= 16) return {16, 1};
   if (n <= 32) return {32, 1};
-  if (n <= 64) return {64, 1};
-  if (n <= 128) return {128, 1};
-  if (n <= 256) return {256, 1};
-  if (n <= 512) return {512, 1};
-  if (n <= 1024) return {512, 2};
-  if (n <= 2048) return {512, 4};
-  if (n <= 4096) return {1024, 4};
-  return {1024, 0};
+  if (n > 4096) return {1024, 0};
+  const int chunks = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+  return {int((n + 64 * chunks - 1) / (64 * chunks)) * 64, chunks};
 }
 
 namespace {
@@ -120,7 +118,7 @@ __device__ __forceinline__ void store_codes8(int8_t* row, uint32_t c, uint32_t c
 // loads of a row's chunks stand in no branch and are all in flight together (a
 // branch around a load makes the compiler wait where its paths join: 37 rows of
 // 5001 values, norm to codes, 6.8 -> 6.6 us).  With an odd count the last word
-// holds one value past the row; trim() clears it.
+// holds one value past the row (trim).
 constexpr int kRawBuffer = 0x00020000;
 struct RowWords {
   __amdgpu_buffer_rsrc_t rs;
@@ -133,16 +131,36 @@ struct RowWords {
   }
 };
 
-// Applied where the values are used: it waits for them, and at the loads it would
-// hold up those behind (48643 x 313 backward, rows read ahead: 66 against 37 us).
-template <int TPR, int C>
-__device__ __forceinline__ void trim(uint32_t t, uint32_t cols, u32x4 (&v)[C]) {
-  if (cols % 2 == 0) return;
+// How a row lies on a block.  TPR > 0: TPR lanes of a wavefront share a row (8 to
+// 64, one chunk each), a block of 256 threads has several rows.  TPR 0: the whole
+// block shares one, C chunks a thread, at most MAXT threads.
+template <int TPR, int MAXT, int C>
+struct Lay {
+  static constexpr int kTpr = TPR;
+  static constexpr int kMax = TPR ? kRowBlock : MAXT;
+  static constexpr int kRows = TPR ? kRowBlock / TPR : 1;   // rows at a time
+  static constexpr int kChunks = C;
+  __device__ __forceinline__ static uint32_t threads() { return TPR ? TPR : blockDim.x; }
+  __device__ __forceinline__ static uint32_t lane() {
+    return TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
+  }
+  __device__ __forceinline__ static uint32_t row() { return TPR ? threadIdx.x / (TPR ? TPR : 1) : 0; }
+};
+
+// Clears what a load brought of values past the row.  Applied where the values are
+// used: it waits for them, and at the loads it would hold up those behind (48643 x
+// 313 backward, rows read ahead: 66 against 37 us).
+template <class L, int C>
+__device__ __forceinline__ void trim(uint32_t cols, u32x4 (&v)[C]) {
+  // rows of one wavefront or more are cut at whole words by the range check
+  if (cols % (L::kTpr && L::kTpr < 64 ? 8 : 2) == 0) return;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((j * TPR + t) * 8 + 2 * i + 1 == cols) v[j][i] &= 0xFFFFu;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t e = (j * L::threads() + L::lane()) * 8 + 2 * i;   // the word's first value
+      v[j][i] &= e >= cols ? 0u : e + 1 == cols ? 0xFFFFu : 0xFFFFFFFFu;
+    }
   }
 }
 
@@ -175,35 +193,37 @@ __device__ __forceinline__ uint32_t lane_max(uint32_t v, int levels) {
 constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 
 // The row's sum of squares and largest magnitude (bits), in each of its
-// threads.  TPR > 64: over the row's wavefronts through LDS, added in wavefront
-// order by every thread alike; the block's ROWS rows each have a place.
-template <int TPR, int ROWS>
+// threads: across lanes, and for a row of several wavefronts through LDS, added in
+// wavefront order by every thread alike.
+template <class L>
 struct RowCombine {
-  static constexpr int kWaves = TPR > 64 ? TPR / 64 : 1;
+  static constexpr int kWaves = L::kTpr ? 1 : L::kMax / 64;
   struct Lds {
-    float s[ROWS][kWaves];
-    uint32_t m[ROWS][kWaves];
+    float s[kWaves];
+    uint32_t m[kWaves];
   };
   // `turn` alternates between the two halves of `lds` from row to row, so one
   // barrier per row is enough
   __device__ __forceinline__ static void run(float& s, uint32_t& m, Lds* lds, int turn) {
-    constexpr int levels = log2_of(TPR > 64 ? 64 : TPR);
+    constexpr int levels = log2_of(L::kTpr ? L::kTpr : 64);
     s = lane_tree(s, levels);
     m = lane_max(m, levels);
-    if constexpr (TPR > 64) {
+    if constexpr (L::kTpr == 0) {
       Lds& l = lds[turn];
-      const int row = wave_id() / kWaves;
       if (lane_id() == 0) {
-        l.s[row][wave_id() % kWaves] = s;
-        l.m[row][wave_id() % kWaves] = m;
+        l.s[wave_id()] = s;
+        l.m[wave_id()] = m;
       }
       __syncthreads();
-      s = 0.0f;
-      m = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        s += l.s[row][w];
-        m = max_u32(m, l.m[row][w]);
+      s = l.s[0];
+      m = l.m[0];
+      // (a lane per wavefront and a tree instead: norm to codes of 3728 x 9000 50.0 ->
+      // 63.2 us)
+      const int waves = num_waves();
+#pragma unroll 4
+      for (int w = 1; w < waves; ++w) {
+        s += l.s[w];
+        m = max_u32(m, l.m[w]);
       }
     }
   }
@@ -326,35 +346,44 @@ __device__ __forceinline__ u32x4 load_sum(const uint16_t* xr, const uint16_t* rr
   return sum8<TYPE>(x, load_chunk8(rr, c, cols));
 }
 
-// Chunks t, t + TPR, ... of a row that TPR threads share, to be trimmed: p is the
-// first row of the block's, ld its pitch, `live` whether this thread's row exists.
-template <int TPR, int C>
-__device__ __forceinline__ void load_row(const uint16_t* p, uint64_t ld, bool live, uint32_t t,
+// The chunks that a thread holds of its row, to be trimmed: p is the first row of
+// the block's, ld their pitch (narrow rows: below kNarrowMaxLd), `rows` how many
+// there are from it on.
+template <class L, int C>
+__device__ __forceinline__ void load_row(const uint16_t* p, uint64_t ld, uint64_t rows,
                                          uint32_t cols, u32x4 (&v)[C]) {
-  if constexpr (TPR >= 64) {
-    const uint64_t r = uint64_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x / TPR)));
-    const uint32_t count = __builtin_amdgcn_readfirstlane(live ? int(cols) : 0);
-    const RowWords row(p + (count ? r * ld : 0), count);
+  const uint32_t t = L::lane();
+  if constexpr (L::kTpr == 0 || L::kTpr == 64) {
+    const uint64_t r = L::kTpr ? uint64_t(wave_id()) : 0;
+    const bool live = r < rows;
+    const RowWords row(p + (live ? r * ld : 0), live ? cols : 0);
 #pragma unroll
-    for (int j = 0; j < C; ++j) v[j] = row.load(j * TPR + t);
+    for (int j = 0; j < C; ++j) v[j] = row.load(j * L::threads() + t);
   } else {
-    const uint32_t chunks = (cols + 7) / 8;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      v[j] = u32x4{0, 0, 0, 0};
-      if (live && j * TPR + t < chunks)
-        v[j] = load_chunk8(p + (threadIdx.x / TPR) * ld, j * TPR + t, cols);
-    }
+    static_assert(C == 1, "a narrow row has a chunk per lane");
+    constexpr uint32_t kRows = 64 / (L::kTpr ? L::kTpr : 1);   // a wavefront's
+    const uint64_t first = uint64_t(wave_id()) * kRows;
+    const uint64_t left = first < rows ? rows - first : 0;
+    const uint32_t live = uint32_t(left < kRows ? left : kRows);
+    const uint32_t rr = L::row() % kRows;
+    const bool in = rr < live && t * 8 < cols;
+    // the wavefront's rows as one range-checked buffer; what a chunk takes of the
+    // pitch behind its row is trimmed
+    const uint32_t bytes =
+        live ? uint32_t((live - 1) * uint32_t(ld) * 2 + (cols + 1) / 2 * 4) : 0u;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p + (live ? first * ld : 0)), 0, int(bytes), kRawBuffer);
+    const uint32_t off = in ? rr * uint32_t(ld) * 2 + t * 16 : 0xFFFFFFF0u;
+    v[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
   }
 }
 
 // The weight's chunks of a thread, to be trimmed.
-template <int TPR, int C>
-__device__ __forceinline__ void load_weight(const uint16_t* w, uint32_t t, uint32_t cols,
-                                            u32x4 (&v)[C]) {
+template <class L, int C>
+__device__ __forceinline__ void load_weight(const uint16_t* w, uint32_t cols, u32x4 (&v)[C]) {
   const RowWords row(w, cols);
 #pragma unroll
-  for (int j = 0; j < C; ++j) v[j] = row.load(j * TPR + t);
+  for (int j = 0; j < C; ++j) v[j] = row.load(j * L::threads() + L::lane());
 }
 
 // A chunk's share of the sum of squares and of the largest |p|.
@@ -413,54 +442,51 @@ __device__ __forceinline__ void finish_row(const NormArgs& k, uint64_t row, floa
   }
 }
 
-// Rows in registers: TPR threads per row, C chunks each; a block of at least
-// kRowBlock threads takes block / TPR rows at a time.
-template <int TYPE, int OUT, bool RES, bool STREAM, int TPR, int C>
-__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel(NormArgs k) {
-  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
-  constexpr int kRows = kBlock / TPR;
-  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
-  const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
-  const uint32_t chunks = (cols + 7) / 8;
+// Rows in registers (Lay).
+template <int TYPE, int OUT, bool RES, bool STREAM, class L>
+__global__ __launch_bounds__(L::kMax) void norm_kernel(NormArgs k) {
+  constexpr int C = L::kChunks;
+  __shared__ typename RowCombine<L>::Lds lds[2];
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   u32x4 w[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) w[j] = u32x4{0, 0, 0, 0};
-  if constexpr (OUT != kOutQuant) load_weight<TPR>(k.weight, t, cols, w);
+  if constexpr (OUT != kOutQuant) load_weight<L>(k.weight, cols, w);
   int turn = 0;
   // every thread of a block makes the same number of rounds (barriers)
-  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows;
-       base += uint64_t(gridDim.x) * kRows, turn ^= 1) {
-    const uint64_t row = base + threadIdx.x / TPR;
+  for (uint64_t base = uint64_t(blockIdx.x) * L::kRows; base < k.rows;
+       base += uint64_t(gridDim.x) * L::kRows, turn ^= 1) {
+    const uint64_t row = base + L::row();
     const bool live = row < k.rows;
     u32x4 h[C];
     float s = 0.0f;
     uint32_t m = 0;
-    load_row<TPR>(k.x + base * k.ldx, k.ldx, live, t, cols, h);
+    load_row<L>(k.x + base * k.ldx, k.ldx, k.rows - base, cols, h);
     if constexpr (RES) {
       u32x4 res[C];
-      load_row<TPR>(k.residual + base * k.ldr, k.ldr, live, t, cols, res);
+      load_row<L>(k.residual + base * k.ldr, k.ldr, k.rows - base, cols, res);
 #pragma unroll
       for (int j = 0; j < C; ++j) h[j] = sum8<TYPE>(h[j], res[j]);
     }
-    trim<TPR>(t, cols, h);
-    if constexpr (OUT != kOutQuant) trim<TPR>(t, cols, w);
+    trim<L>(cols, h);
+    if constexpr (OUT != kOutQuant) trim<L>(cols, w);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
+      const uint32_t c = j * L::threads() + L::lane();
       if (RES && k.sum_out && live && c < chunks)
         store_chunk8<STREAM>(k.sum_out + row * k.lds, c, cols, h[j]);
       measure_chunk<TYPE, OUT>(h[j], w[j], s, m);
     }
-    RowCombine<TPR, kRows>::run(s, m, lds, turn);
+    RowCombine<L>::run(s, m, lds, turn);
     const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
     const CodeScale cs(m);
     if (!live) continue;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
+      const uint32_t c = j * L::threads() + L::lane();
       if (c < chunks) finish_chunk<TYPE, OUT, STREAM>(k, row, c, h[j], w[j], inv, cs);
     }
-    if (t == 0) finish_row<OUT>(k, row, inv, m);
+    if (L::lane() == 0) finish_row<OUT>(k, row, inv, m);
   }
 }
 
@@ -470,7 +496,7 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_kernel
 // where inputs did.
 template <int TYPE, int OUT, bool RES>
 __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
-  __shared__ typename RowCombine<1024, 1>::Lds lds[2];
+  __shared__ typename RowCombine<Lay<0, 1024, 1>>::Lds lds[2];
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   int turn = 0;
   for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x, turn ^= 1) {
@@ -484,7 +510,7 @@ __global__ __launch_bounds__(1024) void norm_loop_kernel(NormArgs k) {
       const u32x4 w = OUT == kOutCodes ? load_chunk8(k.weight, c, cols) : u32x4{0, 0, 0, 0};
       measure_chunk<TYPE, OUT>(h, w, s, m);
     }
-    RowCombine<1024, 1>::run(s, m, lds, turn);
+    RowCombine<Lay<0, 1024, 1>>::run(s, m, lds, turn);
     const float inv = OUT == kOutQuant ? 1.0f : inv_rms_of(s, k.cols, k.eps);
     const CodeScale cs(m);
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
@@ -507,39 +533,60 @@ hipError_t launch_rows_kernel(const void* fn, uint64_t blocks, int threads, void
                        cfg && last ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
 }
 
-#define ARMX_EACH_SHAPE_BELOW_1024(CASE) \
-  CASE(8, 1);                 \
-  CASE(16, 1);                \
-  CASE(32, 1);                \
-  CASE(64, 1);                \
-  CASE(128, 1);               \
-  CASE(256, 1);               \
-  CASE(512, 1);               \
-  CASE(512, 2);               \
-  CASE(512, 4)
-#define ARMX_EACH_SHAPE(CASE)       \
-  ARMX_EACH_SHAPE_BELOW_1024(CASE); \
-  CASE(1024, 4)
+// Calls CASE(Lay) for the layout of shape `s`, if its rows lie in registers.
+#define ARMX_OF_SHAPE(s, CASE)                                                       \
+  do {                                                                               \
+    if ((s).chunks == 1 && (s).threads == 8) CASE(ARMX_LAY(8, 0, 1));                \
+    if ((s).chunks == 1 && (s).threads == 16) CASE(ARMX_LAY(16, 0, 1));              \
+    if ((s).chunks == 1 && (s).threads == 32) CASE(ARMX_LAY(32, 0, 1));              \
+    if ((s).chunks == 1 && (s).threads == 64) CASE(ARMX_LAY(64, 0, 1));              \
+    if ((s).chunks == 1 && (s).threads > 64) CASE(ARMX_LAY(0, 512, 1));              \
+    if ((s).chunks == 2) CASE(ARMX_LAY(0, 512, 2));                                  \
+    if ((s).chunks == 4 && (s).threads <= 512) CASE(ARMX_LAY(0, 512, 4));            \
+  } while (0)
+#define ARMX_LAY(...) Lay<__VA_ARGS__>
+typedef Lay<0, 1024, 4> WidestLay;
+
+// Narrow rows of a larger pitch take a wavefront each: a wavefront's rows, at most
+// 8, are reached by 32-bit offsets.  A row's bits stay the same, the lanes in front
+// adding as before and the others 0.
+constexpr uint64_t kNarrowMaxLd = uint64_t(1) << 27;
+RowShape for_pitch(RowShape s, uint64_t ld) {
+  if (s.threads < 64 && ld >= kNarrowMaxLd) s.threads = 64;
+  return s;
+}
+
+bool is_widest(const RowShape& s) { return s.chunks == 4 && s.threads > 512; }
+
+// Threads of a block and the rows it takes at a time.
+int block_threads(const RowShape& s) { return s.threads > 64 ? s.threads : kRowBlock; }
+uint64_t block_rows(const RowShape& s) { return s.threads > 64 ? 1 : kRowBlock / s.threads; }
 
 template <int TYPE, int OUT, bool RES>
 hipError_t launch_norm_typed(const NormArgs& a, const armx_config* cfg, hipStream_t stream) {
-  const RowShape s = row_shape(a.cols);
+  const RowShape s = for_pitch(row_shape(a.cols), RES && a.ldr > a.ldx ? a.ldr : a.ldx);
   const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
-#define ARMX_NORM_CASE(T, C) \
-  if (s.threads == T && s.chunks == C) \
-    fn = stream_out ? reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, true, T, C>) \
-                    : reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, false, T, C>)
-  ARMX_EACH_SHAPE(ARMX_NORM_CASE);
+#define ARMX_NORM_CASE(...)                                                             \
+  fn = stream_out ? reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, true, __VA_ARGS__>) \
+                  : reinterpret_cast<const void*>(&norm_kernel<TYPE, OUT, RES, false, __VA_ARGS__>)
+  ARMX_OF_SHAPE(s, ARMX_NORM_CASE);
+  if (is_widest(s)) ARMX_NORM_CASE(WidestLay);
 #undef ARMX_NORM_CASE
   if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_loop_kernel<TYPE, OUT, RES>);
-  const int block = s.threads > kRowBlock ? s.threads : kRowBlock;
-  const uint64_t per = uint64_t(block / s.threads);
-  uint64_t blocks = (a.rows + per - 1) / per;
-  if (blocks > kMaxGrid) blocks = kMaxGrid;
+  // One block per row group, the next blocks' loads hiding what one waits for.  Where
+  // codes are all that is written, four times the blocks that fill the card, which
+  // walk on (335544 x 100 27.0 -> 24.6 us, 13421 x 2500 25.0 -> 23.6; with a norm the
+  // other way, its codes 64.6 -> 72.5 and its 16-bit values 79.6 -> 86.2; on longer
+  // rows too, 16384 x 8192 70.1 -> 72.3).
+  uint64_t blocks = (a.rows + block_rows(s) - 1) / block_rows(s);
+  const uint64_t most = OUT == kOutQuant && s.chunks == 1
+                            ? uint64_t(current_cu_count()) * 32 * 256 / block_threads(s)
+                            : kMaxGrid;
+  if (blocks > most) blocks = most;
   NormArgs copy = a;
   void* args[] = {&copy};
-  return launch_rows_kernel(fn, blocks, block, args, cfg, stream);
+  return launch_rows_kernel(fn, blocks, block_threads(s), args, cfg, stream);
 }
 
 template <int TYPE>
@@ -554,44 +601,61 @@ hipError_t launch_norm_out(const NormArgs& a, const armx_config* cfg, hipStream_
 
 // ---- backward ---------------------------------------------------------------------------
 
+// One chunk's share of the row's sum of g h.
+template <int TYPE>
+__device__ __forceinline__ float dot_chunk(u32x4 dy, u32x4 h, u32x4 w, float dot) {
+  float fy[8], fh[8], fw[8];
+  widen8<TYPE>(dy, fy);
+  widen8<TYPE>(h, fh);
+  widen8<TYPE>(w, fw);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
+  return dot;
+}
+
+// dx of a chunk; f = inv^2 mean(g h)
+template <int TYPE, bool DSUM>
+__device__ __forceinline__ u32x4 grad_chunk(u32x4 dy, u32x4 h, u32x4 w, u32x4 ds, float inv,
+                                            float f) {
+  float fy[8], fh[8], fw[8], fd[8];
+  widen8<TYPE>(dy, fy);
+  widen8<TYPE>(h, fh);
+  widen8<TYPE>(w, fw);
+  if constexpr (DSUM) widen8<TYPE>(ds, fd);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
+    if constexpr (DSUM) fy[i] += fd[i];
+  }
+  return narrow8<TYPE>(fy);
+}
+
 // dx of the chunks of a row that a thread holds.
-template <int TYPE, bool DSUM, bool STREAM, int TPR, int C>
-__device__ __forceinline__ void store_grads(const NormBackwardArgs& k, uint64_t row, uint32_t t,
-                                            float inv, float dot, const u32x4 (&dy)[C],
-                                            const u32x4 (&h)[C], const u32x4 (&ds)[C],
-                                            const u32x4 (&w)[C]) {
+template <int TYPE, bool DSUM, bool STREAM, class L, int C>
+__device__ __forceinline__ void store_grads(const NormBackwardArgs& k, uint64_t row, float inv,
+                                            float dot, const u32x4 (&dy)[C], const u32x4 (&h)[C],
+                                            const u32x4 (&ds)[C], const u32x4 (&w)[C]) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   const float f = inv * inv * (dot / float(k.cols));
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const uint32_t c = j * TPR + t;
-    if (c >= chunks) continue;
-    float fy[8], fh[8], fw[8], fd[8];
-    widen8<TYPE>(dy[j], fy);
-    widen8<TYPE>(h[j], fh);
-    widen8<TYPE>(w[j], fw);
-    if constexpr (DSUM) widen8<TYPE>(ds[j], fd);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
-      if constexpr (DSUM) fy[i] += fd[i];
-    }
-    store_chunk8<STREAM>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
+    const uint32_t c = j * L::threads() + L::lane();
+    if (c < chunks)
+      store_chunk8<STREAM>(k.dx + row * k.ldx, c, cols,
+                           grad_chunk<TYPE, DSUM>(dy[j], h[j], w[j], ds[j], inv, f));
   }
 }
 
 // Block b takes the row groups b, b + blocks, ...; every thread keeps the
 // dweight sums of its own columns in registers over the block's rows.  A block
 // of several rows at a time adds its row groups' sums through LDS, in order.
-template <int TYPE, bool DSUM, bool STREAM, int TPR, int C>
-__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backward_kernel(
-    NormBackwardArgs k, float* dst, uint64_t pitch) {
-  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
-  constexpr int kRows = kBlock / TPR;
-  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
-  __shared__ float part[kRows > 1 ? kRows * TPR * C * 8 : 1];
-  const uint32_t t = threadIdx.x % TPR, cols = uint32_t(k.cols);
-  const uint32_t chunks = (cols + 7) / 8;
+template <int TYPE, bool DSUM, bool STREAM, class L>
+__global__ __launch_bounds__(L::kMax) void norm_backward_kernel(NormBackwardArgs k, float* dst,
+                                                               uint64_t pitch) {
+  constexpr int C = L::kChunks;
+  __shared__ typename RowCombine<L>::Lds lds[2];
+  __shared__ float part[L::kRows > 1 ? kRowBlock * 8 : 1];
+  const uint32_t cols = uint32_t(k.cols);
   u32x4 w[C];
   float acc[C][8];
 #pragma unroll
@@ -599,31 +663,30 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
   }
-  load_weight<TPR>(k.weight, t, cols, w);
+  load_weight<L>(k.weight, cols, w);
   // One row group's values; with kAhead the next group's are on their way while
-  // this one's are combined (8192 x 4096 56.6 -> 54.3 us; at 512 threads x 4, where
-  // the registers no longer hold both, 62 -> 71).
+  // this one's are combined (8192 x 4096 56.6 -> 54.3 us; at four chunks a thread,
+  // where the registers no longer hold both, 62 -> 71).
   struct Rows {
     u32x4 dy[C], h[C], ds[C];
     float inv;
   };
-  constexpr bool kAhead = TPR * C <= 1024;
+  constexpr bool kAhead = C <= 2;
   auto load = [&](uint64_t base) __attribute__((always_inline)) {
     Rows v;
-    const uint64_t row = base + threadIdx.x / TPR;
-    const bool live = row < k.rows;
-    v.inv = live ? k.inv_rms[row] : 0.0f;
-    load_row<TPR>(k.dy + base * k.ldy, k.ldy, live, t, cols, v.dy);
-    load_row<TPR>(k.h + base * k.ldh, k.ldh, live, t, cols, v.h);
-    if constexpr (DSUM) load_row<TPR>(k.dsum + base * k.ldd, k.ldd, live, t, cols, v.ds);
+    const uint64_t row = base + L::row(), left = k.rows - base;
+    v.inv = row < k.rows ? k.inv_rms[row] : 0.0f;
+    load_row<L>(k.dy + base * k.ldy, k.ldy, left, cols, v.dy);
+    load_row<L>(k.h + base * k.ldh, k.ldh, left, cols, v.h);
+    if constexpr (DSUM) load_row<L>(k.dsum + base * k.ldd, k.ldd, left, cols, v.ds);
     return v;
   };
   int turn = 0;
-  const uint64_t stride = uint64_t(gridDim.x) * kRows;
+  const uint64_t stride = uint64_t(gridDim.x) * L::kRows;
   Rows ahead;
-  if constexpr (kAhead) ahead = load(uint64_t(blockIdx.x) * kRows);
-  for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < k.rows; base += stride, turn ^= 1) {
-    const uint64_t row = base + threadIdx.x / TPR;
+  if constexpr (kAhead) ahead = load(uint64_t(blockIdx.x) * L::kRows);
+  for (uint64_t base = uint64_t(blockIdx.x) * L::kRows; base < k.rows; base += stride, turn ^= 1) {
+    const uint64_t row = base + L::row();
     const bool live = row < k.rows;
     Rows now;
     if constexpr (kAhead) {
@@ -632,46 +695,41 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
     } else {
       now = load(base);
     }
-    trim<TPR>(t, cols, now.dy);
-    trim<TPR>(t, cols, now.h);
-    trim<TPR>(t, cols, w);
-    const u32x4 (&dy)[C] = now.dy, (&h)[C] = now.h, (&ds)[C] = now.ds;
-    const float inv = now.inv;
+    trim<L>(cols, now.dy);
+    trim<L>(cols, now.h);
+    trim<L>(cols, w);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      float fy[8], fh[8], fw[8];
-      widen8<TYPE>(dy[j], fy);
-      widen8<TYPE>(h[j], fh);
-      widen8<TYPE>(w[j], fw);
+      dot = dot_chunk<TYPE>(now.dy[j], now.h[j], w[j], dot);
+      if (live) {
+        float fy[8], fh[8];
+        widen8<TYPE>(now.dy[j], fy);
+        widen8<TYPE>(now.h[j], fh);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
-        if (live) acc[j][i] = __builtin_fmaf(fy[i], fh[i] * inv, acc[j][i]);
+        for (int i = 0; i < 8; ++i) acc[j][i] = __builtin_fmaf(fy[i], fh[i] * now.inv, acc[j][i]);
       }
     }
     uint32_t unused = 0;
-    RowCombine<TPR, kRows>::run(dot, unused, lds, turn);
-    if (!live) continue;
-    store_grads<TYPE, DSUM, STREAM, TPR>(k, row, t, inv, dot, dy, h, ds, w);
+    RowCombine<L>::run(dot, unused, lds, turn);
+    if (live)
+      store_grads<TYPE, DSUM, STREAM, L>(k, row, now.inv, dot, now.dy, now.h, now.ds, w);
   }
-  if constexpr (kRows > 1) {
+  if constexpr (L::kRows > 1) {
+    constexpr uint32_t kPitch = L::kTpr * 8;
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        part[(threadIdx.x / TPR) * (TPR * C * 8) + (j * TPR + t) * 8 + i] = acc[j][i];
+    for (int i = 0; i < 8; ++i) part[L::row() * kPitch + L::lane() * 8 + i] = acc[0][i];
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < cols; e += kBlock) {
+    for (uint32_t e = threadIdx.x; e < cols; e += kRowBlock) {
       float v = part[e];
-      for (int r = 1; r < kRows; ++r) v += part[r * (TPR * C * 8) + e];
+      for (int r = 1; r < L::kRows; ++r) v += part[r * kPitch + e];
       dst[uint64_t(blockIdx.x) * pitch + e] = v;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const uint32_t c = j * TPR + t;
-      float* d = dst + uint64_t(blockIdx.x) * pitch + c * 8;
+      const uint32_t c = j * L::threads() + L::lane();
+      float* d = dst + uint64_t(blockIdx.x) * pitch + uint64_t(c) * 8;
       if (c * 8 + 8 <= cols) {
         reinterpret_cast<floatx4*>(d)[0] = floatx4{acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
         reinterpret_cast<floatx4*>(d)[1] = floatx4{acc[j][4], acc[j][5], acc[j][6], acc[j][7]};
@@ -684,130 +742,47 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
   }
 }
 
-// Rows too long for the registers: two walks per row, the block's dweight sums
-// kept in its own row of `dst` (each thread reads and writes its own columns).
-template <int TYPE, bool DSUM>
-__global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardArgs k, float* dst,
-                                                                  uint64_t pitch) {
-  __shared__ typename RowCombine<1024, 1>::Lds lds[2];
-  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-  float* sums = dst + uint64_t(blockIdx.x) * pitch;
-  for (uint32_t c = threadIdx.x; c < chunks; c += 1024)
-    for (uint32_t i = 0; i < 8; ++i)
-      if (c * 8 + i < cols) sums[c * 8 + i] = 0.0f;
-  int turn = 0;
-  for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x, turn ^= 1) {
-    const uint16_t* yr = k.dy + row * k.ldy;
-    const uint16_t* hr = k.h + row * k.ldh;
-    const float inv = k.inv_rms[row];
-    float dot = 0.0f;
-    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
-      float fy[8], fh[8], fw[8];
-      widen8<TYPE>(load_chunk8(yr, c, cols), fy);
-      widen8<TYPE>(load_chunk8(hr, c, cols), fh);
-      widen8<TYPE>(load_chunk8(k.weight, c, cols), fw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
-    }
-    uint32_t unused = 0;
-    RowCombine<1024, 1>::run(dot, unused, lds, turn);
-    const float f = inv * inv * (dot / float(k.cols));
-    for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
-      float fy[8], fh[8], fw[8], fd[8];
-      widen8<TYPE>(load_chunk8(yr, c, cols), fy);
-      widen8<TYPE>(load_chunk8(hr, c, cols), fh);
-      widen8<TYPE>(load_chunk8(k.weight, c, cols), fw);
-      if constexpr (DSUM) widen8<TYPE>(load_chunk8(k.dsum + row * k.ldd, c, cols), fd);
-      for (uint32_t i = 0; i < 8; ++i)
-        if (c * 8 + i < cols) sums[c * 8 + i] = __builtin_fmaf(fy[i], fh[i] * inv, sums[c * 8 + i]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        fy[i] = inv * (fy[i] * fw[i] - fh[i] * f);
-        if constexpr (DSUM) fy[i] += fd[i];
-      }
-      store_chunk8<false>(k.dx + row * k.ldx, c, cols, narrow8<TYPE>(fy));
-    }
-  }
-}
+// A chunk that starts at any value.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-// dx and dweight apart, in one launch without a workspace: the first `col_blocks`
-// blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
-// and the others make the dx of their row groups.
-template <int TYPE, bool DSUM, int TPR, int C>
-__global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backward_apart_kernel(
-    NormBackwardArgs k, unsigned col_blocks) {
-  constexpr int kBlock = TPR > kRowBlock ? TPR : kRowBlock;
-  constexpr int kRows = kBlock / TPR;
-  constexpr int kWaves = kBlock / 64;
-  __shared__ typename RowCombine<TPR, kRows>::Lds lds[2];
-  __shared__ float part[kWaves][64];
+// dweight over all rows for 64 columns (number `block` of them), by a whole block: 8
+// lanes take a row's 64 columns, 8 rows to a wavefront; rows in steps of the block's,
+// four in flight.  part: 64 floats per wavefront.
+template <int TYPE>
+__device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t block,
+                                            float (*part)[64]) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-  if (blockIdx.x >= col_blocks) {
-    const uint32_t t = threadIdx.x % TPR;
-    u32x4 w[C];
-    load_weight<TPR>(k.weight, t, cols, w);
-    int turn = 0;
-    const uint64_t stride = uint64_t(gridDim.x - col_blocks) * kRows;
-    for (uint64_t base = uint64_t(blockIdx.x - col_blocks) * kRows; base < k.rows;
-         base += stride, turn ^= 1) {
-      const uint64_t row = base + threadIdx.x / TPR;
-      const bool live = row < k.rows;
-      u32x4 dy[C], h[C], ds[C];
-      load_row<TPR>(k.dy + base * k.ldy, k.ldy, live, t, cols, dy);
-      load_row<TPR>(k.h + base * k.ldh, k.ldh, live, t, cols, h);
-      if constexpr (DSUM) load_row<TPR>(k.dsum + base * k.ldd, k.ldd, live, t, cols, ds);
-      const float inv = live ? k.inv_rms[row] : 0.0f;
-      trim<TPR>(t, cols, dy);
-      trim<TPR>(t, cols, h);
-      trim<TPR>(t, cols, w);
-      float dot = 0.0f;
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        float fy[8], fh[8], fw[8];
-        widen8<TYPE>(dy[j], fy);
-        widen8<TYPE>(h[j], fh);
-        widen8<TYPE>(w[j], fw);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(fy[i] * fw[i], fh[i], dot);
-      }
-      uint32_t unused = 0;
-      RowCombine<TPR, kRows>::run(dot, unused, lds, turn);
-      if (live) store_grads<TYPE, DSUM, false, TPR>(k, row, t, inv, dot, dy, h, ds, w);
-    }
-    return;
-  }
-  // 8 lanes take a row's 64 columns, 8 rows to a wavefront; rows in steps of the
-  // block's, four in flight
-  const uint32_t c = blockIdx.x * 8 + (threadIdx.x & 7);
-  const bool whole = (blockIdx.x + 1) * 64 <= cols;   // the same for the block
-  constexpr uint32_t kStep = kBlock / 8;
+  const uint32_t c = block * 8 + (threadIdx.x & 7);
+  // The last chunk is read as the row's last 8 values, without a branch (a lane with
+  // none too); those in front of the chunk are the lane's before it.
+  const uint32_t e0 = c * 8 + 8 <= cols ? c * 8 : cols - 8;
+  const uint32_t step = blockDim.x / 8;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](u32x4 y, u32x4 x, float inv) __attribute__((always_inline)) {
-    float fy[8], fh[8];
-    widen8<TYPE>(y, fy);
-    widen8<TYPE>(x, fh);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(fy[i], fh[i] * inv, acc[i]);
-  };
-  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += 4 * kStep) {
+  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += 4 * step) {
     u32x4 y[4], x[4];
     float inv[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       // a row past the last is read as this thread's first, and not added
-      const uint64_t rq = r + q * kStep < k.rows ? r + q * kStep : r;
+      const uint64_t rq = r + q * step < k.rows ? r + q * step : r;
       inv[q] = k.inv_rms[rq];
-      if (whole) {
-        y[q] = *reinterpret_cast<const u32x4*>(k.dy + rq * k.ldy + uint64_t(c) * 8);
-        x[q] = *reinterpret_cast<const u32x4*>(k.h + rq * k.ldh + uint64_t(c) * 8);
+      if (cols >= 8) {
+        y[q] = *reinterpret_cast<const u32x4_any*>(k.dy + rq * k.ldy + e0);
+        x[q] = *reinterpret_cast<const u32x4_any*>(k.h + rq * k.ldh + e0);
       } else {
-        y[q] = c < chunks ? load_chunk8(k.dy + rq * k.ldy, c, cols) : u32x4{0, 0, 0, 0};
-        x[q] = c < chunks ? load_chunk8(k.h + rq * k.ldh, c, cols) : u32x4{0, 0, 0, 0};
+        y[q] = c == 0 ? load_chunk8(k.dy + rq * k.ldy, 0, cols) : u32x4{0, 0, 0, 0};
+        x[q] = c == 0 ? load_chunk8(k.h + rq * k.ldh, 0, cols) : u32x4{0, 0, 0, 0};
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (r + q * kStep < k.rows) add(y[q], x[q], inv[q]);
+    for (int q = 0; q < 4; ++q) {
+      if (r + q * step >= k.rows) continue;
+      float fy[8], fh[8];
+      widen8<TYPE>(y[q], fy);
+      widen8<TYPE>(x[q], fh);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(fy[i], fh[i] * inv[q], acc[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {   // over the wavefront's 8 rows: lanes 8, 16 and 32 apart
@@ -815,15 +790,125 @@ __global__ __launch_bounds__(TPR > kRowBlock ? TPR : kRowBlock) void norm_backwa
     v += dpp<kDppRor8>(v);
     v = add_xor16(v);
     v = add_xor32(v);
-    if (lane_id() < 8) part[wave_id()][lane_id() * 8 + i] = v;
+    const uint32_t e = (cols >= 8 ? e0 : c * 8) + i;
+    if (lane_id() < 8 && c < chunks && e >= c * 8) part[wave_id()][e - block * 64] = v;
   }
   __syncthreads();
-  const uint32_t e = blockIdx.x * 64 + threadIdx.x;
+  const uint32_t e = block * 64 + threadIdx.x;
   if (threadIdx.x < 64 && e < cols) {
     float v = part[0][threadIdx.x];
-#pragma unroll
-    for (int q = 1; q < kWaves; ++q) v += part[q][threadIdx.x];
+    const int waves = num_waves();
+    for (int q = 1; q < waves; ++q) v += part[q][threadIdx.x];
     k.dweight[e] = v;
+  }
+}
+
+// dx and dweight apart, in one launch without a workspace: the first `col_blocks`
+// blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
+// and the others make the dx of their row groups.
+template <int TYPE, bool DSUM, class L>
+__global__ __launch_bounds__(L::kMax) void norm_backward_apart_kernel(NormBackwardArgs k,
+                                                                     unsigned col_blocks) {
+  constexpr int C = L::kChunks;
+  __shared__ typename RowCombine<L>::Lds lds[2];
+  __shared__ float part[L::kMax / 64][64];
+  if (blockIdx.x < col_blocks) {
+    sum_columns<TYPE>(k, blockIdx.x, part);
+    return;
+  }
+  const uint32_t cols = uint32_t(k.cols);
+  u32x4 w[C];
+  load_weight<L>(k.weight, cols, w);
+  int turn = 0;
+  const uint64_t stride = uint64_t(gridDim.x - col_blocks) * L::kRows;
+  for (uint64_t base = uint64_t(blockIdx.x - col_blocks) * L::kRows; base < k.rows;
+       base += stride, turn ^= 1) {
+    const uint64_t row = base + L::row(), left = k.rows - base;
+    const bool live = row < k.rows;
+    u32x4 dy[C], h[C], ds[C];
+    load_row<L>(k.dy + base * k.ldy, k.ldy, left, cols, dy);
+    load_row<L>(k.h + base * k.ldh, k.ldh, left, cols, h);
+    if constexpr (DSUM && C < 4) load_row<L>(k.dsum + base * k.ldd, k.ldd, left, cols, ds);
+    const float inv = live ? k.inv_rms[row] : 0.0f;
+    trim<L>(cols, dy);
+    trim<L>(cols, h);
+    trim<L>(cols, w);
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) dot = dot_chunk<TYPE>(dy[j], h[j], w[j], dot);
+    uint32_t unused = 0;
+    // the registers do not hold dsum's four chunks during the sums above (16-bit dx of
+    // 1677 x 20000 96.5 -> 92.7 us)
+    if constexpr (DSUM && C == 4) load_row<L>(k.dsum + base * k.ldd, k.ldd, left, cols, ds);
+    RowCombine<L>::run(dot, unused, lds, turn);
+    if (live) store_grads<TYPE, DSUM, false, L>(k, row, inv, dot, dy, h, ds, w);
+  }
+}
+
+// The same for rows too long for the registers, which are walked twice, four chunks
+// a thread at a time.
+template <int TYPE, bool DSUM>
+__global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardArgs k,
+                                                                  unsigned col_blocks) {
+  typedef Lay<0, 1024, 4> L;
+  __shared__ typename RowCombine<L>::Lds lds[2];
+  __shared__ float part[16][64];
+  if (blockIdx.x < col_blocks) {
+    sum_columns<TYPE>(k, blockIdx.x, part);
+    return;
+  }
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+  const RowWords wr(k.weight, cols);
+  // a whole row's loads of one chunk; values past the row cleared
+  auto cut = [&](u32x4 v, uint32_t c) __attribute__((always_inline)) {
+    if (cols & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c * 8 + 2 * i + 1 == cols) v[i] &= 0xFFFFu;
+    }
+    return v;
+  };
+  int turn = 0;
+  for (uint64_t row = blockIdx.x - col_blocks; row < k.rows;
+       row += gridDim.x - col_blocks, turn ^= 1) {
+    const RowWords yr(k.dy + row * k.ldy, cols), hr(k.h + row * k.ldh, cols);
+    const float inv = k.inv_rms[row];
+    float dot = 0.0f;
+    for (uint32_t c0 = threadIdx.x; c0 < chunks; c0 += 4096) {
+      u32x4 y[4], h[4], w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = yr.load(c0 + j * 1024);
+        h[j] = hr.load(c0 + j * 1024);
+        w[j] = wr.load(c0 + j * 1024);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = c0 + j * 1024;
+        dot = dot_chunk<TYPE>(cut(y[j], c), cut(h[j], c), cut(w[j], c), dot);
+      }
+    }
+    uint32_t unused = 0;
+    RowCombine<L>::run(dot, unused, lds, turn);
+    const float f = inv * inv * (dot / float(k.cols));
+    const RowWords dr(DSUM ? k.dsum + row * k.ldd : nullptr, DSUM ? cols : 0);
+    for (uint32_t c0 = threadIdx.x; c0 < chunks; c0 += 4096) {
+      u32x4 y[4], h[4], w[4], d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = yr.load(c0 + j * 1024);
+        h[j] = hr.load(c0 + j * 1024);
+        w[j] = wr.load(c0 + j * 1024);
+        if constexpr (DSUM) d[j] = dr.load(c0 + j * 1024);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = c0 + j * 1024;
+        if (c < chunks)
+          store_chunk8<false>(k.dx + row * k.ldx, c, cols,
+                              grad_chunk<TYPE, DSUM>(y[j], h[j], w[j], d[j], inv, f));
+      }
+    }
   }
 }
 
@@ -870,16 +955,23 @@ bool meet(const void* a, uint64_t lda, const void* b, uint64_t ldb, uint64_t row
   return pa < pb + 2 * ((rows - 1) * ldb + cols) && pb < pa + 2 * ((rows - 1) * lda + cols);
 }
 
+RowShape backward_shape(const NormBackwardArgs& a, const NormBackwardPlan& plan) {
+  uint64_t ld = a.ldy > a.ldh ? a.ldy : a.ldh;
+  if (a.dsum && a.ldd > ld) ld = a.ldd;
+  return for_pitch(plan.shape, ld);
+}
+
 template <int TYPE, bool DSUM>
 hipError_t launch_backward_apart(const NormBackwardArgs& a, const NormBackwardPlan& plan,
                                  const armx_config* cfg, hipStream_t stream) {
-  const RowShape s = plan.shape;
+  const RowShape s = backward_shape(a, plan);
   const void* fn = nullptr;
-#define ARMX_NORM_CASE(T, C)              \
-  if (s.threads == T && s.chunks == C)    \
-    fn = reinterpret_cast<const void*>(&norm_backward_apart_kernel<TYPE, DSUM, T, C>)
-  ARMX_EACH_SHAPE(ARMX_NORM_CASE);
+#define ARMX_NORM_CASE(...) \
+  fn = reinterpret_cast<const void*>(&norm_backward_apart_kernel<TYPE, DSUM, __VA_ARGS__>)
+  ARMX_OF_SHAPE(s, ARMX_NORM_CASE);
+  if (is_widest(s)) ARMX_NORM_CASE(WidestLay);
 #undef ARMX_NORM_CASE
+  if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_backward_loop_kernel<TYPE, DSUM>);
   NormBackwardArgs copy = a;
   unsigned col_blocks = unsigned((a.cols + 63) / 64);
   void* args[] = {&copy, &col_blocks};
@@ -898,24 +990,21 @@ template <int TYPE, bool DSUM>
 hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPlan& plan,
                                  const armx_config* cfg, hipStream_t stream) {
   if (plan.apart) return launch_backward_apart<TYPE, DSUM>(a, plan, cfg, stream);
-  const RowShape s = plan.shape;
+  const RowShape s = backward_shape(a, plan);
   const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
-#define ARMX_NORM_CASE(T, C)                                                                   \
-  if (s.threads == T && s.chunks == C)                                                         \
-    fn = stream_out                                                                            \
-             ? reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, true, T, C>)    \
-             : reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, false, T, C>)
-  ARMX_EACH_SHAPE_BELOW_1024(ARMX_NORM_CASE);
+#define ARMX_NORM_CASE(...)                                                                    \
+  fn = stream_out                                                                              \
+           ? reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, true, __VA_ARGS__>) \
+           : reinterpret_cast<const void*>(&norm_backward_kernel<TYPE, DSUM, false, __VA_ARGS__>)
+  ARMX_OF_SHAPE(s, ARMX_NORM_CASE);
 #undef ARMX_NORM_CASE
-  if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_backward_loop_kernel<TYPE, DSUM>);
   NormBackwardArgs copy = a;
-  const bool join = plan.blocks > 1;
-  float* dst = join ? a.partials : a.dweight;
-  uint64_t pitch = join ? plan.pitch : 0;
+  float* dst = a.partials;
+  uint64_t pitch = plan.pitch;
   void* args[] = {&copy, &dst, &pitch};
-  hipError_t e = launch_rows_kernel(fn, plan.blocks, plan.block, args, cfg, stream, true, !join);
-  if (e != hipSuccess || !join) return e;
+  hipError_t e = launch_rows_kernel(fn, plan.blocks, plan.block, args, cfg, stream, true, false);
+  if (e != hipSuccess) return e;
   const float* partials = a.partials;
   uint64_t blocks = plan.blocks, cols = a.cols;
   float* dweight = a.dweight;
@@ -930,30 +1019,28 @@ hipError_t launch_backward_typed(const NormBackwardArgs& a, const NormBackwardPl
 NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) {
   NormBackwardPlan p;
   p.shape = row_shape(cols);
-  p.block = p.shape.threads > kRowBlock ? p.shape.threads : kRowBlock;
+  p.block = block_threads(p.shape);
   if (rows == 0 || cols == 0) return p;
-  const uint64_t per = uint64_t(p.block / p.shape.threads);
-  const uint64_t groups = (rows + per - 1) / per;
+  const uint64_t groups = (rows + block_rows(p.shape) - 1) / block_rows(p.shape);
   // Few rows: the column blocks read them in at most four rounds, from the caches
   // (us, partial sums / columns apart: 512 x 1024 8.1 / 5.3, 1024 x 8192 17.9 / 15.9,
   // 2048 x 4096 16.9 / 16.8, 2048 x 1024 9.6 / 21.7, 1024 x 16384 36.3 / 36.5).
-  // 1024 threads of four chunks each, of any number of rows: their registers do not
-  // hold the partial sums too (512 x 32768 106 / 39).
-  p.apart = (p.shape.chunks > 0 && rows <= 2 * uint64_t(p.block) &&
-             rows * cols <= uint64_t(1) << 23) ||
-            (p.shape.threads == 1024 && p.shape.chunks > 0);
+  // Rows of more than 16384 values, however many: the registers do not hold the
+  // partial sums too (512 x 32768 106 / 39, 559 x 60001 294 / 104).
+  p.apart = (rows <= 2 * uint64_t(p.block) && rows * cols <= uint64_t(1) << 23) ||
+            is_widest(p.shape) || p.shape.chunks == 0;
   if (p.apart) {
     p.blocks = (cols + 63) / 64 + (groups < kMaxGrid / 2 ? groups : kMaxGrid / 2);
     return p;
   }
   // Every block's dweight sums are written and read again, so fewer blocks move
-  // less, and too few leave loads unsent.  Measured on MI355X at 1, 2 and 4 blocks
-  // of 256 threads per compute unit (us): 8192 x 4096 55.4, 54.3, 61.2; 4096 x 8192
-  // 54.9, 58.9, 69.0; 32768 x 128 11.6, 10.7, 11.7.
-  const uint64_t most = uint64_t(cu_count) * (cols <= 2048 ? 2 : 1);
+  // less, and too few leave loads unsent: about 8 wavefronts per compute unit.
+  // Measured on MI355X at 4, 8 and 16 of them (us): 8192 x 4096 55.4, 54.3, 61.2;
+  // 32768 x 128 11.6, 10.7, 11.7.
+  const uint64_t most = uint64_t(cu_count) * ((511 + p.block) / p.block);
   p.blocks = groups < most ? groups : most;
   p.pitch = (cols + 63) / 64 * 64;
-  if (p.blocks > 1) p.ws_bytes = size_t(p.blocks * p.pitch * sizeof(float));
+  p.ws_bytes = size_t(p.blocks * p.pitch * sizeof(float));
   return p;
 }
 

@@ -388,8 +388,9 @@ int reduce_sum_noalloc(const void* x, size_t n, float* out, const armx_config* c
  *   least the row's length).  Rows of 16-bit values start at multiples of 16
  *   bytes (pointer 16-byte aligned, pitch a multiple of 8 when there is more
  *   than one row); rows of codes too (pitch a multiple of 16).  Pitch padding
- *   is never written; of what follows a row's last value, reads may cover the
- *   rest of its 4-byte word and what matmul_int8 says, and never use it.
+ *   is never written.  Reads may cover it, and of what follows the last row's
+ *   last value the rest of its 4-byte word and what matmul_int8 says; they
+ *   never use it.
  * - `cfg` may give the two events only; every other field must be zero
  *   (ARMX_ERR_CONFIG).
  * - A row's result depends on that row's values (and weight, scales and bias)
@@ -397,7 +398,7 @@ int reduce_sum_noalloc(const void* x, size_t n, float* out, const armx_config* c
  *   stands (batch invariance); dweight, a sum over rows, depends on the row
  *   count and the device's compute-unit count too.  Nothing depends on timing.
  * - Row counts of 0 write nothing.  At most 2^40 elements from a matrix's
- *   first to its last, rows of fewer than 2^31, codes as matmul_int8 says.
+ *   first to its last, rows of fewer than 2^30, codes as matmul_int8 says.
  */
 typedef enum armx_type {
   ARMX_F16 = 0,  /* IEEE binary16 */

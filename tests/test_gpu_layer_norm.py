@@ -52,7 +52,7 @@ def check_codes(q, s, p, inv, rel_inv):
                   <= ((rel_inv + 2 * U) * 1.01 * want_s + 2.0 ** -149)[~np.isnan(want_s)])
 
 
-# every row_shape (8 .. 64 lanes, 2 chunks a lane, 256 x 1, 2, 4, 512 x 4, 1024 x 4, the
+# every row_shape (8 .. 64 lanes; whole wavefronts with 1, 2 or 4 chunks a lane; the
 # loop) at its ends, odd widths among them
 COLS = [1, 7, 8, 63, 64, 65, 128, 129, 250, 256, 257, 511, 512, 513, 1001, 1024, 1025, 2048,
         2049, 2056, 4096, 4097, 5001, 8192, 8193, 16384, 16391, 32768, 32769, 40000, 100003]
@@ -376,3 +376,25 @@ def test_more_than_2_to_the_31_bytes_of_rows():
     # 600 times the same rows; every partial sum is below the total, so
     # (rows + 10) U of it bounds any order
     assert float((d.dweight.double() / 600 / s.dweight.double() - 1).abs().max()) <= 2 * (rows + 10) * U
+
+
+def test_narrow_rows_of_a_pitch_past_32_bit_offsets():
+    # two rows 2^28 bytes apart and more: bits as with the rows side by side
+    cols, pitch = 41, (1 << 27) + 8
+    rng = np.random.default_rng(12)
+    near = [make(rng, 3, cols, torch.bfloat16, device="cuda") for _ in range(3)]
+    hold = torch.zeros(2 * pitch + 192, dtype=torch.bfloat16, device="cuda")
+    x, r, dy = (torch.as_strided(hold, (3, cols), (pitch, 1), 64 * i) for i in range(3))
+    for a, b in zip((x, r, dy), near):
+        a.copy_(b)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(cols)).bfloat16().cuda()
+    far = armx.rms_norm_rows(x, w, residual=r, keep_inv_rms=True)
+    want = armx.rms_norm_rows(near[0], w, residual=near[1], keep_inv_rms=True)
+    for a, b in zip(far, want):
+        assert np.array_equal(bits(a), bits(b))
+    for a, b in zip(armx.rms_norm_rows_int8(x, w, residual=r),
+                    armx.rms_norm_rows_int8(near[0], w, residual=near[1])):
+        assert np.array_equal(bits(a), bits(b))
+    for a, b in zip(armx.rms_norm_rows_backward(dy, x, w, far.inv_rms, dsum=r),
+                    armx.rms_norm_rows_backward(near[2], near[0], w, want.inv_rms, dsum=near[1])):
+        assert np.array_equal(bits(a), bits(b))

@@ -57,7 +57,7 @@ def test_norm_refusals():
         for kw in (dict(type=2), dict(type=-1), dict(eps=-1e-9), dict(eps=NAN),
                    dict(sum=P, lds=64), *(dict(c=cfg(**b)) for b in BAD_CONFIGS)):
             assert f(**kw) == -3, (f, kw)
-        for kw in (dict(ldx=56), dict(ldx=0), dict(cols=1 << 31, rows=1), dict(rows=(1 << 40) + 1),
+        for kw in (dict(ldx=56), dict(ldx=0), dict(cols=1 << 30, rows=1), dict(rows=(1 << 40) + 1),
                    dict(rows=1 << 36), dict(res=P, ldr=56)):
             assert f(**kw) == -5, (f, kw)
         # nothing to do
@@ -92,7 +92,7 @@ def test_backward_refusals():
     need = armx.workspace_bytes(armx.OP_RMS_BACKWARD, 4096, 4096)
     assert need > 0
     assert back(ws_bytes=need - 1, **big) == -4
-    for kw in (dict(ldy=56), dict(ldh=56), dict(ldx=56), dict(ds=P, ldd=56), dict(cols=1 << 31)):
+    for kw in (dict(ldy=56), dict(ldh=56), dict(ldx=56), dict(ds=P, ldd=56), dict(cols=1 << 30)):
         assert back(**kw) == -5, kw
     assert back(cols=0, dy=None, h=None, dx=None, dw=None, w=None, inv=None, ws=None) == 0
 
@@ -100,13 +100,13 @@ def test_backward_refusals():
 def test_backward_workspace_and_plan():
     assert armx.workspace_bytes(armx.OP_RMS_BACKWARD, 0, 4096) == 0
     assert armx.workspace_bytes(armx.OP_RMS_BACKWARD, 1, 4096) == 0
-    # few rows, and rows of 16385 to 32768 values: dweight's columns in blocks of
+    # few rows, and rows of more than 16384 values: dweight's columns in blocks of
     # their own, one launch, no workspace; otherwise every block's partial sums and
     # a launch that joins them
     for rows, cols, apart in ((2, 4096, True), (1024, 4096, True), (1025, 4096, False),
                               (512, 128, True), (513, 128, False), (1024, 8200, False),
                               (5000, 20000, True), (5000, 100, False), (8192, 4096, False),
-                              (77, 40000, False)):
+                              (77, 40000, True), (5000, 40000, True)):
         p = armx.launch_plan(armx.OP_RMS_BACKWARD, rows, cols)
         pitch = (cols + 63) // 64 * 64
         blocks = p["grid_blocks"]
