@@ -19,6 +19,8 @@ constexpr uint64_t kMaxCols = uint64_t(1) << 30;     // exclusive: 32-bit byte o
 constexpr uint64_t kMaxProductK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr uint64_t kMaxProductLd = uint64_t(1) << 23;
 constexpr uint64_t kMaxProductRows = uint64_t(1) << 30;
+// tiles of 256 x 256, the largest, that a grid holds: threads are counted in 32 bits
+constexpr uint64_t kMaxProductTiles = 0x7FFFFFFF / 1024;
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -224,6 +226,7 @@ int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t
                     check_matrix(out, m, n, ldo, size, 1)});
   if (st != ARMX_OK) return st;
   if ((m > 1 && lda > kMaxProductLd) || (n > 1 && ldb > kMaxProductLd)) return ARMX_ERR_SHAPE;
+  if ((m + 255) / 256 * ((n + 255) / 256) > kMaxProductTiles) return ARMX_ERR_SHAPE;
   if (m == 0 || n == 0) return ARMX_OK;
   if (!a_scales || !b_scales) return ARMX_ERR_NULL;
   if (!aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(bias, size))

@@ -165,18 +165,18 @@ inline int aligned_rows(const MatmulArgs& p) {
 // share k: a group takes every KS-th step of 128 codes and sums over its own.
 // A step's rows of a and b go from memory straight to LDS (buffer_load ... lds,
 // 16 bytes per lane, 8 rows of 128 bytes per wavefront load) into one of the
-// group's NS buffers, NS - 1 steps ahead of the one that is multiplied.  (Steps of 64 codes in four
-// buffers, with rows of 64 bytes, measured slower, 8192^3 450 -> 715 us: memory
-// moves lines of 128 bytes, and each was moved twice.)
+// group's NS buffers, NS - 1 steps ahead of the one that is multiplied.  (Steps of
+// 64 codes in four buffers, with rows of 64 bytes, measured slower, 8192^3 450 ->
+// 715 us: memory moves lines of 128 bytes, and each was moved twice.)
 //
 // Row 4 q + e of a wavefront's operand tile y of b is its column 4 (q kNT + y) + e,
 // so that the lanes of group q end with 4 kNT consecutive columns of a row over the
 // tiles, which they store together.
 //
 // LDS rows are 128 bytes, 8 slots of 16; row r keeps its piece c in slot
-// c ^ swizzle(r), taken of the row's place in its operand tile.  A 16-byte LDS read serves 16 lanes at a time (lanes 0-3,
-// 12-15, 20-23 and 24-27 first, and so on) from 64 banks, that is from 16
-// slots: rows r and r + 1 lie in different halves of them, and the rows of
+// c ^ swizzle(r), taken of the row's place in its operand tile.  A 16-byte LDS read
+// serves 16 lanes at a time (lanes 0-3, 12-15, 20-23 and 24-27 first, and so on)
+// from 64 banks, that is from 16 slots: rows r and r + 1 lie in different halves of them, and the rows of
 // one parity that are read together differ in swizzle (no bank conflicts, by
 // count).  The load writes LDS in lane order, so the swizzle is made on the
 // memory side: the lane that fills slot s of row r fetches piece s ^ swizzle(r).
@@ -556,7 +556,7 @@ hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cf
     case 8: return launch_tiled<OUT, 32, 32, 1, 1, 4, 4>(p, cfg, stream);
     case 9: return launch_tiled<OUT, 16, 32, 1, 1, 8, 2>(p, cfg, stream);
     case 10: return launch_tiled<OUT, 16, 16, 1, 1, 8, 4>(p, cfg, stream);
-    default: return hipErrorInvalidValue;  // no grid holds that many tiles
+    default: return hipErrorInvalidValue;  // more tiles than the entry point lets through
   }
 }
 

@@ -133,7 +133,8 @@ def test_matmul_refusals():
         assert mm(**kw) == -3, kw
     for kw in (dict(k=131072, lda=131072, ldb=131072), dict(lda=48), dict(ldb=48), dict(ldo=3),
                dict(lda=(1 << 23) + 16), dict(ldb=(1 << 23) + 16), dict(m=(1 << 30) + 1),
-               dict(n=(1 << 30) + 1, ldo=1 << 31), dict(m=1 << 30, lda=1 << 23)):
+               dict(n=(1 << 30) + 1, ldo=1 << 31), dict(m=1 << 30, lda=1 << 23),
+               dict(m=1 << 30), dict(m=2097151 * 256 + 1), dict(m=1 << 22, n=1 << 17, ldo=1 << 17)):
         assert mm(**kw) == -5, kw
     assert mm(m=0, a=None, sa=None, out=None) == 0
     assert mm(n=0, b=None, sb=None, out=None) == 0
