@@ -224,7 +224,8 @@ PyObject* norm(const char* name, bool codes, PyObject* const* a, Py_ssize_t n) {
     PyErr_Format(PyExc_ValueError, "%s: sum_out goes with a residual", name);
     return nullptr;
   }
-  if (!output(c, a[5], "out", codes ? code_multiple(c.cols) : 8, codes ? at::kChar : c.type, &out, &r.o[0]))
+  if (!output(c, a[5], "out", codes ? code_multiple(c.cols) : 8, codes ? at::kChar : c.type,
+              &out, &r.o[0]))
     return nullptr;
   if (keep && !vector_output(c, a[6], "scales", c.rows, &side, side_result)) return nullptr;
   const armx_config* cfg = c.has_cfg ? &c.cfg : nullptr;

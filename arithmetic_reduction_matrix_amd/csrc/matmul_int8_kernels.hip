@@ -176,10 +176,17 @@ inline int aligned_rows(const MatmulArgs& p) {
 // LDS rows are 128 bytes, 8 slots of 16; row r keeps its piece c in slot
 // c ^ swizzle(r), taken of the row's place in its operand tile.  A 16-byte LDS read
 // serves 16 lanes at a time (lanes 0-3, 12-15, 20-23 and 24-27 first, and so on)
-// from 64 banks, that is from 16 slots: rows r and r + 1 lie in different halves of them, and the rows of
-// one parity that are read together differ in swizzle (no bank conflicts, by
-// count).  The load writes LDS in lane order, so the swizzle is made on the
-// memory side: the lane that fills slot s of row r fetches piece s ^ swizzle(r).
+// from 64 banks, that is from 16 slots: rows r and r + 1 lie in different halves of
+// them, and the rows of one parity that are read together differ in swizzle (no bank
+// conflicts, by count).  The load writes LDS in lane order, so the swizzle is made on
+// the memory side: the lane that fills slot s of row r fetches piece s ^ swizzle(r).
+//
+// What bounds it on MI355X: at many full tiles the matrix units, busy in 68% of the
+// cycles, and the clock, which falls under them (8192^3 420 us, 2.6e15 operations a
+// second); at 128 x 128 and smaller the LDS, whose operands serve fewer products
+// (128 x 128: 128 KB read or written per step, 0.43 of its 0.52 us; 777 x 4100 x 5001
+// 25.1 us); with few rows the reading of b and the way to the first product
+// (48 x 8192 x 4096 8.8 us, 3.8 TB/s of b; 1 x 4096 x 4096 5.2).
 __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
 
 constexpr int kStepK = 128;
@@ -479,7 +486,8 @@ hipError_t launch_tiled(const MatmulArgs& p, const armx_config* cfg, hipStream_t
   unsigned tiles_m = unsigned((p.m + BM - 1) / BM), tiles_n = unsigned((p.n + BN - 1) / BN);
   int aligned = aligned_rows(p);
   void* args[] = {&copy, &tiles_m, &tiles_n, &aligned};
-  return launch_kernel(reinterpret_cast<const void*>(&matmul_tiled_kernel<BM, BN, WM, WN, KS, NS, OUT>),
+  const auto fn = &matmul_tiled_kernel<BM, BN, WM, WN, KS, NS, OUT>;
+  return launch_kernel(reinterpret_cast<const void*>(fn),
                        dim3(tiles_m * tiles_n), dim3(64 * WM * WN * KS), args, 0, stream,
                        cfg ? static_cast<hipEvent_t>(cfg->start_event) : nullptr,
                        cfg ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);

@@ -144,7 +144,9 @@ struct Lay {
   __device__ __forceinline__ static uint32_t lane() {
     return TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
   }
-  __device__ __forceinline__ static uint32_t row() { return TPR ? threadIdx.x / (TPR ? TPR : 1) : 0; }
+  __device__ __forceinline__ static uint32_t row() {
+    return TPR ? threadIdx.x / (TPR ? TPR : 1) : 0;
+  }
 };
 
 // Clears what a load brought of values past the row.  Applied where the values are
@@ -442,7 +444,13 @@ __device__ __forceinline__ void finish_row(const NormArgs& k, uint64_t row, floa
   }
 }
 
-// Rows in registers (Lay).
+// Norm, norm to codes and codes of rows in registers (Lay): loads, the two row
+// sums, results.  HBM bounds it where there are many rows (us and TB/s of what it
+// reads and writes, on MI355X: the norm of 8192 x 4096 with its sum 46.1, 5.8; its
+// codes of 8192 x 8192 79.3, 5.9; codes of 16384 x 8192 70.0, 5.8), and the chain of
+// a load, a combine and a store where there are few (1 x 4096 2.5 us, 64 x 14336
+// 4.8).  Odd and narrow rows pay for the lanes without a chunk and for lines shared
+// by rows (335544 x 100 at a pitch of 104: norm 79 us, half the rate).
 template <int TYPE, int OUT, bool RES, bool STREAM, class L>
 __global__ __launch_bounds__(L::kMax) void norm_kernel(NormArgs k) {
   constexpr int C = L::kChunks;
@@ -490,7 +498,8 @@ __global__ __launch_bounds__(L::kMax) void norm_kernel(NormArgs k) {
   }
 }
 
-// Rows too long for the registers: one block per row, walked twice.  The
+// Rows too long for the registers: one block per row, walked twice, the second time
+// mostly from the caches (norm of 1016 x 33000 60 us, 4.5 TB/s of one read).  The
 // second walk forms h again from what the first read, or reads it from
 // sum_out (where each thread wrote its own chunks), so that outputs may stand
 // where inputs did.
@@ -646,6 +655,8 @@ __device__ __forceinline__ void store_grads(const NormBackwardArgs& k, uint64_t 
   }
 }
 
+// HBM bounds it: 8192 x 4096 with dsum 47.9 us, and 4.7 for norm_join_kernel, against
+// 51.8 for its bytes at a large copy's rate.
 // Block b takes the row groups b, b + blocks, ...; every thread keeps the
 // dweight sums of its own columns in registers over the block's rows.  A block
 // of several rows at a time adds its row groups' sums through LDS, in order.
@@ -805,7 +816,10 @@ __device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t 
 
 // dx and dweight apart, in one launch without a workspace: the first `col_blocks`
 // blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
-// and the others make the dx of their row groups.
+// and the others make the dx of their row groups.  With few rows (515 x 2056 7.1 us)
+// the column blocks' rounds of loads bound it, with long ones the second read and, at
+// 128 registers a thread, one block per compute unit (1024 x 32768 94 us, 3.6 TB/s of
+// one read).
 template <int TYPE, bool DSUM, class L>
 __global__ __launch_bounds__(L::kMax) void norm_backward_apart_kernel(NormBackwardArgs k,
                                                                      unsigned col_blocks) {

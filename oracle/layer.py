@@ -1,9 +1,6 @@
 """Norms of rows, 8-bit codes and products of codes from their definitions, in
-binary64 (numpy), for the tests.
-
-Inputs are float32 or float64 arrays holding values of a 16-bit type; `rnd`
-rounds an array to that type and returns it widened again.
-"""
+binary64 (numpy), for the tests.  Inputs are float32 or float64 arrays holding
+values of a 16-bit type."""
 from __future__ import annotations
 
 import numpy as np
