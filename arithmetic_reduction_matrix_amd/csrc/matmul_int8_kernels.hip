@@ -167,7 +167,10 @@ struct Columns {
 // With SHIFT a step's window of a row starts at the last 128-byte line before the
 // step, `phase` pieces early, so that a load takes whole lines and none is moved
 // twice; a step of the row then lies in its window and the next one's, and what is
-// read from LDS comes `phase` pieces further on.
+// read from LDS comes `phase` pieces further on.  (That brings rows of unlike phase to
+// one bank, half of the reads by count; kept in the slots of the step's own pieces they
+// never meet, but four lanes then load from both halves of a line: 1500 x 8192 x 4112
+// at 128 x 128 64.3 against 67.4 us, and nothing gained elsewhere.)
 //
 // Row 4 q + e of a wavefront's operand tile y of b is its column 4 (q kNT + y) + e,
 // so that the lanes of group q end with 4 kNT consecutive columns of a row over the
@@ -183,10 +186,11 @@ struct Columns {
 //
 // What bounds it on MI355X: at many full tiles the matrix units, busy in 68% of the
 // cycles, and the clock, which falls under them (8192^3 420 us, 2.6e15 operations a
-// second); at 128 x 128 and smaller the LDS, whose operands serve fewer products
-// (128 x 128: 128 KB read or written per step, 0.43 of its 0.52 us; 777 x 4100 x 5001
-// 23.6 us); with few rows the reading of b and the way to the first product
-// (48 x 8192 x 4096 8.8 us, 3.8 TB/s of b; 1 x 4096 x 4096 5.2).
+// second); at smaller tiles the L2, from which the compute units together take a step's
+// rows at 15 to 20 TB/s (192 x 192 48 KB in 0.84 us each, 128 x 128 32 KB in 0.52, two
+// 64 x 64 32 KB in 0.38; matrix units 41% busy at 777 x 4100 x 5001, 23.6 us); with few
+// rows the reading of b and the way to the first product (48 x 8192 x 4096 8.8 us,
+// 3.8 TB/s of b; 1 x 4096 x 4096 5.2).
 __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
 
 constexpr int kStepK = 128;
