@@ -990,8 +990,9 @@ hipError_t launch_backward_apart(const NormBackwardArgs& a, const NormBackwardPl
   unsigned col_blocks = unsigned((a.cols + 63) / 64);
   void* args[] = {&copy, &col_blocks};
   const uint64_t row_blocks = plan.blocks - col_blocks;
-  // dx where dy is: every column's sums before any row's gradient
-  if (!meet(a.dx, a.ldx, a.dy, a.ldy, a.rows, a.cols))
+  // dx where dy or h is: every column's sums before any row's gradient
+  if (!meet(a.dx, a.ldx, a.dy, a.ldy, a.rows, a.cols) &&
+      !meet(a.dx, a.ldx, a.h, a.ldh, a.rows, a.cols))
     return launch_rows_kernel(fn, plan.blocks, plan.block, args, cfg, stream);
   const hipError_t e =
       launch_rows_kernel(fn, col_blocks, plan.block, args, cfg, stream, true, false);

@@ -476,7 +476,8 @@ int quantize_rows_int8(const void* x, size_t ldx, int type, size_t rows, size_t 
  * inv_rms  device, rows binary32, as rms_norm_rows wrote them.
  * dsum     device, rows x cols, the gradient that flows into sum_out from
  *          elsewhere, or NULL.
- * dx       device, rows x cols; may be dy or dsum themselves.
+ * dx       device, rows x cols; may be dy or dsum themselves (and those h, or
+ *          one another).
  * dweight  device, cols binary32, 16-byte aligned; zeros when rows == 0.
  * ws       device workspace of armx_workspace_bytes(ARMX_OP_RMS_BACKWARD, rows,
  *          cols, NULL) bytes; it needs no zeros and none are left (it has no
@@ -503,7 +504,8 @@ int rms_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh
  * b         device, n x k int8 (a linear layer's weight, one output channel
  *           per row), rows 16-byte aligned.
  *           Every row's first 16 ceil(k / 16) bytes must be readable, the last
- *           row's too; what stands past k is not used.
+ *           row's too; what stands past k is not used.  Rows that all start at
+ *           multiples of 128 bytes are read fastest (by up to a seventh).
  * a_scales  device, m binary32; b_scales device, n binary32.
  * bias      device, n values of out_type, or NULL.
  * out       device, m x n of out_type (ARMX_F16, ARMX_BF16 or ARMX_F32), any

@@ -241,6 +241,23 @@ def test_outputs_may_stand_where_inputs_did(cols, dtype):
         assert np.array_equal(bits(got.dweight), bits(g.dweight))
 
 
+@pytest.mark.parametrize("rows,cols", [(9, 40), (600, 2056), (3000, 1000), (70, 20000), (40, 40000)])
+def test_gradients_where_everything_is_one_matrix(rows, cols):
+    # dy, h and dsum the same matrix, or two of them, and dx written over it
+    rng = np.random.default_rng(13)
+    x, y = (make(rng, rows, cols, torch.bfloat16, device="cuda") for _ in range(2))
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(cols)).bfloat16().cuda()
+    inv = armx.rms_norm_rows(x, w, keep_inv_rms=True).inv_rms
+    for dy, ds in ((x, x), (y, x), (x, y), (x, None)):
+        want = armx.rms_norm_rows_backward(dy, x, w, inv, dsum=ds)
+        one, other = x.clone(), y.clone()
+        of = {id(x): one, id(y): other, id(None): None}
+        got = armx.rms_norm_rows_backward(of[id(dy)], one, w, inv, dsum=of[id(ds)], out=one)
+        assert got.dx is one
+        assert np.array_equal(bits(got.dx), bits(want.dx))
+        assert np.array_equal(bits(got.dweight), bits(want.dweight))
+
+
 @pytest.mark.parametrize("cols", [8, 100, 1000, 2048, 5001, 33000])
 def test_batch_invariance(cols):
     rng = np.random.default_rng(7)
