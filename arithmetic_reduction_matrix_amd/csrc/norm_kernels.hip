@@ -758,9 +758,9 @@ typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
 // dweight over all rows for 64 columns (number `block` of them), by a whole block: 8
 // lanes take a row's 64 columns, 8 rows to a wavefront; rows in steps of the block's,
-// four in flight.  part: 64 floats per wavefront.
-template <int TYPE>
-__device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t block,
+// FLIGHT in flight.  part: 64 floats per wavefront.
+template <int TYPE, int FLIGHT>
+__device__ __forceinline__ void sum_columns_in(const NormBackwardArgs& k, uint32_t block,
                                             float (*part)[64]) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   const uint32_t c = block * 8 + (threadIdx.x & 7);
@@ -769,11 +769,11 @@ __device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t 
   const uint32_t e0 = c * 8 + 8 <= cols ? c * 8 : cols - 8;
   const uint32_t step = blockDim.x / 8;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += 4 * step) {
-    u32x4 y[4], x[4];
-    float inv[4];
+  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += FLIGHT * step) {
+    u32x4 y[FLIGHT], x[FLIGHT];
+    float inv[FLIGHT];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < FLIGHT; ++q) {
       // a row past the last is read as this thread's first, and not added
       const uint64_t rq = r + q * step < k.rows ? r + q * step : r;
       inv[q] = k.inv_rms[rq];
@@ -786,7 +786,7 @@ __device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t 
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < FLIGHT; ++q) {
       if (r + q * step >= k.rows) continue;
       float fy[8], fh[8];
       widen8<TYPE>(y[q], fy);
@@ -814,9 +814,21 @@ __device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t 
   }
 }
 
+// Eight rows in flight where four would take a second round (us: 515 x 2056 7.1 -> 6.7,
+// 300 x 16384 11.8 -> 11.1; with one round 64 x 4096 3.3 -> 3.8, and where the row
+// blocks' registers fill the compute units 559 x 60001 90 -> 93).
+template <int TYPE, bool LONG>
+__device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t block,
+                                            float (*part)[64]) {
+  if (LONG || k.rows <= blockDim.x / 2)
+    sum_columns_in<TYPE, 4>(k, block, part);
+  else
+    sum_columns_in<TYPE, 8>(k, block, part);
+}
+
 // dx and dweight apart, in one launch without a workspace: the first `col_blocks`
 // blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
-// and the others make the dx of their row groups.  With few rows (515 x 2056 7.1 us)
+// and the others make the dx of their row groups.  With few rows (515 x 2056 6.7 us)
 // the column blocks' rounds of loads bound it, with long ones the second read and, at
 // 128 registers a thread, one block per compute unit (1024 x 32768 94 us, 3.6 TB/s of
 // one read).
@@ -827,7 +839,7 @@ __global__ __launch_bounds__(L::kMax) void norm_backward_apart_kernel(NormBackwa
   __shared__ typename RowCombine<L>::Lds lds[2];
   __shared__ float part[L::kMax / 64][64];
   if (blockIdx.x < col_blocks) {
-    sum_columns<TYPE>(k, blockIdx.x, part);
+    sum_columns<TYPE, (L::kMax > 512)>(k, blockIdx.x, part);
     return;
   }
   const uint32_t cols = uint32_t(k.cols);
@@ -868,7 +880,7 @@ __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardAr
   __shared__ typename RowCombine<L>::Lds lds[2];
   __shared__ float part[16][64];
   if (blockIdx.x < col_blocks) {
-    sum_columns<TYPE>(k, blockIdx.x, part);
+    sum_columns<TYPE, true>(k, blockIdx.x, part);
     return;
   }
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
