@@ -567,6 +567,15 @@ RowShape for_pitch(RowShape s, uint64_t ld) {
 
 bool is_widest(const RowShape& s) { return s.chunks == 4 && s.threads > 512; }
 
+// Columns of a block that sums dweight apart from dx: 64, whole lines of a row, but 32
+// on rows of up to 320 chunks, of which 64 would make few blocks (us, 64 / 32: 500 x 333
+// 6.2 / 4.3, 515 x 2056 6.7 / 6.2; 1000 x 4096 9.9 / 11.2, 256 x 8192 6.0 / 7.1).
+bool half_columns(const RowShape& s) { return s.chunks == 1 && s.threads <= 320; }
+uint64_t column_blocks(const RowShape& s, uint64_t cols) {
+  const uint64_t width = half_columns(s) ? 32 : 64;
+  return (cols + width - 1) / width;
+}
+
 // Threads of a block and the rows it takes at a time.
 int block_threads(const RowShape& s) { return s.threads > 64 ? s.threads : kRowBlock; }
 uint64_t block_rows(const RowShape& s) { return s.threads > 64 ? 1 : kRowBlock / s.threads; }
@@ -756,20 +765,20 @@ __global__ __launch_bounds__(L::kMax) void norm_backward_kernel(NormBackwardArgs
 // A chunk that starts at any value.
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-// dweight over all rows for 64 columns (number `block` of them), by a whole block: 8
-// lanes take a row's 64 columns, 8 rows to a wavefront; rows in steps of the block's,
-// FLIGHT in flight.  part: 64 floats per wavefront.
-template <int TYPE, int FLIGHT>
+// dweight over all rows for 8 LANES columns (number `block` of them), by a whole block:
+// LANES lanes take a row's, rows in steps of the block's, FLIGHT in flight.  part: 64
+// floats per wavefront.
+template <int TYPE, int LANES, int FLIGHT>
 __device__ __forceinline__ void sum_columns_in(const NormBackwardArgs& k, uint32_t block,
                                             float (*part)[64]) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-  const uint32_t c = block * 8 + (threadIdx.x & 7);
+  const uint32_t c = block * LANES + threadIdx.x % LANES;
   // The last chunk is read as the row's last 8 values, without a branch (a lane with
   // none too); those in front of the chunk are the lane's before it.
   const uint32_t e0 = c * 8 + 8 <= cols ? c * 8 : cols - 8;
-  const uint32_t step = blockDim.x / 8;
+  const uint32_t step = blockDim.x / LANES;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (uint64_t r = threadIdx.x >> 3; r < k.rows; r += FLIGHT * step) {
+  for (uint64_t r = threadIdx.x / LANES; r < k.rows; r += FLIGHT * step) {
     u32x4 y[FLIGHT], x[FLIGHT];
     float inv[FLIGHT];
 #pragma unroll
@@ -796,17 +805,19 @@ __device__ __forceinline__ void sum_columns_in(const NormBackwardArgs& k, uint32
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {   // over the wavefront's 8 rows: lanes 8, 16 and 32 apart
+  for (int i = 0; i < 8; ++i) {   // over the wavefront's rows: lanes LANES and more apart
     float v = acc[i];
+    if constexpr (LANES == 4) v += dpp<kDppRor4>(v);
     v += dpp<kDppRor8>(v);
     v = add_xor16(v);
     v = add_xor32(v);
     const uint32_t e = (cols >= 8 ? e0 : c * 8) + i;
-    if (lane_id() < 8 && c < chunks && e >= c * 8) part[wave_id()][e - block * 64] = v;
+    if (lane_id() < LANES && c < chunks && e >= c * 8)
+      part[wave_id()][e - block * (8 * LANES)] = v;
   }
   __syncthreads();
-  const uint32_t e = block * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && e < cols) {
+  const uint32_t e = block * (8 * LANES) + threadIdx.x;
+  if (threadIdx.x < 8 * LANES && e < cols) {
     float v = part[0][threadIdx.x];
     const int waves = num_waves();
     for (int q = 1; q < waves; ++q) v += part[q][threadIdx.x];
@@ -819,27 +830,39 @@ __device__ __forceinline__ void sum_columns_in(const NormBackwardArgs& k, uint32
 // blocks' registers fill the compute units 559 x 60001 90 -> 93).
 template <int TYPE, bool LONG>
 __device__ __forceinline__ void sum_columns(const NormBackwardArgs& k, uint32_t block,
-                                            float (*part)[64]) {
-  if (LONG || k.rows <= blockDim.x / 2)
-    sum_columns_in<TYPE, 4>(k, block, part);
-  else
-    sum_columns_in<TYPE, 8>(k, block, part);
+                                            float (*part)[64], bool half) {
+  const uint32_t lanes = half ? 4 : 8;
+  const bool one_round = k.rows <= 4 * (blockDim.x / lanes);
+  if constexpr (LONG) {
+    sum_columns_in<TYPE, 8, 4>(k, block, part);
+  } else if (half) {
+    if (one_round)
+      sum_columns_in<TYPE, 4, 4>(k, block, part);
+    else
+      sum_columns_in<TYPE, 4, 8>(k, block, part);
+  } else {
+    if (one_round)
+      sum_columns_in<TYPE, 8, 4>(k, block, part);
+    else
+      sum_columns_in<TYPE, 8, 8>(k, block, part);
+  }
 }
 
 // dx and dweight apart, in one launch without a workspace: the first `col_blocks`
-// blocks each sum dweight over all rows for 64 columns, reading dy and h once more,
-// and the others make the dx of their row groups.  With few rows (515 x 2056 6.7 us)
-// the column blocks' rounds of loads bound it, with long ones the second read and, at
-// 128 registers a thread, one block per compute unit (1024 x 32768 94 us, 3.6 TB/s of
-// one read).
+// blocks each sum dweight over all rows for 64 or 32 columns (`half`), reading dy and
+// h once more, and the others make the dx of their row groups.  With few rows (515 x
+// 2056 6.2 us) the column blocks' rounds of loads bound it, with long ones the second
+// read and, at 128 registers a thread, one block per compute unit (1024 x 32768 with
+// dsum 94 us, 3.6 TB/s of one read).
 template <int TYPE, bool DSUM, class L>
 __global__ __launch_bounds__(L::kMax) void norm_backward_apart_kernel(NormBackwardArgs k,
-                                                                     unsigned col_blocks) {
+                                                                     unsigned col_blocks,
+                                                                     bool half) {
   constexpr int C = L::kChunks;
   __shared__ typename RowCombine<L>::Lds lds[2];
   __shared__ float part[L::kMax / 64][64];
   if (blockIdx.x < col_blocks) {
-    sum_columns<TYPE, (L::kMax > 512)>(k, blockIdx.x, part);
+    sum_columns<TYPE, (L::kMax > 512)>(k, blockIdx.x, part, half);
     return;
   }
   const uint32_t cols = uint32_t(k.cols);
@@ -875,12 +898,13 @@ __global__ __launch_bounds__(L::kMax) void norm_backward_apart_kernel(NormBackwa
 // a thread at a time.
 template <int TYPE, bool DSUM>
 __global__ __launch_bounds__(1024) void norm_backward_loop_kernel(NormBackwardArgs k,
-                                                                  unsigned col_blocks) {
+                                                                  unsigned col_blocks,
+                                                                  bool half) {
   typedef Lay<0, 1024, 4> L;
   __shared__ typename RowCombine<L>::Lds lds[2];
   __shared__ float part[16][64];
   if (blockIdx.x < col_blocks) {
-    sum_columns<TYPE, true>(k, blockIdx.x, part);
+    sum_columns<TYPE, true>(k, blockIdx.x, part, half);
     return;
   }
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
@@ -999,8 +1023,9 @@ hipError_t launch_backward_apart(const NormBackwardArgs& a, const NormBackwardPl
 #undef ARMX_NORM_CASE
   if (s.chunks == 0) fn = reinterpret_cast<const void*>(&norm_backward_loop_kernel<TYPE, DSUM>);
   NormBackwardArgs copy = a;
-  unsigned col_blocks = unsigned((a.cols + 63) / 64);
-  void* args[] = {&copy, &col_blocks};
+  unsigned col_blocks = unsigned(column_blocks(plan.shape, a.cols));
+  bool half = half_columns(plan.shape);
+  void* args[] = {&copy, &col_blocks, &half};
   const uint64_t row_blocks = plan.blocks - col_blocks;
   // dx where dy or h is: every column's sums before any row's gradient
   if (!meet(a.dx, a.ldx, a.dy, a.ldy, a.rows, a.cols) &&
@@ -1049,15 +1074,16 @@ NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count) 
   p.block = block_threads(p.shape);
   if (rows == 0 || cols == 0) return p;
   const uint64_t groups = (rows + block_rows(p.shape) - 1) / block_rows(p.shape);
-  // Few rows: the column blocks read them in at most four rounds, from the caches
-  // (us, partial sums / columns apart: 512 x 1024 8.1 / 5.3, 1024 x 8192 17.9 / 15.9,
-  // 2048 x 4096 16.9 / 16.8, 2048 x 1024 9.6 / 21.7, 1024 x 16384 36.3 / 36.5).
+  // Few rows: the column blocks read them in a few rounds, from the caches (us,
+  // partial sums / columns apart: 512 x 100 5.5 / 3.5, 1024 x 100 5.6 / 4.6, 1536 x 256
+  // 6.0 / 5.8, 2048 x 256 5.9 / 7.0, 512 x 1024 7.3 / 4.8, 1024 x 1024 9.2 / 9.3, 1536 x
+  // 1024 10.3 / 13.1, 1024 x 8192 17.9 / 14.0, 2048 x 4096 15.4 / 16.8).
   // Rows of more than 16384 values, however many: the registers do not hold the
   // partial sums too (512 x 32768 106 / 39, 559 x 60001 294 / 104).
-  p.apart = (rows <= 2 * uint64_t(p.block) && rows * cols <= uint64_t(1) << 23) ||
+  p.apart = (rows <= 1024 && rows * cols <= uint64_t(1) << 23) ||
             is_widest(p.shape) || p.shape.chunks == 0;
   if (p.apart) {
-    p.blocks = (cols + 63) / 64 + (groups < kMaxGrid / 2 ? groups : kMaxGrid / 2);
+    p.blocks = column_blocks(p.shape, cols) + (groups < kMaxGrid / 2 ? groups : kMaxGrid / 2);
     return p;
   }
   // Every block's dweight sums are written and read again, so fewer blocks move

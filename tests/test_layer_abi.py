@@ -104,7 +104,7 @@ def test_backward_workspace_and_plan():
     # their own, one launch, no workspace; otherwise every block's partial sums and
     # a launch that joins them
     for rows, cols, apart in ((2, 4096, True), (1024, 4096, True), (1025, 4096, False),
-                              (512, 128, True), (513, 128, False), (1024, 8200, False),
+                              (1024, 128, True), (1025, 128, False), (1024, 8200, False),
                               (5000, 20000, True), (5000, 100, False), (8192, 4096, False),
                               (77, 40000, True), (5000, 40000, True)):
         p = armx.launch_plan(armx.OP_RMS_BACKWARD, rows, cols)
