@@ -122,7 +122,7 @@ hipError_t launch_row_plans(const armx::RowPlans& plans, const void* x, float* o
 int plan_backward(size_t rows, size_t cols, const armx_config* cfg, armx::NormBackwardPlan* p) {
   if (cfg && (cfg->block_threads || cfg->chain_r || cfg->grid_blocks || cfg->flags))
     return ARMX_ERR_CONFIG;
-  if (rows > armx::kMaxN || cols >= (uint64_t(1) << 30)) return ARMX_ERR_SHAPE;
+  if (rows > armx::kMaxN || cols > armx::kMaxBackwardCols) return ARMX_ERR_SHAPE;
   *p = armx::plan_norm_backward(rows, cols, rows && cols ? current_cu_count() : 256);
   return ARMX_OK;
 }

@@ -71,6 +71,9 @@ struct NormBackwardPlan {
   size_t ws_bytes = 0;
 };
 
+// Longest rows of the backward pass: their column blocks of 64 and a block for each of
+// 2^20 rows fill the largest grid.
+constexpr uint64_t kMaxBackwardCols = uint64_t(1) << 26;
 NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count);
 
 struct MatmulArgs {

@@ -479,6 +479,7 @@ int quantize_rows_int8(const void* x, size_t ldx, int type, size_t rows, size_t 
  * dx       device, rows x cols; may be dy or dsum themselves (and those h, or
  *          one another).
  * dweight  device, cols binary32, 16-byte aligned; zeros when rows == 0.
+ * cols     at most 2^26.
  * ws       device workspace of armx_workspace_bytes(ARMX_OP_RMS_BACKWARD, rows,
  *          cols, NULL) bytes; it needs no zeros and none are left (it has no
  *          counter region).  NULL when that is 0.

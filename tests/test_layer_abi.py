@@ -92,7 +92,8 @@ def test_backward_refusals():
     need = armx.workspace_bytes(armx.OP_RMS_BACKWARD, 4096, 4096)
     assert need > 0
     assert back(ws_bytes=need - 1, **big) == -4
-    for kw in (dict(ldy=56), dict(ldh=56), dict(ldx=56), dict(ds=P, ldd=56), dict(cols=1 << 30)):
+    for kw in (dict(ldy=56), dict(ldh=56), dict(ldx=56), dict(ds=P, ldd=56), dict(cols=1 << 30),
+               dict(cols=(1 << 26) + 1, rows=1)):
         assert back(**kw) == -5, kw
     assert back(cols=0, dy=None, h=None, dx=None, dw=None, w=None, inv=None, ws=None) == 0
 
@@ -119,6 +120,13 @@ def test_backward_workspace_and_plan():
         armx.workspace_bytes(armx.OP_RMS_BACKWARD, 4, 64, chain_r=2)
     with pytest.raises(armx.ArmxError):
         armx.launch_plan(armx.OP_RMS_BACKWARD, 4, 1 << 31)
+    with pytest.raises(armx.ArmxError):
+        armx.workspace_bytes(armx.OP_RMS_BACKWARD, 4, (1 << 26) + 1)
+    # the largest grid: a block per row up to half of it, column blocks the other half
+    p = armx.launch_plan(armx.OP_RMS_BACKWARD, 1 << 14, 1 << 26)
+    assert p["grid_blocks"] == (1 << 20) + (1 << 14) and p["workspace_bytes"] == 0
+    p = armx.launch_plan(armx.OP_RMS_BACKWARD, 1 << 22, 1 << 18)
+    assert p["grid_blocks"] * p["block_threads"] < 1 << 31
     assert armx.launch_plan(armx.OP_RMS_BACKWARD, 4, 0)["launches"] == 0
 
 
