@@ -228,9 +228,12 @@ typedef __attribute__((address_space(3))) int8_t lds_byte;
 // 16 bytes per lane from `rows` into LDS at `lds` + 16 lane.  Written as asm so
 // that the compiler, which cannot tell the two buffers apart, does not wait for
 // these loads before every read of LDS; nothing comes back in registers, and
-// wait_loads() and a barrier stand between these writes and their reads.
+// wait_loads() and a barrier stand between these writes and their reads.  The load
+// reads M0, which needs a wait state after its scalar write; the compiler puts none
+// inside an asm string.  (M0 is a reserved register, which a clobber list cannot name;
+// the compiler uses it for nothing else here.)
 __device__ __forceinline__ void lds_load16(const CodeRows& rows, uint32_t lds, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(off), "s"(rows.rs)
                : "memory");
