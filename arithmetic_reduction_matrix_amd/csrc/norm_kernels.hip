@@ -313,8 +313,10 @@ __device__ __forceinline__ u32x2 codes8(const float (&p)[8], const CodeScale& cs
   return v;
 }
 
+// (a row of zeros has an infinite inv where eps is 0; its scale is 0 all the same)
 __device__ __forceinline__ float code_scale(uint32_t top_bits, float inv) {
   if (top_bits >= kInfBits) return __builtin_nanf("");
+  if (top_bits == 0) return 0.0f;
   return __builtin_bit_cast(float, top_bits) * inv / 127.0f;
 }
 
