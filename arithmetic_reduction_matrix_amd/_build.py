@@ -4,7 +4,8 @@ plain read stream, for measurement only).
 
 Run ``python arithmetic_reduction_matrix_amd/_build.py`` or call ``build()`` (it imports
 only the standard library, so it runs whether or not a library is built; the
-binding is compiled against the headers of the installed PyTorch).
+binding is compiled against the headers of the installed PyTorch, and the libraries
+need none).
 Every source is compiled each time; objects go to ``_build/`` next to this
 file and the library is written to ``libarmx.so`` in this package.
 """
@@ -65,57 +66,62 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
-def _torch_dir() -> str:
-    """Where PyTorch is installed (found without importing it)."""
+def _torch_dir() -> str | None:
+    """Where PyTorch is installed (found without importing it); None if it is not."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch is not installed")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
 def build(verbose: bool = False, jobs: int | None = None) -> str:
-    """Compiles every source and links libarmx.so; returns its path."""
+    """Compiles every source and links libarmx.so; returns its path.
+
+    libarmx.so needs no PyTorch and is linked before the binding's outcome counts: a
+    binding that does not compile raises with the library in place, and without PyTorch
+    there is none."""
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
-    objs = []
-    cmds = []
-    for src in HIP_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        objs.append(obj)
-        cmds.append([hipcc, *COMMON, *DEVICE, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj])
-    for src in HOST_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        objs.append(obj)
-        cmds.append([hipcc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj])
-    probe_objs = []
-    for src in PROBE_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        probe_objs.append(obj)
-        cmds.append([hipcc, *COMMON, *DEVICE, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj])
-    binding_objs = []
-    torch_dir = _torch_dir()
-    include = [os.path.join(torch_dir, "include"),
-               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"]]
-    for src in BINDING_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        binding_objs.append(obj)
-        # first in the list: it takes longest
-        cmds.insert(0, [hipcc, *COMMON, *(f"-isystem{d}" for d in include), "-DUSE_ROCM", "-c",
-                        os.path.join(CSRC, src), "-o", obj])
-    with ThreadPoolExecutor(max_workers=jobs) as pool:
-        list(pool.map(lambda c: _run(c, verbose), cmds))
-    torch_lib = os.path.join(torch_dir, "lib")
-    for out, parts, more in (
-            (LIB, objs, []), (PROBE_LIB, probe_objs, []),
-            (BINDING, binding_objs,
-             [f"-L{PKG}", "-l:libarmx.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch",
-              "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])):
+
+    def compile_all(sources: list[str], flags: list[str]) -> tuple[list[str], list]:
+        objs = [os.path.join(BUILD, src + ".o") for src in sources]
+        return objs, [pool.submit(_run, [hipcc, *COMMON, *flags, "-c", os.path.join(CSRC, src),
+                                         "-o", obj], verbose)
+                      for src, obj in zip(sources, objs)]
+
+    def link(out: str, objs: list[str], more: list[str]) -> None:
         tmp = out + ".tmp"
-        _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *parts, *more, "-o", tmp],
+        _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, *more, "-o", tmp],
              verbose)
         os.replace(tmp, out)
+
+    torch_dir = _torch_dir()
+    hip = [*DEVICE, "-x", "hip"]
+    with ThreadPoolExecutor(max_workers=jobs) as pool:
+        if torch_dir is not None:   # first: it takes longest
+            include = [os.path.join(torch_dir, "include"),
+                       os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                       sysconfig.get_paths()["include"]]
+            binding = compile_all(BINDING_SOURCES,
+                                  [*(f"-isystem{d}" for d in include), "-DUSE_ROCM"])
+        kernels = compile_all(HIP_SOURCES, hip)
+        host = compile_all(HOST_SOURCES, [])
+        probe = compile_all(PROBE_SOURCES, hip)
+        for _, running in (kernels, host, probe):
+            for r in running:
+                r.result()
+        link(LIB, kernels[0] + host[0], [])
+        link(PROBE_LIB, probe[0], [])
+        if torch_dir is None:
+            print("PyTorch is not installed: _binding.so is not built", file=sys.stderr)
+            return LIB
+        for r in binding[1]:
+            r.result()
+        torch_lib = os.path.join(torch_dir, "lib")
+        link(BINDING, binding[0],
+             [f"-L{os.path.dirname(LIB)}", "-l:libarmx.so", f"-L{torch_lib}", "-ltorch_python",
+              "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])
     return LIB
 
 

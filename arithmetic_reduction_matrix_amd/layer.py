@@ -20,12 +20,26 @@ import torch   # before the module that is linked against it
 
 from . import Config, _check, _event_handle, lib
 
+
+
+class _NotLoaded:
+    """Stands for the module of the calls where it does not load: the sums do not need
+    it, so only these calls raise."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name: str):
+        raise ImportError(
+            f"{name}: arithmetic_reduction_matrix_amd/_binding.so does not load "
+            f"({self._cause}): build it with `python arithmetic_reduction_matrix_amd/_build.py` "
+            "(or __graft_entry__.build())") from self._cause
+
+
 try:
     from . import _binding
-except ImportError as e:
-    raise ImportError(
-        f"arithmetic_reduction_matrix_amd/_binding.so does not load ({e}): build it with "
-        "`python arithmetic_reduction_matrix_amd/_build.py` (or __graft_entry__.build())") from e
+except ImportError as _cause:
+    _binding = _NotLoaded(_cause)
 
 __all__ = ["rms_norm_rows", "rms_norm_rows_int8", "rms_norm_rows_backward",
            "quantize_rows_int8", "matmul_int8", "RmsNorm", "RmsNormInt8", "RmsNormGrads",
