@@ -130,31 +130,67 @@ Tensor make_rows(const Call& c, int64_t multiple, ScalarType type, Rows* out) {
 // them by (1024 x 4096 x 4112, a pitch of 4224 against 4112: 20.0 against 22.0 us).
 int64_t code_multiple(int64_t cols) { return cols < 512 ? 16 : 128; }
 
-// An output: the caller's (returned as it came) or a new one.
-bool output(const Call& c, PyObject* given, const char* what, int64_t multiple, ScalarType type,
-            Rows* out, PyObject** result) {
-  if (given != Py_None) {
-    if (!matrix(c, given, what, c.rows, c.cols, type, out)) return false;
-    Py_INCREF(given);
-    *result = given;
-    return true;
-  }
-  *result = THPVariable_Wrap(make_rows(c, multiple, type, out));
-  return *result != nullptr;
+// Writes that autograd does not see: what it saved of the tensor's old values is then
+// refused.  (Inference tensors have no version, and nothing saves them.)
+void written(PyObject* o) {
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-bool vector_output(const Call& c, PyObject* given, const char* what, int64_t n, void** p,
-                   PyObject** result) {
+// Owned references that are released unless handed on; `given`: to the caller's own
+// tensors.
+struct Owned {
+  PyObject* o[3] = {nullptr, nullptr, nullptr};
+  bool given[3] = {false, false, false};
+  ~Owned() {
+    for (PyObject* p : o) Py_XDECREF(p);
+  }
+  void give(int i, PyObject* tensor) {
+    Py_INCREF(tensor);
+    o[i] = tensor;
+    given[i] = true;
+  }
+  // The tuple of `n` of them (None for those that are missing), or the status.
+  PyObject* done(int status, int n) {
+    if (status != ARMX_OK) return PyLong_FromLong(status);
+    PyObject* t = PyTuple_New(n);
+    if (!t) return nullptr;
+    for (int i = 0; i < n; ++i) {
+      if (!o[i]) {
+        Py_INCREF(Py_None);
+        o[i] = Py_None;
+      }
+      if (given[i]) written(o[i]);
+      PyTuple_SET_ITEM(t, i, o[i]);
+      o[i] = nullptr;
+    }
+    return t;
+  }
+};
+
+// Output i of a call: the caller's (returned as it came) or a new one.
+bool output(const Call& c, PyObject* given, const char* what, int64_t multiple, ScalarType type,
+            Rows* out, Owned& r, int i) {
+  if (given != Py_None) {
+    if (!matrix(c, given, what, c.rows, c.cols, type, out)) return false;
+    r.give(i, given);
+    return true;
+  }
+  r.o[i] = THPVariable_Wrap(make_rows(c, multiple, type, out));
+  return r.o[i] != nullptr;
+}
+
+bool vector_output(const Call& c, PyObject* given, const char* what, int64_t n, void** p, Owned& r,
+                   int i) {
   if (given != Py_None) {
     if (!vector(c, given, what, n, at::kFloat, p)) return false;
-    Py_INCREF(given);
-    *result = given;
+    r.give(i, given);
     return true;
   }
   Tensor t = make(c, {n}, at::kFloat);
   *p = t.data_ptr();
-  *result = THPVariable_Wrap(std::move(t));
-  return *result != nullptr;
+  r.o[i] = THPVariable_Wrap(std::move(t));
+  return r.o[i] != nullptr;
 }
 
 // hipEvent_t handles (ints or None) into the call's configuration.
@@ -174,29 +210,6 @@ bool arity(const char* name, Py_ssize_t got, Py_ssize_t want) {
 
 void* stream_of(const Call& c) { return c10::hip::getCurrentHIPStream(c.device.index()).stream(); }
 
-// Owned references that are released unless handed on.
-struct Owned {
-  PyObject* o[3] = {nullptr, nullptr, nullptr};
-  ~Owned() {
-    for (PyObject* p : o) Py_XDECREF(p);
-  }
-  // The tuple of `n` of them (None for those that are missing), or the status.
-  PyObject* done(int status, int n) {
-    if (status != ARMX_OK) return PyLong_FromLong(status);
-    PyObject* t = PyTuple_New(n);
-    if (!t) return nullptr;
-    for (int i = 0; i < n; ++i) {
-      if (!o[i]) {
-        Py_INCREF(Py_None);
-        o[i] = Py_None;
-      }
-      PyTuple_SET_ITEM(t, i, o[i]);
-      o[i] = nullptr;
-    }
-    return t;
-  }
-};
-
 // (x, weight, residual, eps, keep_inv_rms | None, out, scales, sum_out, start, stop);
 // codes: rms_norm_rows_int8, whose `out` is int8
 PyObject* norm(const char* name, bool codes, PyObject* const* a, Py_ssize_t n) {
@@ -213,21 +226,20 @@ PyObject* norm(const char* name, bool codes, PyObject* const* a, Py_ssize_t n) {
   const int keep = codes ? 1 : PyObject_IsTrue(a[4]);
   if (keep < 0 || !events(c, a[8], a[9])) return nullptr;
   Owned r;   // out, sum, inv_rms; or codes, scales, sum
-  PyObject** sum_result = &r.o[codes ? 2 : 1];
-  PyObject** side_result = &r.o[codes ? 1 : 2];
+  const int sum_result = codes ? 2 : 1, side_result = codes ? 1 : 2;
   c10::DeviceGuard guard(c.device);
   if (a[2] != Py_None) {
     if (!matrix(c, a[2], "residual", c.rows, c.cols, c.type, &res) ||
-        !output(c, a[7], "sum_out", 8, c.type, &sum, sum_result))
+        !output(c, a[7], "sum_out", 8, c.type, &sum, r, sum_result))
       return nullptr;
   } else if (a[7] != Py_None) {
     PyErr_Format(PyExc_ValueError, "%s: sum_out goes with a residual", name);
     return nullptr;
   }
   if (!output(c, a[5], "out", codes ? code_multiple(c.cols) : 8, codes ? at::kChar : c.type,
-              &out, &r.o[0]))
+              &out, r, 0))
     return nullptr;
-  if (keep && !vector_output(c, a[6], "scales", c.rows, &side, side_result)) return nullptr;
+  if (keep && !vector_output(c, a[6], "scales", c.rows, &side, r, side_result)) return nullptr;
   const armx_config* cfg = c.has_cfg ? &c.cfg : nullptr;
   const int st =
       codes ? rms_norm_rows_int8(x.p, x.ld, res.p, res.ld, w, type_code(c.type), size_t(c.rows),
@@ -259,8 +271,8 @@ PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   Owned r;
   c10::DeviceGuard guard(c.device);
-  if (!output(c, a[1], "out", code_multiple(c.cols), at::kChar, &out, &r.o[0]) ||
-      !vector_output(c, a[2], "scales", c.rows, &scales, &r.o[1]))
+  if (!output(c, a[1], "out", code_multiple(c.cols), at::kChar, &out, r, 0) ||
+      !vector_output(c, a[2], "scales", c.rows, &scales, r, 1))
     return nullptr;
   const int st = quantize_rows_int8(x.p, x.ld, type_code(c.type), size_t(c.rows), size_t(c.cols),
                                     static_cast<int8_t*>(out.p), out.ld,
@@ -286,8 +298,8 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   Owned r;
   c10::DeviceGuard guard(c.device);
-  if (!output(c, a[5], "out", 8, c.type, &dx, &r.o[0]) ||
-      !vector_output(c, a[6], "dweight", c.cols, &dw, &r.o[1]))
+  if (!output(c, a[5], "out", 8, c.type, &dx, r, 0) ||
+      !vector_output(c, a[6], "dweight", c.cols, &dw, r, 1))
     return nullptr;
   Tensor space;   // from the allocator, which knows streams and graph captures: it
                   // needs no zeros, so nothing is gained by keeping one
@@ -311,6 +323,7 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(inv), ds.p, ds.ld, type_code(c.type),
       size_t(c.rows), size_t(c.cols), dx.p, dx.ld, static_cast<float*>(dw), ws, ws_bytes,
       c.has_cfg ? &c.cfg : nullptr, stream_of(c));
+  if (st == ARMX_OK && ws_bytes && a[7] != Py_None) written(a[7]);
   return r.done(st, 2);
   END_HANDLE_TH_ERRORS
 }
@@ -362,7 +375,7 @@ PyObject* py_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Owned r;
   c10::DeviceGuard guard(c.device);
   c.cols = cols;
-  if (!output(c, a[5], "out", 1, type, &out, &r.o[0])) return nullptr;
+  if (!output(c, a[5], "out", 1, type, &out, r, 0)) return nullptr;
   const int st = matmul_int8(static_cast<const int8_t*>(ar.p), ar.ld, static_cast<const float*>(as),
                              static_cast<const int8_t*>(br.p), br.ld, static_cast<const float*>(bs),
                              bias, size_t(m), size_t(cols), size_t(k), out.p, out.ld, int(code),

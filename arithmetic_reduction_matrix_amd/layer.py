@@ -9,7 +9,8 @@ rows of 16-bit values start at multiples of 16 bytes (a row pitch that is a
 multiple of 8) and rows of codes too (a multiple of 16).  Matrices made here
 have such a pitch, so results of odd width are views of wider ones.  Calls run
 on the current stream of the inputs' device and record no autograd graph:
-``rms_norm_rows_backward`` gives the norm's gradients.
+``rms_norm_rows_backward`` gives the norm's gradients.  A tensor given for a result
+counts as written in place, so that a backward pass which saved its old values raises.
 """
 from __future__ import annotations
 

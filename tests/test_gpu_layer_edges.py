@@ -36,3 +36,67 @@ def test_codes_of_rows_of_zeros_without_eps(cols, dtype):
         assert n.codes[others].abs().amax(1).eq(127).all()
         y = armx.matmul_int8(n.codes, n.scales, n.codes, n.scales, dtype=torch.float32)
         assert not y[zeros].any() and not y[:, zeros].any() and torch.isfinite(y).all()
+
+
+def every_output(rows=6, cols=40):
+    """Each call with every output that it takes, as (call, outputs, inputs)."""
+    rng = np.random.default_rng(1)
+    x, r, dy, o, s, d = (make(rng, rows, cols, torch.float16, device="cuda") for _ in range(6))
+    w = torch.ones(cols, dtype=torch.float16, device="cuda")
+    inv, sc, sc2, sa = (torch.ones(rows, device="cuda") for _ in range(4))
+    q, q2 = (torch.zeros(rows, 48, dtype=torch.int8, device="cuda")[:, :cols] for _ in range(2))
+    dw, y = torch.zeros(cols, device="cuda"), torch.zeros(rows, rows, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    big = make(rng, 2000, cols, torch.float16, device="cuda")
+    ones = torch.ones(2000, device="cuda")
+    return [
+        (lambda: armx.rms_norm_rows(x, w, residual=r, out=o, sum_out=s), (o, s), (x, r, w)),
+        (lambda: armx.rms_norm_rows_int8(x, w, residual=r, out=q, scales=sc, sum_out=s),
+         (q, sc, s), (x, r, w)),
+        (lambda: armx.quantize_rows_int8(x, out=q2, scales=sc2), (q2, sc2), (x,)),
+        (lambda: armx.rms_norm_rows_backward(dy, x, w, inv, dsum=r, out=d, dweight=dw), (d, dw),
+         (dy, x, w, inv, r)),
+        (lambda: armx.rms_norm_rows_backward(big, big, w, ones, dweight=dw, workspace=ws), (dw, ws),
+         (big, w, ones)),
+        (lambda: armx.matmul_int8(q, sa, q2, sa, out=y), (y,), (q, q2, sa)),
+    ]
+
+
+def test_outputs_count_as_written():
+    for call, outs, ins in every_output():
+        was = [t._version for t in outs + ins]
+        call()
+        now = [t._version for t in outs + ins]
+        n = len(outs)
+        assert all(b > a for a, b in zip(was[:n], now[:n])) and was[n:] == now[n:]
+    # a result made by the call is new, and a refused call writes nothing
+    x = torch.ones(4, 64, dtype=torch.float16, device="cuda")
+    w = torch.ones(64, dtype=torch.float16, device="cuda")
+    assert armx.rms_norm_rows(x, w).out._version == 0
+    was = x._version
+    with pytest.raises(armx.ArmxError):
+        armx.rms_norm_rows(x, w, out=x, eps=-1.0)
+    assert x._version == was
+
+
+def test_a_backward_pass_notices_what_was_written_over():
+    w = torch.ones(64, dtype=torch.float16, device="cuda")
+    for write in (lambda t: armx.rms_norm_rows(t, w, out=t),
+                  lambda t: armx.rms_norm_rows(t, w, residual=w.expand(4, 64).contiguous(), sum_out=t),
+                  lambda t: armx.rms_norm_rows_backward(t, t, w, torch.ones(4, device="cuda"), out=t)):
+        leaf = torch.ones(4, 64, dtype=torch.float16, device="cuda", requires_grad=True)
+        y = torch.sigmoid(leaf)             # saves its result
+        loss = y.sum()
+        write(y.detach())
+        with pytest.raises(RuntimeError, match="inplace|in-place"):
+            loss.backward()
+
+
+def test_outputs_made_in_inference_mode():
+    with torch.inference_mode():
+        calls = every_output()
+        for call, _, _ in calls:
+            call()
+    for call, _, _ in calls:
+        call()
+    torch.cuda.synchronize()
