@@ -375,7 +375,8 @@ PyObject* py_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Owned r;
   c10::DeviceGuard guard(c.device);
   c.cols = cols;
-  if (!output(c, a[5], "out", 1, type, &out, r, 0)) return nullptr;
+  // 16-bit rows as the norms and the quantiser read them
+  if (!output(c, a[5], "out", type == at::kFloat ? 1 : 8, type, &out, r, 0)) return nullptr;
   const int st = matmul_int8(static_cast<const int8_t*>(ar.p), ar.ld, static_cast<const float*>(as),
                              static_cast<const int8_t*>(br.p), br.ld, static_cast<const float*>(bs),
                              bias, size_t(m), size_t(cols), size_t(k), out.p, out.ld, int(code),

@@ -100,3 +100,25 @@ def test_outputs_made_in_inference_mode():
     for call, _, _ in calls:
         call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("m,n", [(1, 5), (2, 1), (7, 60), (33, 1003), (130, 4100)])
+def test_a_product_feeds_the_next_operator(m, n, dtype):
+    rng = np.random.default_rng([m, n])
+    a, b = (armx.quantize_rows_int8(make(rng, rows, 200, dtype, device="cuda")) for rows in (m, n))
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(n)).to(dtype).cuda()
+    y = armx.matmul_int8(*a, *b, dtype=dtype)
+    assert y.shape == (m, n)
+    wide = make(rng, m, n, dtype, device="cuda")      # the same values in a matrix of its own
+    wide.copy_(y)
+    flat = torch.empty(m, n, dtype=dtype, device="cuda")
+    assert torch.equal(armx.matmul_int8(*a, *b, out=flat), y)
+    r = make(rng, m, n, dtype, device="cuda")
+    for f in (lambda t: armx.rms_norm_rows(t, w, residual=r),
+              lambda t: armx.rms_norm_rows(r, w, residual=t),
+              lambda t: armx.rms_norm_rows_int8(t, w, residual=r), armx.quantize_rows_int8,
+              lambda t: armx.rms_norm_rows_backward(t, r, w, torch.ones(m, device="cuda"), dsum=t)):
+        for got, want in zip(f(y), f(wide)):
+            assert (got is None and want is None) or torch.equal(got, want)
+    assert armx.matmul_int8(*a, *b, dtype=torch.float32).is_contiguous()
