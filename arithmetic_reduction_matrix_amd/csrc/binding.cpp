@@ -116,13 +116,18 @@ Tensor make(const Call& c, at::IntArrayRef size, ScalarType type) {
   return at::empty(size, at::TensorOptions().dtype(type).device(c.device));
 }
 
-// A new matrix whose rows start at multiples of `multiple` values.
+// A new matrix whose rows start at multiples of `multiple` values: allocated with its
+// pitch as width, then given its own (a view of the wide one took 0.7 us more a call).
 Tensor make_rows(const Call& c, int64_t multiple, ScalarType type, Rows* out) {
   const int64_t pitch = (c.cols + multiple - 1) / multiple * multiple;
   Tensor t = make(c, {c.rows, pitch}, type);
   out->p = t.data_ptr();
   out->ld = size_t(pitch);
-  return pitch == c.cols ? t : t.narrow(1, 0, c.cols);
+  if (pitch != c.cols) {
+    const int64_t sizes[] = {c.rows, c.cols}, strides[] = {pitch, 1};
+    t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(sizes), at::IntArrayRef(strides));
+  }
+  return t;
 }
 
 // Rows of codes made here: at least 16 codes apart in multiples of 16, which the

@@ -8,7 +8,7 @@ summed exactly.  Matrices are 2-D with contiguous rows (``stride(1) == 1``);
 rows of 16-bit values start at multiples of 16 bytes (a row pitch that is a
 multiple of 8) and rows of codes too (a multiple of 16).  Matrices of both made here
 have such a pitch, so that one call's result is the next one's input, and results of
-odd width are views of wider ones (float32 products are contiguous).  Calls run
+odd width are not contiguous (float32 products are).  Calls run
 on the current stream of the inputs' device and record no autograd graph:
 ``rms_norm_rows_backward`` gives the norm's gradients.  A tensor given for a result
 counts as written in place, so that a backward pass which saved its old values raises.

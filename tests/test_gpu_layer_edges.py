@@ -122,3 +122,23 @@ def test_a_product_feeds_the_next_operator(m, n, dtype):
         for got, want in zip(f(y), f(wide)):
             assert (got is None and want is None) or torch.equal(got, want)
     assert armx.matmul_int8(*a, *b, dtype=torch.float32).is_contiguous()
+
+
+@pytest.mark.parametrize("cols", [1, 13, 1003, 5001])
+def test_results_of_odd_width(cols):
+    # their rows' pitch, the memory behind their last row, and what PyTorch makes of them
+    rng = np.random.default_rng(cols)
+    x = make(rng, 3, cols, torch.float16, device="cuda")
+    w = torch.ones(cols, dtype=torch.float16, device="cuda")
+    n = armx.rms_norm_rows(x, w, residual=x, keep_inv_rms=True)
+    q = armx.rms_norm_rows_int8(x, w, residual=x)
+    g = armx.rms_norm_rows_backward(x, n.sum, w, n.inv_rms)
+    for t, multiple in ((n.out, 8), (n.sum, 8), (q.sum, 8), (g.dx, 8), (q.codes, 16)):
+        pitch = t.stride(0)
+        assert t.shape == (3, cols) and t.stride(1) == 1 and t.storage_offset() == 0
+        assert pitch % multiple == 0 and pitch >= cols and not t.is_contiguous()
+        assert t.untyped_storage().nbytes() >= 3 * pitch * t.element_size()
+        assert t.numel() == 3 * cols and t._base is None
+        flat = torch.cat([t[i] for i in range(3)])
+        assert torch.equal(t.contiguous().view(-1), flat) and torch.equal(t.clone(), t)
+        assert torch.equal(t.cpu().reshape(-1), flat.cpu())
