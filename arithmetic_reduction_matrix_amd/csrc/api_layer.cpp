@@ -179,7 +179,8 @@ int rms_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh
                            const armx_config* cfg, void* stream) {
   int st = first_error(
       {check_type(type), check_cfg(cfg), check_sizes(rows, cols),
-       cols > armx::kMaxBackwardCols ? ARMX_ERR_SHAPE : ARMX_OK, check_matrix(dy, rows, cols, ldy, 16, 8), check_matrix(h, rows, cols, ldh, 16, 8),
+       cols > armx::kMaxBackwardCols ? ARMX_ERR_SHAPE : ARMX_OK,
+       check_matrix(dy, rows, cols, ldy, 16, 8), check_matrix(h, rows, cols, ldh, 16, 8),
        check_matrix(dsum, rows, cols, ldd, 16, 8, true),
        check_matrix(dx, rows, cols, ldx, 16, 8)});
   if (st != ARMX_OK) return st;

@@ -554,7 +554,10 @@ size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols,
  *                    compute-unit count (0 when nothing is launched)
  *   workspace_bytes  as armx_workspace_bytes
  *   lds_bytes        dynamic LDS per block of that launch
- *   launches         kernel launches the call enqueues
+ *   launches         kernel launches the call enqueues (ARMX_OP_RMS_BACKWARD
+ *                    of some rows without a workspace: one more, grid_blocks in
+ *                    the two together, where dx's memory from its first value
+ *                    to its last meets that of dy or h)
  * Without a device it assumes 256 compute units.  For the row operations
  * the plan is the one made with a workspace.  Returns ARMX_OK, or
  * ARMX_ERR_NULL (info NULL), ARMX_ERR_CONFIG or ARMX_ERR_SHAPE as the call
