@@ -89,6 +89,7 @@ int prepare_norm(const armx::NormArgs& a, bool norm, const armx_config* cfg, hip
   if (norm && a.rows && a.cols && !a.weight) return ARMX_ERR_NULL;
   if (norm && !aligned(a.weight, 16)) return ARMX_ERR_ALIGN;
   if (a.sum_out && !a.residual) return ARMX_ERR_CONFIG;
+  if (a.sum_out && a.sum_out == a.out && a.rows && a.cols) return ARMX_ERR_CONFIG;
   if (!aligned(a.inv_rms, 4) || !aligned(a.scales, 4)) return ARMX_ERR_ALIGN;
   if (a.rows == 0) return ARMX_OK;
   if (codes && !a.scales) return ARMX_ERR_NULL;

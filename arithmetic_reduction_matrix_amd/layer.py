@@ -108,8 +108,8 @@ def rms_norm_rows(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tens
     bfloat16, the sum rounded once and returned), times ``weight``.
 
     ``keep_inv_rms`` returns 1 / rms of every row (float32), which
-    ``rms_norm_rows_backward`` takes.  ``out`` and ``sum_out`` may be ``x`` or
-    ``residual`` themselves."""
+    ``rms_norm_rows_backward`` takes.  ``out`` and ``sum_out`` may each be ``x`` or
+    ``residual`` themselves, not both the same one."""
     return _done(_binding.rms_norm_rows(x, weight, residual, eps, keep_inv_rms, out, None, sum_out,
                                         _event_handle(start_event), _event_handle(stop_event)),
                  "rms_norm_rows", RmsNorm)

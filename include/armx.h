@@ -422,11 +422,12 @@ typedef enum armx_type {
  * sum_out      device, receives h; may be NULL (h is not written) and must be
  *              without a residual.
  * inv_rms      device, rows binary32 (inv, for the backward pass), or NULL.
- * out or sum_out may be x or residual themselves (same pointer and pitch);
- * nothing else may overlap.  A sum of squares past binary32's range counts as
+ * out and sum_out may each be x or residual themselves (same pointer and
+ * pitch), not both the same one; nothing else may overlap.  A sum of squares past binary32's range counts as
  * an infinity (inv 0); a NaN or an infinity in a row makes NaNs in that row.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other
- * than the two, or an eps that is negative or NaN, is ARMX_ERR_CONFIG.
+ * than the two, an eps that is negative or NaN, or an out that starts where
+ * sum_out does is ARMX_ERR_CONFIG.
  */
 int rms_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
                   const void* weight, int type, size_t rows, size_t cols, float eps, void* out,
