@@ -241,11 +241,17 @@ int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t
   // a single row's pitch is never used as one; keep it in range
   p.lda = m > 1 ? lda : 0, p.ldb = n > 1 ? ldb : 0, p.ldo = m > 1 ? ldo : n;
   p.out_type = out_type;
-  if (log_enabled())
-    std::fprintf(stderr, "armx: matmul_int8 m=%llu n=%llu k=%llu out_type=%d\n",
-                 (unsigned long long)m, (unsigned long long)n, (unsigned long long)k, out_type);
+  const int cu_count = armx::current_cu_count();
+  if (log_enabled()) {
+    const armx::MatmulTile t = armx::choose_matmul_tile(p, cu_count);
+    std::fprintf(stderr,
+                 "armx: matmul_int8 m=%llu n=%llu k=%llu out_type=%d tile=%dx%d groups=%d "
+                 "off_lines=%d\n",
+                 (unsigned long long)m, (unsigned long long)n, (unsigned long long)k, out_type,
+                 t.rows, t.cols, t.groups, int(t.off_lines));
+  }
   return hip_status(
-      armx::launch_matmul_int8(p, armx::current_cu_count(), cfg, static_cast<hipStream_t>(stream)));
+      armx::launch_matmul_int8(p, cu_count, cfg, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -87,6 +87,15 @@ struct MatmulArgs {
   int out_type = ARMX_F16;
 };
 
+// The tile of out that a block of the product makes, and over how many groups of its
+// wavefronts k is split.
+struct MatmulTile {
+  int rows, cols, groups;
+  bool off_lines;  // rows of codes do not all start on a 128-byte line
+  int index;       // in its table
+};
+MatmulTile choose_matmul_tile(const MatmulArgs& args, int cu_count);
+
 // Each launches on the current device and stream with the call's events.
 hipError_t launch_norm(const NormArgs& args, const armx_config* cfg, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackwardArgs& args, const NormBackwardPlan& plan,

@@ -610,10 +610,9 @@ int choose_tile(const TileTime (&tiles)[11], const MatmulArgs& p, int cu_count) 
 template <int OUT>
 hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cfg,
                         hipStream_t stream) {
-  const uint64_t starts = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) |
-                          p.lda | p.ldb;
-  if (starts % 128 == 0) {
-    switch (choose_tile(kTiles, p, cu_count)) {
+  const MatmulTile tile = choose_matmul_tile(p, cu_count);
+  if (!tile.off_lines) {
+    switch (tile.index) {
       case 0: return launch_tiled<OUT, 256, 256, 2, 4, 1, 2>(p, cfg, stream);
       case 1: return launch_tiled<OUT, 192, 192, 4, 2, 1, 3>(p, cfg, stream);
       case 2: return launch_tiled<OUT, 128, 256, 2, 4, 1, 3>(p, cfg, stream);
@@ -627,7 +626,7 @@ hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cf
       case 10: return launch_tiled<OUT, 16, 16, 1, 1, 8, 4>(p, cfg, stream);
     }
   } else {
-    switch (choose_tile(kOffLineTiles, p, cu_count)) {
+    switch (tile.index) {
       case 0: return launch_tiled<OUT, 256, 256, 2, 4, 1, 2>(p, cfg, stream);
       case 1: return launch_tiled<OUT, 192, 192, 4, 2, 1, 3, true>(p, cfg, stream);
       case 2: return launch_tiled<OUT, 128, 256, 2, 4, 1, 3>(p, cfg, stream);
@@ -645,6 +644,16 @@ hipError_t launch_typed(const MatmulArgs& p, int cu_count, const armx_config* cf
 }
 
 }  // namespace
+
+MatmulTile choose_matmul_tile(const MatmulArgs& p, int cu_count) {
+  const uint64_t starts = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) |
+                          p.lda | p.ldb;
+  const bool off = starts % 128 != 0;
+  const TileTime(&tiles)[11] = off ? kOffLineTiles : kTiles;
+  const int i = choose_tile(tiles, p, cu_count);
+  if (i < 0) return {0, 0, 0, off, i};
+  return {tiles[i].bm, tiles[i].bn, tiles[i].ks, off, i};
+}
 
 hipError_t launch_matmul_int8(const MatmulArgs& args, int cu_count, const armx_config* cfg,
                               hipStream_t stream) {
