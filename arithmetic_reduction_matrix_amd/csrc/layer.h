@@ -27,10 +27,16 @@ struct RowShape {
 RowShape row_shape(uint64_t cols);
 constexpr int kRowBlock = 256;  // threads per block of rows of at most a wavefront
 
-// Results of at least this many values are written past the caches: they are more
-// than the 32 MiB of L2 would keep for a reader, and written so they take less of
-// HBM's time (MI355X, us: 8192 x 4096 norm 49.3 -> 47.6, to codes 44.7 -> 42.5;
-// 8192 x 8192 to codes 86.3 -> 81.5; 16384 x 1024 27.8 -> 21.1).
+// Results of at least this many values are written past the caches: 16-bit ones of
+// 32 MiB, what the L2s hold together, and codes of half of that.  Written so they take
+// less of HBM's time (MI355X, us, through the caches / past them: norm of 8192 x 4096
+// 47.6 / 46.4, 16384 x 1024 24.7 / 21.0, 17000 x 1001 25.9 / 22.6; to codes 8192 x 4096
+// 44.9 / 43.6, 17000 x 1001 22.7 / 21.8, 335544 x 100 70.3 / 59.4; gradients of 17000 x
+// 1001 28.7 / 27.8), except on narrow rows, whose tails and neighbours complete the same
+// lines (norm of 335544 x 100 78.2 / 79.0, 1016800 x 33 104.7 / 108.8).  What reads them
+// next finds less in the caches: codes of a norm and their product with 256 rows, both
+// calls, 8192 x 4096 57.2 / 61.7, 4096 x 8192 56.0 / 64.0, 17000 x 1001 33.6 / 34.0; a
+// norm and its codes 16384 x 1024 37.5 / 34.7, 335544 x 100 101.9 / 107.3.
 constexpr uint64_t kStreamValues = uint64_t(1) << 24;
 
 struct NormArgs {

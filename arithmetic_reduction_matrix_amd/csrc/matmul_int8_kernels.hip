@@ -539,26 +539,25 @@ hipError_t launch_tiled(const MatmulArgs& p, const armx_config* cfg, hipStream_t
 // loads, its epilogue) and, per step of KS x 128 codes, `alone` or, with several
 // blocks on the unit, `each` of them if that is more.  The constants (us) are
 // fitted to times of each tile on MI355X over 192 shapes of 1 to 8192 rows, 128 to
-// 28672 columns and lengths of 128 to 14336; the tile they choose is 1.3% behind
-// the fastest of all 29 measured on average and 17% at worst.  Each of the eleven
-// pays where it is chosen (us, it and the best of the others): 256 x 256 at
-// 4096 x 4096 x 14336 177 (208); 192 x 192 at 2048 x 4096 x 14336 103 (108);
-// 128 x 256 at 512 x 14336 x 4096 36.8 (39.0); 192 x 128 at 1500 x 4096 x 14336 83
-// (97); 128 x 128 at 1024 x 4096 x 14336 68.5 (79.4); 64 x 128 at 512 x 4096 x 14336
-// 51.9 (58.9); 64 x 64 at 256 x 4096 x 14336 35.6 (45.6); 64 x 32 at
-// 128 x 4096 x 14336 26.3 (35.6); 32 x 32 at 48 x 4096 x 14336 19.2 (25.0);
-// 16 x 32 at 16 x 8192 x 8192 15.1 (15.7 and more); 16 x 16 at 16 x 4096 x 14336
-// 13.7 (18.4).
+// 28672 columns and lengths of 128 to 14336.  All eleven timed at 192 shapes of that
+// range, the one they choose is 0.6% behind the fastest on average and 11% at worst.
+// Each pays where it is chosen (us, it and the best of the others): 256 x 256 at
+// 4096 x 4096 x 14336 175 (212); 192 x 192 at 2048 x 4100 x 5001 44.1 (56.5);
+// 128 x 256 at 8192 x 1024 x 8192 61.4 (80.3); 192 x 128 at 1024 x 4100 x 5001 28.2
+// (33.1); 128 x 128 at 1024 x 4096 x 14336 67.8 (78.0); 64 x 128 at 512 x 4096 x 14336
+// 49.9 (58.6); 64 x 64 at 256 x 4096 x 14336 35.4 (44.8); 64 x 32 at
+// 128 x 4096 x 14336 25.7 (34.9); 32 x 32 at 33 x 4096 x 14336 17.0 (22.3);
+// 16 x 32 at 128 x 1024 x 8192 7.3 (8.3); 16 x 16 at 16 x 4096 x 14336 13.4 (18.2).
 //
 // Where rows do not all start on a 128-byte line, a step of a row lies in two lines,
 // and each is moved twice; the tiles with SHIFT move it once (us, without and with it,
 // at a pitch of k rounded up to 16: 128 x 128 at 777 x 4096 x 4112 24.2, 20.1;
 // 192 x 128 at 1500 x 4096 x 14336 + 16 117, 84), and their times and those of the
-// others at such rows are in a table of their own.  Fitted over 195 shapes of 1 to
-// 8192 rows, the tiles it chooses are 0.9% behind the fastest of all 22 measured on
-// average and 12% at worst; without the shifted ones 8.2% and up to 40%.  256 x 256
-// has no room for a third buffer, and on 16 and 32 rows, whose lines stay in the
-// first cache until their second use, the split along k pays more.
+// others at such rows are in a table of their own.  The tiles it chooses are 0.7%
+// behind the fastest of the eleven on average and 24% at worst (1 x 12288 x 1024,
+// 6.9 us; over the same shapes, at pitches off the lines).  256 x 256 has no room for a
+// third buffer, and on 16 and 32 rows, whose lines stay in the first cache until their
+// second use, the split along k pays more.
 struct TileTime {
   int bm, bn, ks, resident;
   float fixed, alone, each;

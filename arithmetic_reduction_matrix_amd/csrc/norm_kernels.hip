@@ -259,10 +259,11 @@ struct CodeScale {
 // the sum's low byte.
 //
 // NARROW (p of at most 11 bits, a value of a 16-bit type): a v that is no half lies
-// at least 2^-9 |v| / 127 from one, since 2 * 127 p and every odd multiple of top
-// are whole multiples of the smaller's last bit; only true halves, which are common
-// (one value in some tens where top has few bits), need care.  One correction,
-// t + (127 p - t top) / top with the difference exact, gives them exactly.
+// at least 2^-12 |v| / 127 from one (bfloat16's 8 bits: 2^-9), since 2 * 127 p and every
+// odd multiple of top are whole multiples of the smaller's last bit; only true halves,
+// which are common (one value in some tens where top has few bits), need care.  One
+// correction, t + (127 p - t top) / top with the difference exact, gives them exactly and
+// any other v to 2^-24 |v|.
 //
 // Otherwise t rounds as v does unless it is within 2^-14 of a half.  There 254 |p|
 // is compared with the odd multiple m of top: hi + lo = m top and e = 254 |p| - hi
@@ -452,7 +453,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& k, uint64_t row, floa
 // codes of 8192 x 8192 79.3, 5.9; codes of 16384 x 8192 70.0, 5.8), and the chain of
 // a load, a combine and a store where there are few (1 x 4096 2.5 us, 64 x 14336
 // 4.8).  Odd and narrow rows pay for the lanes without a chunk and for lines shared
-// by rows (335544 x 100 at a pitch of 104: norm 79 us, half the rate).
+// by rows (335544 x 100 at a pitch of 104: norm 79 us, 3.4 TB/s).
 template <int TYPE, int OUT, bool RES, bool STREAM, class L>
 __global__ __launch_bounds__(L::kMax) void norm_kernel(NormArgs k) {
   constexpr int C = L::kChunks;

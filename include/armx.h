@@ -513,7 +513,7 @@ int rms_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh
  * out       device, m x n of out_type (ARMX_F16, ARMX_BF16 or ARMX_F32), any
  *           pitch and any alignment its type has.
  * k         at most 131071, so that no sum of products can leave 32 bits;
- *           k == 0 gives the bias (or 0) where both scales are finite.
+ *           k == 0 gives the bias (or 0) where the scales' product is finite.
  * lda, ldb  at most 2^23; m and n at most 2^30, and ceil(m / 256) * ceil(n / 256)
  *           at most 2097151.
  * Needs no workspace.  Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}.
