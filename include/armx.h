@@ -421,10 +421,13 @@ typedef enum armx_type {
  * out          device, rows x cols.
  * sum_out      device, receives h; may be NULL (h is not written) and must be
  *              without a residual.
- * inv_rms      device, rows binary32 (inv, for the backward pass), or NULL.
+ * inv_rms      device, rows binary32 (inv, for the backward pass; 0 when cols is 0),
+ *              or NULL.
  * out and sum_out may each be x or residual themselves (same pointer and
- * pitch), not both the same one; nothing else may overlap.  A sum of squares past binary32's range counts as
- * an infinity (inv 0); a NaN or an infinity in a row makes NaNs in that row.
+ * pitch), not both the same one; nothing else may overlap.  A sum of squares
+ * past binary32's range counts as an infinity (inv 0); a NaN or an infinity in
+ * a row makes NaNs in that row.  Squares below binary32's normal range
+ * (magnitudes under 2^-63) lose bits, which counts where eps is below 2^-100.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other
  * than the two, an eps that is negative or NaN, or an out that starts where
  * sum_out does is ARMX_ERR_CONFIG.
