@@ -23,7 +23,6 @@ import torch   # before the module that is linked against it
 from . import Config, _check, _event_handle, lib
 
 
-
 class _NotLoaded:
     """Stands for the module of the calls where it does not load: the sums do not need
     it, so only these calls raise."""
