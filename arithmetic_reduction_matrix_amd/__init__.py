@@ -39,7 +39,10 @@ __all__ = [
     "PlanInfo", "LIB_PATH",
     "rms_norm_rows", "rms_norm_rows_int8", "rms_norm_rows_backward", "quantize_rows_int8",
     "matmul_int8", "RmsNorm", "RmsNormInt8", "RmsNormGrads", "RowCodes",
+    "dropout_rows", "layer_norm_rows", "layer_norm_rows_backward", "Dropout", "LayerNorm",
+    "LayerNormGrads",
     "OP_SUM", "OP_ROWS", "OP_FIXED", "OP_ROWS_FIXED", "OP_EXACT", "OP_RMS_BACKWARD",
+    "OP_LAYER_NORM_BACKWARD",
     "FLAG_PLAIN", "FLAG_CACHED_LOADS", "FLAG_ONE_CHAIN", "FLAG_TWO_PASS", "FLAG_MMA_LEVELS",
     "FLAG_MMA_LEAVES", "FLAG_ALL_ONES", "FLAG_INT_LIMBS",
 ]
@@ -47,6 +50,7 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libarmx.so")
 
 OP_SUM, OP_ROWS, OP_FIXED, OP_ROWS_FIXED, OP_EXACT, OP_RMS_BACKWARD = 0, 1, 2, 3, 4, 5
+OP_LAYER_NORM_BACKWARD = 6
 FLAG_PLAIN, FLAG_CACHED_LOADS, FLAG_ONE_CHAIN, FLAG_TWO_PASS = 0x1, 0x2, 0x4, 0x8
 FLAG_MMA_LEVELS = 0x10
 FLAG_MMA_LEAVES = 0x20
@@ -366,3 +370,5 @@ def reduce_rows_fixed_order(x: torch.Tensor, *, out: torch.Tensor | None = None,
 from .layer import (  # noqa: E402  (needs the names above)
     RmsNorm, RmsNormGrads, RmsNormInt8, RowCodes, matmul_int8, quantize_rows_int8,
     rms_norm_rows, rms_norm_rows_backward, rms_norm_rows_int8)
+from .training import (  # noqa: E402
+    Dropout, LayerNorm, LayerNormGrads, dropout_rows, layer_norm_rows, layer_norm_rows_backward)

@@ -119,11 +119,16 @@ hipError_t launch_row_plans(const armx::RowPlans& plans, const void* x, float* o
 }
 
 // The plan of rms_norm_rows_backward, which takes no configuration but events.
-int plan_backward(size_t rows, size_t cols, const armx_config* cfg, armx::NormBackwardPlan* p) {
+bool is_backward(int op) { return op == ARMX_OP_RMS_BACKWARD || op == ARMX_OP_LAYER_NORM_BACKWARD; }
+
+int plan_backward(int op, size_t rows, size_t cols, const armx_config* cfg,
+                  armx::NormBackwardPlan* p) {
   if (cfg && (cfg->block_threads || cfg->chain_r || cfg->grid_blocks || cfg->flags))
     return ARMX_ERR_CONFIG;
   if (rows > armx::kMaxN || cols > armx::kMaxBackwardCols) return ARMX_ERR_SHAPE;
-  *p = armx::plan_norm_backward(rows, cols, rows && cols ? current_cu_count() : 256);
+  const int cus = rows && cols ? current_cu_count() : 256;
+  *p = op == ARMX_OP_RMS_BACKWARD ? armx::plan_norm_backward(rows, cols, cus)
+                                  : armx::plan_layer_norm_backward(rows, cols, cus);
   return ARMX_OK;
 }
 
@@ -225,9 +230,9 @@ int reduce_rows_fixed_order(const void* x, size_t rows, size_t cols, size_t ld, 
 
 size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols, const armx_config* cfg) {
   armx::Plan plan;
-  if (op == ARMX_OP_RMS_BACKWARD) {
+  if (is_backward(op)) {
     armx::NormBackwardPlan p;
-    return plan_backward(n_or_rows, cols, cfg, &p) == ARMX_OK ? p.ws_bytes : size_t(-1);
+    return plan_backward(op, n_or_rows, cols, cfg, &p) == ARMX_OK ? p.ws_bytes : size_t(-1);
   }
   if (op != ARMX_OP_SUM && op != ARMX_OP_ROWS && op != ARMX_OP_FIXED &&
       op != ARMX_OP_ROWS_FIXED && op != ARMX_OP_EXACT)
@@ -250,9 +255,9 @@ size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols, const armx_co
 int armx_launch_plan(int op, size_t n_or_rows, size_t cols, const armx_config* cfg,
                      armx_plan_info* info) {
   if (!info) return ARMX_ERR_NULL;
-  if (op == ARMX_OP_RMS_BACKWARD) {
+  if (is_backward(op)) {
     armx::NormBackwardPlan p;
-    const int st = plan_backward(n_or_rows, cols, cfg, &p);
+    const int st = plan_backward(op, n_or_rows, cols, cfg, &p);
     if (st != ARMX_OK) return st;
     armx_plan_info r{};
     r.workspace_bytes = p.ws_bytes;

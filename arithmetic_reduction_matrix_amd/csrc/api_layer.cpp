@@ -16,6 +16,7 @@ namespace {
 
 constexpr uint64_t kMaxElements = uint64_t(1) << 40;
 constexpr uint64_t kMaxCols = uint64_t(1) << 30;     // exclusive: 32-bit byte offsets
+constexpr uint64_t kMaxDropoutRows = uint64_t(1) << 32;  // a word of the counter
 constexpr uint64_t kMaxProductK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr uint64_t kMaxProductLd = uint64_t(1) << 23;
 constexpr uint64_t kMaxProductRows = uint64_t(1) << 30;
@@ -98,6 +99,24 @@ int prepare_norm(const armx::NormArgs& a, bool norm, const armx_config* cfg, hip
     return zeros ? hip_status(armx::launch_zero(zeros, a.rows, stream)) : ARMX_OK;
   }
   *done = false;
+  return ARMX_OK;
+}
+
+// A dropout as the kernels take it.
+int check_dropout(const armx_dropout* d, uint64_t rows, armx::DropoutArgs* out) {
+  if (!d) return ARMX_OK;
+  if (!(d->p >= 0.0 && d->p <= 1.0)) return ARMX_ERR_CONFIG;
+  if (!aligned(d->step, 8)) return ARMX_ERR_ALIGN;
+  if (d->first_row > kMaxDropoutRows || rows > kMaxDropoutRows - d->first_row)
+    return ARMX_ERR_SHAPE;
+  out->key0 = uint32_t(d->seed);
+  out->key1 = uint32_t(d->seed >> 32);
+  out->offset = d->offset;
+  out->step = d->step;
+  out->first_row = uint32_t(d->first_row);
+  out->limit = uint32_t(d->p * 65536.0 + 0.5);
+  // all dropped: nothing is ever multiplied by it
+  out->scale = out->limit < 65536 ? float(65536.0 / (65536.0 - double(out->limit))) : 0.0f;
   return ARMX_OK;
 }
 
@@ -213,6 +232,122 @@ int rms_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh
   a.type = type;
   log_rows("rms_norm_rows_backward", rows, cols, type);
   return hip_status(armx::launch_norm_backward(a, plan, cfg, s));
+}
+
+int dropout_rows(const void* x, size_t ldx, const void* residual, size_t ldr, int type,
+                 size_t rows, size_t cols, const armx_dropout* dropout, void* out, size_t ldo,
+                 const armx_config* cfg, void* stream) {
+  armx::LayerNormArgs a;
+  if (!dropout) return ARMX_ERR_NULL;
+  const int st = first_error(
+      {check_type(type), check_cfg(cfg), check_sizes(rows, cols),
+       check_dropout(dropout, rows, &a.dropout), check_matrix(x, rows, cols, ldx, 16, 8),
+       check_matrix(residual, rows, cols, ldr, 16, 8, true),
+       check_matrix(out, rows, cols, ldo, 16, 8)});
+  if (st != ARMX_OK || rows == 0 || cols == 0) return st;
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.out = static_cast<uint16_t*>(out);
+  a.rows = rows, a.cols = cols;
+  a.ldx = ldx, a.ldr = ldr, a.ldo = ldo;
+  a.type = type;
+  a.drop = true;
+  log_rows("dropout_rows", rows, cols, type);
+  return hip_status(armx::launch_layer_norm(a, cfg, static_cast<hipStream_t>(stream)));
+}
+
+int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
+                    const void* weight, const void* bias, int type, size_t rows, size_t cols,
+                    float eps, const armx_dropout* dropout, void* out, size_t ldo, void* sum_out,
+                    size_t lds, float* mean, float* inv_std, const armx_config* cfg,
+                    void* stream) {
+  armx::LayerNormArgs a;
+  const int st = first_error(
+      {check_type(type), check_cfg(cfg), !(eps >= 0.0f) ? ARMX_ERR_CONFIG : ARMX_OK,
+       check_sizes(rows, cols), check_dropout(dropout, rows, &a.dropout),
+       check_matrix(x, rows, cols, ldx, 16, 8),
+       check_matrix(residual, rows, cols, ldr, 16, 8, true),
+       check_matrix(out, rows, cols, ldo, 16, 8),
+       check_matrix(sum_out, rows, cols, lds, 16, 8, true)});
+  if (st != ARMX_OK) return st;
+  if (rows && cols && !weight) return ARMX_ERR_NULL;
+  if (!aligned(weight, 16) || !aligned(bias, 16)) return ARMX_ERR_ALIGN;
+  if (sum_out && !residual && !dropout) return ARMX_ERR_CONFIG;
+  if (sum_out && sum_out == out && rows && cols) return ARMX_ERR_CONFIG;
+  if (!aligned(mean, 4) || !aligned(inv_std, 4)) return ARMX_ERR_ALIGN;
+  if (rows == 0) return ARMX_OK;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (cols == 0) {
+    for (float* zeros : {mean, inv_std}) {
+      const hipError_t e = zeros ? armx::launch_zero(zeros, rows, s) : hipSuccess;
+      if (e != hipSuccess) return ARMX_ERR_HIP;
+    }
+    return ARMX_OK;
+  }
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.out = static_cast<uint16_t*>(out);
+  a.sum_out = static_cast<uint16_t*>(sum_out);
+  a.mean = mean, a.inv_std = inv_std;
+  a.rows = rows, a.cols = cols;
+  a.ldx = ldx, a.ldr = ldr, a.ldo = ldo, a.lds = lds;
+  a.eps = eps, a.type = type;
+  a.drop = dropout != nullptr;
+  log_rows("layer_norm_rows", rows, cols, type);
+  return hip_status(armx::launch_layer_norm(a, cfg, s));
+}
+
+int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh,
+                             const void* weight, const float* mean, const float* inv_std,
+                             const void* dsum, size_t ldd, int type, size_t rows, size_t cols,
+                             const armx_dropout* dropout, void* dx, size_t ldx, void* dresidual,
+                             size_t ldr, float* dweight, float* dbias, void* ws,
+                             size_t ws_bytes, const armx_config* cfg, void* stream) {
+  armx::LayerNormBackwardArgs a;
+  const int st = first_error(
+      {check_type(type), check_cfg(cfg), check_sizes(rows, cols),
+       cols > armx::kMaxBackwardCols ? ARMX_ERR_SHAPE : ARMX_OK,
+       check_dropout(dropout, rows, &a.dropout), check_matrix(dy, rows, cols, ldy, 16, 8),
+       check_matrix(h, rows, cols, ldh, 16, 8), check_matrix(dsum, rows, cols, ldd, 16, 8, true),
+       check_matrix(dx, rows, cols, ldx, 16, 8),
+       check_matrix(dresidual, rows, cols, ldr, 16, 8, true)});
+  if (st != ARMX_OK) return st;
+  if (dresidual && !dropout) return ARMX_ERR_CONFIG;
+  if (dresidual && dresidual == dx && rows && cols) return ARMX_ERR_CONFIG;
+  if (cols == 0) return ARMX_OK;
+  if (!dweight || !dbias) return ARMX_ERR_NULL;
+  if (!aligned(dweight, 4) || !aligned(dbias, 4)) return ARMX_ERR_ALIGN;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows == 0) {
+    const hipError_t e = armx::launch_zero(dweight, cols, s);
+    return hip_status(e == hipSuccess ? armx::launch_zero(dbias, cols, s) : e);
+  }
+  if (!weight || !mean || !inv_std) return ARMX_ERR_NULL;
+  if (!aligned(weight, 16) || !aligned(mean, 4) || !aligned(inv_std, 4)) return ARMX_ERR_ALIGN;
+  const armx::NormBackwardPlan plan =
+      armx::plan_layer_norm_backward(rows, cols, armx::current_cu_count());
+  if (plan.ws_bytes) {
+    if (!ws) return ARMX_ERR_NULL;
+    if (!aligned(ws, 256)) return ARMX_ERR_ALIGN;
+    if (ws_bytes < plan.ws_bytes) return ARMX_ERR_WORKSPACE;
+  }
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.h = static_cast<const uint16_t*>(h);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.mean = mean, a.inv_std = inv_std;
+  a.dsum = static_cast<const uint16_t*>(dsum);
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dresidual = static_cast<uint16_t*>(dresidual);
+  a.dweight = dweight, a.dbias = dbias;
+  a.partials = static_cast<float*>(ws);
+  a.rows = rows, a.cols = cols;
+  a.ldy = ldy, a.ldh = ldh, a.ldd = ldd, a.ldx = ldx, a.ldr = ldr;
+  a.type = type;
+  a.drop = dropout != nullptr;
+  log_rows("layer_norm_rows_backward", rows, cols, type);
+  return hip_status(armx::launch_layer_norm_backward(a, plan, cfg, s));
 }
 
 int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t* b, size_t ldb,

@@ -145,8 +145,8 @@ void written(PyObject* o) {
 // Owned references that are released unless handed on; `given`: to the caller's own
 // tensors.
 struct Owned {
-  PyObject* o[3] = {nullptr, nullptr, nullptr};
-  bool given[3] = {false, false, false};
+  PyObject* o[4] = {nullptr, nullptr, nullptr, nullptr};
+  bool given[4] = {false, false, false, false};
   ~Owned() {
     for (PyObject* p : o) Py_XDECREF(p);
   }
@@ -214,6 +214,34 @@ bool arity(const char* name, Py_ssize_t got, Py_ssize_t want) {
 }
 
 void* stream_of(const Call& c) { return c10::hip::getCurrentHIPStream(c.device.index()).stream(); }
+
+// A call's workspace: the caller's, or one from the allocator, which knows streams and
+// graph captures (it needs no zeros, so nothing is gained by keeping one).
+struct Workspace {
+  Tensor space;
+  void* p = nullptr;
+  size_t bytes = 0;
+  bool too_large = false;   // the call takes no such sizes
+  bool take(const Call& c, PyObject* given, size_t need) {
+    if (given == Py_None) {
+      too_large = need == size_t(-1);
+      if (too_large) return false;
+      if (need) space = make(c, {int64_t(need)}, at::kByte);
+      p = need ? space.data_ptr() : nullptr;
+      bytes = need;
+      return true;
+    }
+    const Tensor* t = tensor(given);
+    if (!t || t->device() != c.device || !t->is_contiguous()) {
+      PyErr_Format(PyExc_ValueError, "%s: workspace must be a contiguous tensor on %s", c.name,
+                   c.device.str().c_str());
+      return false;
+    }
+    p = t->data_ptr();
+    bytes = t->nbytes();
+    return true;
+  }
+};
 
 // (x, weight, residual, eps, keep_inv_rms | None, out, scales, sum_out, start, stop);
 // codes: rms_norm_rows_int8, whose `out` is int8
@@ -292,7 +320,7 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Call c{"rms_norm_rows_backward"};
   Rows dy, h, ds, dx;
-  void *w = nullptr, *inv = nullptr, *dw = nullptr, *ws = nullptr;
+  void *w = nullptr, *inv = nullptr, *dw = nullptr;
   if (!arity(c.name, n, 10) || !first(c, a[0], "dy", false) ||
       !matrix(c, a[0], "dy", c.rows, c.cols, c.type, &dy) ||
       !matrix(c, a[1], "h", c.rows, c.cols, c.type, &h) ||
@@ -306,30 +334,163 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!output(c, a[5], "out", 8, c.type, &dx, r, 0) ||
       !vector_output(c, a[6], "dweight", c.cols, &dw, r, 1))
     return nullptr;
-  Tensor space;   // from the allocator, which knows streams and graph captures: it
-                  // needs no zeros, so nothing is gained by keeping one
-  size_t ws_bytes = 0;
-  if (a[7] == Py_None) {
-    ws_bytes = armx_workspace_bytes(ARMX_OP_RMS_BACKWARD, size_t(c.rows), size_t(c.cols), nullptr);
-    if (ws_bytes == size_t(-1)) return PyLong_FromLong(ARMX_ERR_SHAPE);
-    if (ws_bytes) space = make(c, {int64_t(ws_bytes)}, at::kByte);
-    ws = ws_bytes ? space.data_ptr() : nullptr;
-  } else {
-    const Tensor* t = tensor(a[7]);
-    if (!t || t->device() != c.device || !t->is_contiguous()) {
-      PyErr_Format(PyExc_ValueError, "%s: workspace must be a contiguous tensor on %s", c.name,
-                   c.device.str().c_str());
-      return nullptr;
-    }
-    ws = t->data_ptr();
-    ws_bytes = t->nbytes();
-  }
+  Workspace ws;
+  if (!ws.take(c, a[7], armx_workspace_bytes(ARMX_OP_RMS_BACKWARD, size_t(c.rows), size_t(c.cols),
+                                             nullptr)))
+    return ws.too_large ? PyLong_FromLong(ARMX_ERR_SHAPE) : nullptr;
   const int st = rms_norm_rows_backward(
       dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(inv), ds.p, ds.ld, type_code(c.type),
-      size_t(c.rows), size_t(c.cols), dx.p, dx.ld, static_cast<float*>(dw), ws, ws_bytes,
+      size_t(c.rows), size_t(c.cols), dx.p, dx.ld, static_cast<float*>(dw), ws.p, ws.bytes,
       c.has_cfg ? &c.cfg : nullptr, stream_of(c));
-  if (st == ARMX_OK && ws_bytes && a[7] != Py_None) written(a[7]);
+  if (st == ARMX_OK && ws.bytes && a[7] != Py_None) written(a[7]);
   return r.done(st, 2);
+  END_HANDLE_TH_ERRORS
+}
+
+// A Dropout (p, seed, offset, step, first_row), or None where `optional`: *given says
+// which.
+bool dropout(const Call& c, PyObject* o, bool optional, armx_dropout* d, bool* given) {
+  *given = o != Py_None;
+  if (!*given && optional) return true;
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) {
+    PyErr_Format(PyExc_TypeError, "%s: dropout must be a Dropout", c.name);
+    return false;
+  }
+  d->p = PyFloat_AsDouble(PyTuple_GET_ITEM(o, 0));
+  if (d->p == -1.0 && PyErr_Occurred()) return false;
+  if (!(d->p >= 0.0 && d->p <= 1.0)) {
+    PyErr_Format(PyExc_ValueError, "%s: dropout's p must be from 0 to 1", c.name);
+    return false;
+  }
+  const char* names[] = {"seed", "offset", "first_row"};
+  uint64_t* to[] = {&d->seed, &d->offset, &d->first_row};
+  const int at[] = {1, 2, 4};
+  for (int i = 0; i < 3; ++i) {
+    PyObject* v = PyTuple_GET_ITEM(o, at[i]);
+    if (!PyLong_Check(v)) {
+      PyErr_Format(PyExc_TypeError, "%s: dropout's %s must be an int", c.name, names[i]);
+      return false;
+    }
+    *to[i] = PyLong_AsUnsignedLongLong(v);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      PyErr_Format(PyExc_ValueError, "%s: dropout's %s must be from 0 to 2^64 - 1", c.name,
+                   names[i]);
+      return false;
+    }
+  }
+  void* step = nullptr;
+  if (PyTuple_GET_ITEM(o, 3) != Py_None &&
+      !vector(c, PyTuple_GET_ITEM(o, 3), "dropout's step", 1, at::kLong, &step))
+    return false;
+  d->step = static_cast<const uint64_t*>(step);
+  return true;
+}
+
+// (x, weight, bias, residual, dropout, eps, keep_stats, out, sum_out, start, stop)
+PyObject* py_layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c{"layer_norm_rows"};
+  Rows x, res, out, sum;
+  void *w = nullptr, *b = nullptr, *mean = nullptr, *inv = nullptr;
+  armx_dropout drop;
+  bool drops = false;
+  if (!arity(c.name, n, 11) || !first(c, a[0], "x", false) ||
+      !matrix(c, a[0], "x", c.rows, c.cols, c.type, &x) ||
+      !vector(c, a[1], "weight", c.cols, c.type, &w) ||
+      (a[2] != Py_None && !vector(c, a[2], "bias", c.cols, c.type, &b)) ||
+      (a[3] != Py_None && !matrix(c, a[3], "residual", c.rows, c.cols, c.type, &res)) ||
+      !dropout(c, a[4], true, &drop, &drops))
+    return nullptr;
+  const double eps = PyFloat_AsDouble(a[5]);
+  if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+  const int keep = PyObject_IsTrue(a[6]);
+  if (keep < 0 || !events(c, a[9], a[10])) return nullptr;
+  Owned r;   // out, sum, mean, inv_std
+  c10::DeviceGuard guard(c.device);
+  if (a[3] != Py_None || drops) {
+    if (!output(c, a[8], "sum_out", 8, c.type, &sum, r, 1)) return nullptr;
+  } else if (a[8] != Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s: sum_out goes with a residual or a dropout", c.name);
+    return nullptr;
+  }
+  if (!output(c, a[7], "out", 8, c.type, &out, r, 0)) return nullptr;
+  if (keep && (!vector_output(c, Py_None, "mean", c.rows, &mean, r, 2) ||
+               !vector_output(c, Py_None, "inv_std", c.rows, &inv, r, 3)))
+    return nullptr;
+  const int st = layer_norm_rows(
+      x.p, x.ld, res.p, res.ld, w, b, type_code(c.type), size_t(c.rows), size_t(c.cols),
+      float(eps), drops ? &drop : nullptr, out.p, out.ld, sum.p, sum.ld,
+      static_cast<float*>(mean), static_cast<float*>(inv), c.has_cfg ? &c.cfg : nullptr,
+      stream_of(c));
+  return r.done(st, 4);
+  END_HANDLE_TH_ERRORS
+}
+
+// (dy, h, weight, mean, inv_std, dsum, dropout, out, dresidual, dweight, dbias, workspace,
+// start, stop)
+PyObject* py_layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c{"layer_norm_rows_backward"};
+  Rows dy, h, ds, dx, dr;
+  void *w = nullptr, *mean = nullptr, *inv = nullptr, *dw = nullptr, *db = nullptr;
+  armx_dropout drop;
+  bool drops = false;
+  if (!arity(c.name, n, 14) || !first(c, a[0], "dy", false) ||
+      !matrix(c, a[0], "dy", c.rows, c.cols, c.type, &dy) ||
+      !matrix(c, a[1], "h", c.rows, c.cols, c.type, &h) ||
+      !vector(c, a[2], "weight", c.cols, c.type, &w) ||
+      !vector(c, a[3], "mean", c.rows, at::kFloat, &mean) ||
+      !vector(c, a[4], "inv_std", c.rows, at::kFloat, &inv) ||
+      (a[5] != Py_None && !matrix(c, a[5], "dsum", c.rows, c.cols, c.type, &ds)) ||
+      !dropout(c, a[6], true, &drop, &drops) || !events(c, a[12], a[13]))
+    return nullptr;
+  if (!drops && a[8] != Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s: dresidual goes with a dropout (dx is both without)",
+                 c.name);
+    return nullptr;
+  }
+  Owned r;   // dx, dweight, dbias, dresidual
+  c10::DeviceGuard guard(c.device);
+  if (!output(c, a[7], "out", 8, c.type, &dx, r, 0) ||
+      !vector_output(c, a[9], "dweight", c.cols, &dw, r, 1) ||
+      !vector_output(c, a[10], "dbias", c.cols, &db, r, 2) ||
+      (drops && !output(c, a[8], "dresidual", 8, c.type, &dr, r, 3)))
+    return nullptr;
+  Workspace ws;
+  if (!ws.take(c, a[11], armx_workspace_bytes(ARMX_OP_LAYER_NORM_BACKWARD, size_t(c.rows),
+                                              size_t(c.cols), nullptr)))
+    return ws.too_large ? PyLong_FromLong(ARMX_ERR_SHAPE) : nullptr;
+  const int st = layer_norm_rows_backward(
+      dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(mean), static_cast<const float*>(inv),
+      ds.p, ds.ld, type_code(c.type), size_t(c.rows), size_t(c.cols), drops ? &drop : nullptr,
+      dx.p, dx.ld, dr.p, dr.ld, static_cast<float*>(dw), static_cast<float*>(db), ws.p, ws.bytes,
+      c.has_cfg ? &c.cfg : nullptr, stream_of(c));
+  if (st == ARMX_OK && ws.bytes && a[11] != Py_None) written(a[11]);
+  return r.done(st, 4);
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, dropout, residual, out, start, stop)
+PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c{"dropout_rows"};
+  Rows x, res, out;
+  armx_dropout drop;
+  bool drops = false;
+  if (!arity(c.name, n, 6) || !first(c, a[0], "x", false) ||
+      !matrix(c, a[0], "x", c.rows, c.cols, c.type, &x) ||
+      !dropout(c, a[1], false, &drop, &drops) ||
+      (a[2] != Py_None && !matrix(c, a[2], "residual", c.rows, c.cols, c.type, &res)) ||
+      !events(c, a[4], a[5]))
+    return nullptr;
+  Owned r;
+  c10::DeviceGuard guard(c.device);
+  if (!output(c, a[3], "out", 8, c.type, &out, r, 0)) return nullptr;
+  const int st = dropout_rows(x.p, x.ld, res.p, res.ld, type_code(c.type), size_t(c.rows),
+                              size_t(c.cols), &drop, out.p, out.ld, c.has_cfg ? &c.cfg : nullptr,
+                              stream_of(c));
+  return r.done(st, 1);
   END_HANDLE_TH_ERRORS
 }
 
@@ -402,6 +563,9 @@ PyMethodDef methods[] = {
     method<py_norm_backward>("rms_norm_rows_backward"),
     method<py_quantize>("quantize_rows_int8"),
     method<py_matmul>("matmul_int8"),
+    method<py_layer_norm>("layer_norm_rows"),
+    method<py_layer_norm_backward>("layer_norm_rows_backward"),
+    method<py_dropout>("dropout_rows"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,4 +1,4 @@
-// Arguments and launch shapes of the layer entry points (row norms, 8-bit
+// Arguments and launch shapes of the layer entry points (row norms, dropout, 8-bit
 // codes, the product of codes), shared by their C entry points and launchers.
 #pragma once
 
@@ -82,6 +82,56 @@ struct NormBackwardPlan {
 constexpr uint64_t kMaxBackwardCols = uint64_t(1) << 26;
 NormBackwardPlan plan_norm_backward(uint64_t rows, uint64_t cols, int cu_count);
 
+// A dropout as the kernels take it (armx_dropout).
+struct DropoutArgs {
+  uint32_t key0 = 0, key1 = 0;
+  uint64_t offset = 0;
+  const uint64_t* step = nullptr;  // may be null
+  uint32_t first_row = 0;
+  uint32_t limit = 0;  // values whose 16 bits are below it are dropped
+  float scale = 1;
+};
+
+// One call of layer_norm_rows or, with `weight` null, of dropout_rows.
+struct LayerNormArgs {
+  const uint16_t* x = nullptr;
+  const uint16_t* residual = nullptr;  // may be null
+  const uint16_t* weight = nullptr;
+  const uint16_t* bias = nullptr;  // may be null
+  uint16_t* out = nullptr;
+  uint16_t* sum_out = nullptr;  // may be null
+  float* mean = nullptr;        // may be null, like
+  float* inv_std = nullptr;
+  uint64_t rows = 0, cols = 0;
+  uint64_t ldx = 0, ldr = 0, ldo = 0, lds = 0;
+  float eps = 0;
+  int type = ARMX_F16;
+  bool drop = false;
+  DropoutArgs dropout{};
+};
+
+struct LayerNormBackwardArgs {
+  const uint16_t* dy = nullptr;
+  const uint16_t* h = nullptr;
+  const uint16_t* weight = nullptr;
+  const float* mean = nullptr;
+  const float* inv_std = nullptr;
+  const uint16_t* dsum = nullptr;  // may be null
+  uint16_t* dx = nullptr;
+  uint16_t* dresidual = nullptr;  // with a dropout; may be null
+  float* dweight = nullptr;
+  float* dbias = nullptr;
+  float* partials = nullptr;  // blocks x 2 x pitch, when the plan has a workspace
+  uint64_t rows = 0, cols = 0;
+  uint64_t ldy = 0, ldh = 0, ldd = 0, ldx = 0, ldr = 0;
+  int type = ARMX_F16;
+  bool drop = false;
+  DropoutArgs dropout{};
+};
+
+// As plan_norm_backward, for the sums of two gradients.
+NormBackwardPlan plan_layer_norm_backward(uint64_t rows, uint64_t cols, int cu_count);
+
 struct MatmulArgs {
   const int8_t* a = nullptr;
   const int8_t* b = nullptr;
@@ -106,6 +156,11 @@ MatmulTile choose_matmul_tile(const MatmulArgs& args, int cu_count);
 hipError_t launch_norm(const NormArgs& args, const armx_config* cfg, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackwardArgs& args, const NormBackwardPlan& plan,
                                 const armx_config* cfg, hipStream_t stream);
+hipError_t launch_layer_norm(const LayerNormArgs& args, const armx_config* cfg,
+                             hipStream_t stream);
+hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& args,
+                                      const NormBackwardPlan& plan, const armx_config* cfg,
+                                      hipStream_t stream);
 hipError_t launch_matmul_int8(const MatmulArgs& args, int cu_count, const armx_config* cfg,
                               hipStream_t stream);
 

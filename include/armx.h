@@ -525,6 +525,119 @@ int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t
                 const float* b_scales, const void* bias, size_t m, size_t n, size_t k,
                 void* out, size_t ldo, int out_type, const armx_config* cfg, void* stream);
 
+/*
+ * armx_dropout -- a dropout whose mask is never stored: the bits that decide about a
+ * value are a function of the seed, of offset + *step and of the value's row and
+ * column, so the same armx_dropout in a backward pass means the same mask.
+ *
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as
+ * 1, 2, 3", 2011) with the seed's low and high word as key and the counter
+ *   (c, first_row + r, low word of offset + *step, high word of it)
+ * gives 16 bits for each value of columns 8 c .. 8 c + 7 of row r, the low half of each
+ * of its four words first.  With t = 65536 p rounded to a whole number (halves up), a
+ * value is kept where its bits are at least t, and then multiplied by the binary32
+ * 65536 / (65536 - t), so that p counts in steps of 2^-16 and means stay as they were.
+ * A dropped value gives 0 whatever stood there, and p = 1 (t = 65536) drops all.
+ *
+ * p          0 .. 1.
+ * seed, offset  any.  Dropouts that shall be unlike need different ones: an offset
+ *            for each place in a model, say, and a step for each training step.
+ * step       device, 8-byte aligned, added to offset as the kernel runs (a captured
+ *            step's count, which other work of the graph advances), or NULL.
+ * first_row  the place of row 0 in a matrix that is taken in parts; first_row + rows
+ *            is at most 2^32 (ARMX_ERR_SHAPE).
+ */
+typedef struct armx_dropout {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* step;
+  uint64_t first_row;
+} armx_dropout;
+
+/*
+ * dropout_rows -- out[r][c] = x[r][c] kept ? x[r][c] * scale : 0, plus residual[r][c]
+ * if there is one, in binary32 and rounded once to `type`.  The gradient is the same
+ * call on the result's gradient (without a residual, to whom that goes as it is).
+ *
+ * x, residual  device, rows x cols, ARMX_F16 or ARMX_BF16; residual may be NULL.
+ * dropout      host; required.
+ * out          device, rows x cols; may be x or residual themselves.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a p outside 0 .. 1 is
+ * ARMX_ERR_CONFIG.
+ */
+int dropout_rows(const void* x, size_t ldx, const void* residual, size_t ldr, int type,
+                 size_t rows, size_t cols, const armx_dropout* dropout, void* out, size_t ldo,
+                 const armx_config* cfg, void* stream);
+
+/*
+ * layer_norm_rows -- mean and variance norm of every row, after a dropout and the
+ * residual's addition:
+ *   h[r][c]   = x[r][c], or as dropout_rows gives it of x and residual, rounded once
+ *               to `type`
+ *   mean[r]   = sum over c of h[r][c] / cols
+ *   inv[r]    = 1 / sqrt(sum over c of (h[r][c] - mean[r])^2 / cols + eps)
+ *   out[r][c] = ((h[r][c] - mean[r]) * inv[r]) * weight[c] + bias[c], rounded once
+ * with sums, statistics and products in binary32.  The deviations are summed, not the
+ * squares, so that an offset of the row costs no bits of its variance.
+ *
+ * x, residual  device, rows x cols, ARMX_F16 or ARMX_BF16; residual may be NULL.
+ * weight, bias device, cols values of `type`, 16-byte aligned; bias may be NULL (zeros).
+ * eps          at least 0.
+ * dropout      host, of x, or NULL.
+ * out          device, rows x cols.
+ * sum_out      device, receives h; may be NULL (h is not written) and must be where
+ *              neither a residual nor a dropout is given.
+ * mean, inv_std  device, rows binary32 each (for the backward pass; 0 when cols is 0),
+ *              or NULL.
+ * out and sum_out may each be x or residual themselves (same pointer and pitch), not
+ * both the same one; nothing else may overlap.  A NaN or an infinity in a row's h makes
+ * NaNs in that row, and so does a sum of squared deviations past binary32's range
+ * where it is infinite less infinite (otherwise inv is 0).
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other than the
+ * two, an eps that is negative or NaN, a p outside 0 .. 1, or an out that starts where
+ * sum_out does is ARMX_ERR_CONFIG.
+ */
+int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
+                    const void* weight, const void* bias, int type, size_t rows, size_t cols,
+                    float eps, const armx_dropout* dropout, void* out, size_t ldo, void* sum_out,
+                    size_t lds, float* mean, float* inv_std, const armx_config* cfg,
+                    void* stream);
+
+/*
+ * layer_norm_rows_backward -- gradients of layer_norm_rows: with g = dy * weight and
+ * n = (h - mean[r]) * inv[r],
+ *   dh[r][c]   = inv[r] * (g[r][c] - mean over c of g - n[r][c] * mean over c of (g n))
+ *                + dsum[r][c]
+ *   dweight[c] = sum over r of dy[r][c] * n[r][c],  dbias[c] = sum over r of dy[r][c]
+ * in binary32.  Without a dropout dx = dh is the gradient of x and of residual alike;
+ * with one, dresidual = dh is that of residual and dx = dh kept ? dh * scale : 0 that
+ * of x, each rounded once to `type`.
+ *
+ * dy       device, rows x cols, the gradient of out.
+ * h        device, rows x cols, what was normalised (sum_out, or x).
+ * mean, inv_std  device, rows binary32, as layer_norm_rows wrote them.
+ * dsum     device, rows x cols, the gradient that flows into sum_out from
+ *          elsewhere, or NULL.
+ * dropout  host, as it was given to layer_norm_rows, or NULL.
+ * dx       device, rows x cols.
+ * dresidual  device, rows x cols, or NULL; only with a dropout.
+ *          dx and dresidual may each be dy or dsum themselves (and those h, or one
+ *          another), not both the same one.
+ * dweight, dbias  device, cols binary32 each; zeros when rows == 0.
+ * cols     at most 2^26.
+ * ws       device workspace of armx_workspace_bytes(ARMX_OP_LAYER_NORM_BACKWARD, rows,
+ *          cols, NULL) bytes; it needs no zeros and none are left (it has no
+ *          counter region).  NULL when that is 0.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
+ */
+int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh,
+                             const void* weight, const float* mean, const float* inv_std,
+                             const void* dsum, size_t ldd, int type, size_t rows, size_t cols,
+                             const armx_dropout* dropout, void* dx, size_t ldx, void* dresidual,
+                             size_t ldr, float* dweight, float* dbias, void* ws,
+                             size_t ws_bytes, const armx_config* cfg, void* stream);
+
 /* Operation codes for armx_workspace_bytes. */
 #define ARMX_OP_SUM 0
 #define ARMX_OP_ROWS 1
@@ -532,13 +645,14 @@ int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t
 #define ARMX_OP_ROWS_FIXED 3
 #define ARMX_OP_EXACT 4
 #define ARMX_OP_RMS_BACKWARD 5
+#define ARMX_OP_LAYER_NORM_BACKWARD 6
 
 /*
  * armx_workspace_bytes -- bytes of workspace the matching call needs on the
  * current device with this configuration (0 if none).  `n_or_rows` is n for
  * ARMX_OP_SUM / ARMX_OP_FIXED / ARMX_OP_EXACT and rows for ARMX_OP_ROWS,
- * ARMX_OP_ROWS_FIXED and ARMX_OP_RMS_BACKWARD; `cols` is used by those three
- * only (the last op's workspace has no counter region).  Returns (size_t)-1
+ * ARMX_OP_ROWS_FIXED, ARMX_OP_RMS_BACKWARD and ARMX_OP_LAYER_NORM_BACKWARD; `cols`
+ * is used by those four only (the last two's workspace has no counter region).  Returns (size_t)-1
  * for an invalid op or configuration.  Needs no GPU: without a device it
  * assumes 256 compute units.
  */
@@ -558,10 +672,11 @@ size_t armx_workspace_bytes(int op, size_t n_or_rows, size_t cols,
  *                    compute-unit count (0 when nothing is launched)
  *   workspace_bytes  as armx_workspace_bytes
  *   lds_bytes        dynamic LDS per block of that launch
- *   launches         kernel launches the call enqueues (ARMX_OP_RMS_BACKWARD
- *                    of some rows without a workspace: one more, grid_blocks in
- *                    the two together, where dx's memory from its first value
- *                    to its last meets that of dy or h)
+ *   launches         kernel launches the call enqueues (ARMX_OP_RMS_BACKWARD and
+ *                    ARMX_OP_LAYER_NORM_BACKWARD of some rows without a
+ *                    workspace: one more, grid_blocks in the two together, where
+ *                    dx's or dresidual's memory from its first value to its last
+ *                    meets that of dy or h)
  * Without a device it assumes 256 compute units.  For the row operations
  * the plan is the one made with a workspace.  Returns ARMX_OK, or
  * ARMX_ERR_NULL (info NULL), ARMX_ERR_CONFIG or ARMX_ERR_SHAPE as the call
