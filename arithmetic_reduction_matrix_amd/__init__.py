@@ -39,8 +39,9 @@ __all__ = [
     "PlanInfo", "LIB_PATH",
     "rms_norm_rows", "rms_norm_rows_int8", "rms_norm_rows_backward", "quantize_rows_int8",
     "matmul_int8", "RmsNorm", "RmsNormInt8", "RmsNormGrads", "RowCodes",
-    "dropout_rows", "layer_norm_rows", "layer_norm_rows_backward", "Dropout", "LayerNorm",
-    "LayerNormGrads",
+    "dropout_rows", "layer_norm_rows", "layer_norm_rows_backward", "cross_entropy_rows",
+    "cross_entropy_rows_backward", "Dropout", "LayerNorm", "LayerNormGrads", "CrossEntropy",
+    "CrossEntropyGrads",
     "OP_SUM", "OP_ROWS", "OP_FIXED", "OP_ROWS_FIXED", "OP_EXACT", "OP_RMS_BACKWARD",
     "OP_LAYER_NORM_BACKWARD",
     "FLAG_PLAIN", "FLAG_CACHED_LOADS", "FLAG_ONE_CHAIN", "FLAG_TWO_PASS", "FLAG_MMA_LEVELS",
@@ -371,4 +372,5 @@ from .layer import (  # noqa: E402  (needs the names above)
     RmsNorm, RmsNormGrads, RmsNormInt8, RowCodes, matmul_int8, quantize_rows_int8,
     rms_norm_rows, rms_norm_rows_backward, rms_norm_rows_int8)
 from .training import (  # noqa: E402
-    Dropout, LayerNorm, LayerNormGrads, dropout_rows, layer_norm_rows, layer_norm_rows_backward)
+    CrossEntropy, CrossEntropyGrads, Dropout, LayerNorm, LayerNormGrads, cross_entropy_rows,
+    cross_entropy_rows_backward, dropout_rows, layer_norm_rows, layer_norm_rows_backward)

@@ -35,7 +35,8 @@ BINDING_SOURCES = ["binding.cpp"]
 ARCH = "gfx950"
 HIP_SOURCES = ["sum_kernels.hip", "fixed_kernels.hip", "rows_kernels.hip", "exact_kernels.hip",
                "rows_fixed_kernels.hip", "levels_kernels.hip", "short_rows_kernels.hip",
-               "norm_kernels.hip", "matmul_int8_kernels.hip", "layer_norm_kernels.hip"]
+               "norm_kernels.hip", "matmul_int8_kernels.hip", "layer_norm_kernels.hip",
+               "cross_entropy_kernels.hip", "cross_entropy_backward_kernels.hip"]
 HOST_SOURCES = ["api.cpp", "api_layer.cpp", "plan.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

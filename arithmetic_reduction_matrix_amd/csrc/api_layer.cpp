@@ -9,6 +9,7 @@
 #include <initializer_list>
 
 #include "armx.h"
+#include "cross_entropy.h"
 #include "launch.h"
 #include "layer.h"
 
@@ -118,6 +119,58 @@ int check_dropout(const armx_dropout* d, uint64_t rows, armx::DropoutArgs* out) 
   // all dropped: nothing is ever multiplied by it
   out->scale = out->limit < 65536 ? float(65536.0 / (65536.0 - double(out->limit))) : 0.0f;
   return ARMX_OK;
+}
+
+// Sizes of the cross entropy: 32-bit offsets in a tile's rows, and grids.
+constexpr uint64_t kMaxLossRows = uint64_t(1) << 21, kMaxLossCols = uint64_t(1) << 21;
+constexpr uint64_t kMaxLossVocab = uint64_t(1) << 30, kMaxLossLd = uint64_t(1) << 22;
+
+int check_loss_sizes(uint64_t rows, uint64_t vocab, uint64_t cols, bool backward) {
+  if (rows > kMaxLossRows || vocab > kMaxLossVocab || cols > kMaxLossCols) return ARMX_ERR_SHAPE;
+  if (rows == 0) return ARMX_OK;
+  if (vocab == 0 || cols == 0) return ARMX_ERR_SHAPE;
+  const uint64_t tiles = (rows + 255) / 256;
+  if (tiles * ((vocab + 255) / 256) > kMaxProductTiles) return ARMX_ERR_SHAPE;
+  if (backward && tiles * ((cols + 255) / 256) > kMaxProductTiles) return ARMX_ERR_SHAPE;
+  return ARMX_OK;
+}
+
+// What both passes check of their inputs; `a` receives them.
+int check_loss(const void* x, size_t ldx, const void* weight, size_t ldw, const int64_t* targets,
+               int type, size_t rows, size_t vocab, size_t cols, const armx_config* cfg,
+               bool backward, armx::CrossEntropyArgs* a) {
+  const int st = first_error(
+      {check_type(type), check_cfg(cfg), check_loss_sizes(rows, vocab, cols, backward),
+       check_matrix(x, rows, cols, ldx, 16, 8),
+       rows ? check_matrix(weight, vocab, cols, ldw, 16, 8) : ARMX_OK});
+  if (st != ARMX_OK || rows == 0) return st;
+  if ((rows > 1 && ldx > kMaxLossLd) || (vocab > 1 && ldw > kMaxLossLd)) return ARMX_ERR_SHAPE;
+  if (!targets) return ARMX_ERR_NULL;
+  if (!aligned(targets, 8)) return ARMX_ERR_ALIGN;
+  a->x = static_cast<const uint16_t*>(x);
+  a->weight = static_cast<const uint16_t*>(weight);
+  a->targets = targets;
+  a->rows = rows, a->vocab = vocab, a->cols = cols;
+  // a single row's pitch is never used as one
+  a->ldx = rows > 1 ? ldx : 0, a->ldw = vocab > 1 ? ldw : 0;
+  a->type = type;
+  return ARMX_OK;
+}
+
+int check_space(const void* ws, size_t got, size_t need) {
+  if (need == 0) return ARMX_OK;
+  if (!ws) return ARMX_ERR_NULL;
+  if (!aligned(ws, 256)) return ARMX_ERR_ALIGN;
+  return got < need ? ARMX_ERR_WORKSPACE : ARMX_OK;
+}
+
+void log_loss(const char* entry, const armx::CrossEntropyArgs& a, size_t ws, int cu_count) {
+  if (!log_enabled()) return;
+  const armx::Tile16Size t = armx::tile16_size(
+      armx::choose_tile16(a.rows, a.vocab, a.cols, cu_count));
+  std::fprintf(stderr, "armx: %s rows=%llu vocab=%llu cols=%llu type=%d tile=%dx%d ws=%zu\n", entry,
+               (unsigned long long)a.rows, (unsigned long long)a.vocab,
+               (unsigned long long)a.cols, a.type, t.bm, t.bn, ws);
 }
 
 }  // namespace
@@ -348,6 +401,77 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
   a.drop = dropout != nullptr;
   log_rows("layer_norm_rows_backward", rows, cols, type);
   return hip_status(armx::launch_layer_norm_backward(a, plan, cfg, s));
+}
+
+size_t armx_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols) {
+  if (check_loss_sizes(rows, vocab, cols, false) != ARMX_OK) return size_t(-1);
+  return rows ? armx::plan_cross_entropy(rows, vocab).ws_bytes : 0;
+}
+
+size_t armx_cross_entropy_backward_workspace_bytes(size_t rows, size_t vocab, size_t cols, int dx,
+                                                   int dweight) {
+  if (check_loss_sizes(rows, vocab, cols, true) != ARMX_OK) return size_t(-1);
+  if (rows == 0) return 0;
+  return armx::plan_cross_entropy_backward(rows, vocab, cols, dx != 0, dweight != 0,
+                                           armx::current_cu_count())
+      .ws_bytes;
+}
+
+int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw,
+                       const int64_t* targets, int type, size_t rows, size_t vocab, size_t cols,
+                       int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                       const armx_config* cfg, void* stream) {
+  armx::CrossEntropyArgs a;
+  int st = check_loss(x, ldx, weight, ldw, targets, type, rows, vocab, cols, cfg, false, &a);
+  if (st != ARMX_OK || rows == 0) return st;
+  if (!loss || !lse) return ARMX_ERR_NULL;
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return ARMX_ERR_ALIGN;
+  a.ignore = ignore_index;
+  const armx::CrossEntropyPlan plan = armx::plan_cross_entropy(rows, vocab);
+  st = check_space(ws, ws_bytes, plan.ws_bytes);
+  if (st != ARMX_OK) return st;
+  const int cus = armx::current_cu_count();
+  log_loss("cross_entropy_rows", a, plan.ws_bytes, cus);
+  return hip_status(armx::launch_cross_entropy(a, plan, loss, lse, ws, cus, cfg,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
+                                const void* weight, size_t ldw, const int64_t* targets,
+                                const float* lse, int type, size_t rows, size_t vocab,
+                                size_t cols, int64_t ignore_index, void* dx, size_t lddx,
+                                void* dweight, size_t lddw, int dweight_type, void* ws,
+                                size_t ws_bytes, const armx_config* cfg, void* stream) {
+  armx::CrossEntropyArgs a;
+  int st = check_loss(x, ldx, weight, ldw, targets, type, rows, vocab, cols, cfg, true, &a);
+  if (st != ARMX_OK) return st;
+  if (dweight_type != type && dweight_type != ARMX_F32) return ARMX_ERR_CONFIG;
+  st = first_error({check_matrix(dx, rows, cols, lddx, 16, 8, true),
+                    check_matrix(dweight, vocab, cols, lddw, 16, 8, true)});
+  if (st != ARMX_OK) return st;
+  armx::CrossEntropyGrads g;
+  g.dloss = dloss, g.lse = lse;
+  g.dx = static_cast<uint16_t*>(dx);
+  g.dweight = dweight;
+  g.lddx = lddx, g.lddw = vocab > 1 ? lddw : cols;
+  g.dweight_type = dweight_type;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows == 0) {
+    if (!dweight || vocab == 0 || cols == 0) return ARMX_OK;
+    a.vocab = vocab, a.cols = cols, a.type = type;
+    return hip_status(armx::launch_cross_entropy_backward(a, {}, g, nullptr, 0, cfg, s));
+  }
+  if (!dx && !dweight) return ARMX_ERR_NULL;
+  if (!dloss || !lse) return ARMX_ERR_NULL;
+  if (!aligned(dloss, 4) || !aligned(lse, 4)) return ARMX_ERR_ALIGN;
+  a.ignore = ignore_index;
+  const int cus = armx::current_cu_count();
+  const armx::CrossEntropyGradPlan plan =
+      armx::plan_cross_entropy_backward(rows, vocab, cols, dx != nullptr, dweight != nullptr, cus);
+  st = check_space(ws, ws_bytes, plan.ws_bytes);
+  if (st != ARMX_OK) return st;
+  log_loss("cross_entropy_rows_backward", a, plan.ws_bytes, cus);
+  return hip_status(armx::launch_cross_entropy_backward(a, plan, g, ws, cus, cfg, s));
 }
 
 int matmul_int8(const int8_t* a, size_t lda, const float* a_scales, const int8_t* b, size_t ldb,

@@ -494,6 +494,104 @@ PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+bool int64_arg(const Call& c, PyObject* o, const char* what, int64_t* v) {
+  *v = PyLong_AsLongLong(o);
+  if (*v != -1 || !PyErr_Occurred()) return true;
+  PyErr_Clear();
+  PyErr_Format(PyExc_TypeError, "%s: %s must be an int of 64 bits", c.name, what);
+  return false;
+}
+
+// (x, weight, targets, ignore_index, loss, lse, workspace, start, stop)
+PyObject* py_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c{"cross_entropy_rows"}, other{"cross_entropy_rows"};
+  Rows x, w;
+  void *targets = nullptr, *loss = nullptr, *lse = nullptr;
+  int64_t ignore = 0;
+  if (!arity(c.name, n, 9) || !first(c, a[0], "x", false) || !first(other, a[1], "weight", false) ||
+      !matrix(c, a[0], "x", c.rows, c.cols, c.type, &x) ||
+      !matrix(c, a[1], "weight", other.rows, c.cols, c.type, &w) ||
+      !vector(c, a[2], "targets", c.rows, at::kLong, &targets) ||
+      !int64_arg(c, a[3], "ignore_index", &ignore) || !events(c, a[7], a[8]))
+    return nullptr;
+  const int64_t vocab = other.rows;
+  Owned r;   // loss, lse
+  c10::DeviceGuard guard(c.device);
+  if (!vector_output(c, a[4], "loss", c.rows, &loss, r, 0) ||
+      !vector_output(c, a[5], "lse", c.rows, &lse, r, 1))
+    return nullptr;
+  Workspace ws;
+  if (!ws.take(c, a[6], armx_cross_entropy_workspace_bytes(size_t(c.rows), size_t(vocab),
+                                                           size_t(c.cols))))
+    return ws.too_large ? PyLong_FromLong(ARMX_ERR_SHAPE) : nullptr;
+  const int st = cross_entropy_rows(
+      x.p, x.ld, w.p, w.ld, static_cast<const int64_t*>(targets), type_code(c.type),
+      size_t(c.rows), size_t(vocab), size_t(c.cols), ignore, static_cast<float*>(loss),
+      static_cast<float*>(lse), ws.p, ws.bytes, c.has_cfg ? &c.cfg : nullptr, stream_of(c));
+  if (st == ARMX_OK && ws.bytes && a[6] != Py_None) written(a[6]);
+  return r.done(st, 2);
+  END_HANDLE_TH_ERRORS
+}
+
+// (dloss, x, weight, targets, lse, ignore_index, need_dx, need_dweight, out, dweight,
+// dweight's type code, workspace, start, stop)
+PyObject* py_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c{"cross_entropy_rows_backward"}, other{"cross_entropy_rows_backward"};
+  Rows x, w, dx, dw;
+  void *dloss = nullptr, *targets = nullptr, *lse = nullptr;
+  int64_t ignore = 0;
+  if (!arity(c.name, n, 14) || !first(c, a[1], "x", false) ||
+      !first(other, a[2], "weight", false) ||
+      !matrix(c, a[1], "x", c.rows, c.cols, c.type, &x) ||
+      !matrix(c, a[2], "weight", other.rows, c.cols, c.type, &w) ||
+      !vector(c, a[0], "dloss", c.rows, at::kFloat, &dloss) ||
+      !vector(c, a[3], "targets", c.rows, at::kLong, &targets) ||
+      !vector(c, a[4], "lse", c.rows, at::kFloat, &lse) ||
+      !int64_arg(c, a[5], "ignore_index", &ignore) || !events(c, a[12], a[13]))
+    return nullptr;
+  const int need_dx = PyObject_IsTrue(a[6]), need_dw = PyObject_IsTrue(a[7]);
+  if (need_dx < 0 || need_dw < 0) return nullptr;
+  if ((!need_dx && a[8] != Py_None) || (!need_dw && a[9] != Py_None) || (!need_dx && !need_dw)) {
+    PyErr_Format(PyExc_ValueError, "%s: a gradient that is not wanted takes no tensor, and one "
+                 "is wanted", c.name);
+    return nullptr;
+  }
+  ScalarType type = c.type;   // dweight's
+  if (a[9] != Py_None) {
+    if (const Tensor* given = tensor(a[9])) type = given->scalar_type();
+  } else if (a[10] != Py_None) {
+    const long code = PyLong_AsLong(a[10]);
+    if (code == -1 && PyErr_Occurred()) return nullptr;
+    type = code == ARMX_F16 ? at::kHalf : code == ARMX_BF16 ? at::kBFloat16
+           : code == ARMX_F32 ? at::kFloat : at::kByte;
+  }
+  if (type != c.type && type != at::kFloat) {
+    PyErr_Format(PyExc_TypeError, "%s: dweight is %s or float32", c.name, c10::toString(c.type));
+    return nullptr;
+  }
+  other.type = type, other.device = c.device;
+  other.cols = c.cols;
+  Owned r;   // dx, dweight
+  c10::DeviceGuard guard(c.device);
+  if ((need_dx && !output(c, a[8], "out", 8, c.type, &dx, r, 0)) ||
+      (need_dw && !output(other, a[9], "dweight", 8, type, &dw, r, 1)))
+    return nullptr;
+  Workspace ws;
+  if (!ws.take(c, a[11], armx_cross_entropy_backward_workspace_bytes(
+                             size_t(c.rows), size_t(other.rows), size_t(c.cols), need_dx, need_dw)))
+    return ws.too_large ? PyLong_FromLong(ARMX_ERR_SHAPE) : nullptr;
+  const int st = cross_entropy_rows_backward(
+      static_cast<const float*>(dloss), x.p, x.ld, w.p, w.ld,
+      static_cast<const int64_t*>(targets), static_cast<const float*>(lse), type_code(c.type),
+      size_t(c.rows), size_t(other.rows), size_t(c.cols), ignore, dx.p, dx.ld, dw.p, dw.ld,
+      type_code(type), ws.p, ws.bytes, c.has_cfg ? &c.cfg : nullptr, stream_of(c));
+  if (st == ARMX_OK && ws.bytes && a[11] != Py_None) written(a[11]);
+  return r.done(st, 2);
+  END_HANDLE_TH_ERRORS
+}
+
 // A matrix of codes whose rows can be read in pieces of 16 to their end.
 bool code_rows(const Call& c, PyObject* o, const char* what, int64_t rows, int64_t k, Rows* out) {
   if (!matrix(c, o, what, rows, k, at::kChar, out)) return false;
@@ -566,6 +664,8 @@ PyMethodDef methods[] = {
     method<py_layer_norm>("layer_norm_rows"),
     method<py_layer_norm_backward>("layer_norm_rows_backward"),
     method<py_dropout>("dropout_rows"),
+    method<py_cross_entropy>("cross_entropy_rows"),
+    method<py_cross_entropy_backward>("cross_entropy_rows_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,0 +1,517 @@
+// The gradients of the cross entropy of rows against a vocabulary:
+//   dz = dloss (exp(z - lse) - onehot(target)),  dx = dz w,  dweight = dz^T x,
+// for a piece of the vocabulary at a time: its logits z are made again, turned into dz
+// in the product's registers and stored in 16 bits, once by rows and once by columns;
+// the piece's part of dx and its rows of dweight are products of those with the
+// transposes of w's piece and of x, which like all products here run along both
+// operands' rows.
+//
+// dz is rounded to 16 bits twice, with a scale of its own each time:
+// - for dx, a row is divided by 1 - exp(z[target] - lse), its target's magnitude, which
+//   then is a whole power of two and is not rounded at all (it outweighs the others of
+//   its row together), and the row of dx is multiplied by it and by dloss in 32 bits;
+// - for dweight, by dloss over the largest |dloss|; of a few rows, whose roundings do
+//   not average out, the rest that the rounding leaves is a second 16-bit term
+//   (kTwoTerms), multiplied by the same row of x.
+// Powers of two keep both in binary16's range: 2^14 for dx, 2^15 for dweight.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "cross_entropy.h"
+#include "device_common.hpp"
+#include "launch.h"
+#include "layer.h"
+#include "row_pieces.hpp"
+#include "tile16.hpp"
+#include "tile16_choice.hpp"
+
+namespace armx {
+namespace {
+
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kRowScale = 0x1p14f, kTopScale = 0x1p15f;
+
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2E); }
+
+// What a row of dz is made with: by rows (exp(z - lse) - onehot) * scale, by columns
+// (exp(z - lse) - onehot) * dloss * that of the largest |dloss|; the row of dx is what
+// comes out times `back`.  A row that is ignored has zeros, and one whose target is not
+// in the vocabulary NaNs.
+struct RowScale {
+  float scale, dloss, back;
+  uint32_t skip;
+};
+
+// The scale of the largest |dloss| and what undoes it.  (Below 2^-105, whose scale
+// would not be finite, a fixed one.)
+__device__ __forceinline__ float top_scale(uint32_t top_bits) {
+  const float top = __builtin_bit_cast(float, top_bits);
+  return top < 0x1p-105f ? 0x1p120f : kTopScale / top;
+}
+
+// A row's scales, a wavefront each; the largest |dloss| (bits, NaNs largest) in *top,
+// which is 0 before.
+template <int TYPE>
+__global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, const float* dloss,
+                                                        const float* lse, RowScale* rows,
+                                                        uint32_t* top) {
+  const uint64_t row = uint64_t(blockIdx.x) * 4 + wave_id();
+  if (row >= k.rows) return;
+  const uint64_t bits = uint64_t(k.targets[row]);   // the same in all lanes
+  const int64_t t = int64_t(
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(bits >> 32)))) << 32 |
+      uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(bits)))));
+  RowScale s = {0.0f, 0.0f, 0.0f, 1u};
+  if (t != k.ignore) {
+    s.skip = 0;
+    s.dloss = dloss[row];
+    if (t >= 0 && t < int64_t(k.vocab)) {
+      const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+      const RowWords xr(k.x + row * k.ldx, cols), wr(k.weight + uint64_t(t) * k.ldw, cols);
+      float z = 0.0f;
+      for (uint32_t c = lane_id(); c < chunks; c += 64) {
+        float f[8], g[8];
+        widen8<TYPE>(xr.load(c), f);
+        widen8<TYPE>(wr.load(c), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          z = c * 8 + i < cols ? __builtin_fmaf(f[i], g[i], z) : z;
+      }
+      z = lane_tree_full(z);
+      // (one that is nearly sure of its target keeps a scale that the logit's own
+      // rounding does not turn over)
+      const float rest = __builtin_fmaxf(1.0f - exp_of(z - lse[row]), 0x1p-14f);
+      s.scale = kRowScale / rest;
+      s.back = s.dloss * (rest / kRowScale);
+    } else {
+      s.scale = s.dloss = s.back = __builtin_nanf("");
+    }
+  }
+  if (lane_id() == 0) {
+    rows[row] = s;
+    atomicMax(top, __builtin_bit_cast(uint32_t, s.dloss) & 0x7FFFFFFFu);
+  }
+}
+
+// to[c][r] = from[r][c], r < rows, c < cols, in 64 x 64 tiles; `copies` of them side by
+// side, and zeros for rows that are ignored (targets may be null).
+__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* from, uint64_t ld,
+                                                        uint64_t rows, uint64_t cols,
+                                                        uint16_t* to, uint64_t ldt,
+                                                        const int64_t* targets, int64_t ignore,
+                                                        uint64_t copies) {
+  __shared__ uint16_t tile[64][66];
+  const uint64_t r0 = uint64_t(blockIdx.x) * 64, c0 = uint64_t(blockIdx.y) * 64;
+  const uint32_t j = threadIdx.x % 64, i0 = threadIdx.x / 64;
+#pragma unroll 4
+  for (uint32_t i = i0; i < 64; i += 4) {
+    const uint64_t r = r0 + i, c = c0 + j;
+    const bool in = r < rows && c < cols && !(targets && targets[r] == ignore);
+    tile[i][j] = in ? from[r * ld + c] : uint16_t(0);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (uint32_t i = i0; i < 64; i += 4) {
+    const uint64_t c = c0 + i, r = r0 + j;
+    if (r >= rows || c >= cols) continue;
+    for (uint64_t q = 0; q < copies; ++q) to[c * ldt + q * rows + r] = tile[j][i];
+  }
+}
+
+// dz of a piece of the vocabulary (w: its rows, the first of them number `first`), by
+// rows in dz and by columns in dzt (either may be null).  Both have whole tiles of room
+// for columns, and dzt with one term for rows too; what is past the piece is never used.
+template <class T, int TYPE>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
+    Matrix16 x, Matrix16 w, uint32_t cols, const int64_t* targets, int64_t first,
+    const float* lse, const RowScale* rows, const uint32_t* top, uint16_t* dz, uint64_t ldz,
+    uint16_t* dzt, uint64_t ldt, uint64_t terms, unsigned tiles_m, unsigned tiles_n) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
+  unsigned ti, tj;
+  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  floatx4 z[T::kMT][T::kNT];
+  multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
+  const uint64_t row0 = i0 + lane_row<T>(), col = j0 + lane_col<T>();
+  const float all = top_scale(*top);
+  float each[T::kMT];
+#pragma unroll
+  for (int i = 0; i < T::kMT; ++i) {
+    const uint64_t row = row0 + i < x.rows ? row0 + i : x.rows - 1;
+    const RowScale s = rows[row];
+    const float l = lse[row];
+    const int64_t at = targets[row] - first - int64_t(col);
+    each[i] = s.dloss * all;
+#pragma unroll
+    for (int c = 0; c < T::kCols; ++c) {
+      const float v = exp_of(z[i][c / 4][c % 4] - l) - (at == c ? 1.0f : 0.0f);
+      z[i][c / 4][c % 4] = s.skip ? 0.0f : v;
+    }
+    if (dz && row0 + i < x.rows) {
+#pragma unroll
+      for (int c = 0; c < T::kCols; c += 8) {
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = narrow2<TYPE>(z[i][c / 4 + e / 2][2 * (e % 2)] * s.scale,
+                               z[i][c / 4 + e / 2][2 * (e % 2) + 1] * s.scale);
+        *reinterpret_cast<u32x4*>(dz + row * ldz + col + c) = v;
+      }
+    }
+  }
+  if (!dzt) return;
+  if (terms == 1) {
+#pragma unroll
+    for (int c = 0; c < T::kCols; ++c) {
+      uint16_t* to = dzt + (col + c) * ldt + row0;
+      if constexpr (T::kMT == 1) {
+        *to = uint16_t(narrow2<TYPE>(z[0][c / 4][c % 4] * each[0], 0.0f));
+      } else {
+        uint32_t v[T::kMT / 2];
+#pragma unroll
+        for (int i = 0; i < T::kMT; i += 2)
+          v[i / 2] = narrow2<TYPE>(z[i][c / 4][c % 4] * each[i],
+                                   z[i + 1][c / 4][c % 4] * each[i + 1]);
+        if constexpr (T::kMT == 2) *reinterpret_cast<uint32_t*>(to) = v[0];
+        if constexpr (T::kMT == 4) *reinterpret_cast<u32x2*>(to) = u32x2{v[0], v[1]};
+        if constexpr (T::kMT == 8)
+          *reinterpret_cast<u32x4*>(to) = u32x4{v[0], v[1], v[2], v[3]};
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < T::kMT; ++i) {
+      if (row0 + i >= x.rows) continue;
+#pragma unroll
+      for (int c = 0; c < T::kCols; ++c) {
+        const float v = z[i][c / 4][c % 4] * each[i];
+        const uint32_t high = narrow2<TYPE>(v, 0.0f);
+        float f[8];
+        widen8<TYPE>(u32x4{high, 0, 0, 0}, f);
+        uint16_t* to = dzt + (col + c) * ldt + row0 + i;
+        to[0] = uint16_t(high);
+        to[x.rows] = uint16_t(narrow2<TYPE>(v - f[0], 0.0f));
+      }
+    }
+  }
+}
+
+// The part of dx that a piece of the vocabulary makes: dz (rows x k) times wt (cols x k),
+// k in `splits` parts of `per` whose products stand apart; added to what is there after
+// the first piece.  `to` has whole tiles of room for columns.
+template <class T, int TYPE>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
+    Matrix16 dz, Matrix16 wt, uint32_t k, uint32_t per, float* to, uint64_t ldd, bool more,
+    unsigned tiles_m, unsigned tiles_n) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
+  const unsigned id = unsigned(xcd_block_id()), split = id / (tiles_m * tiles_n);
+  unsigned ti, tj;
+  tile_of(id % (tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
+  const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  const uint32_t k0 = split * per;
+  const uint32_t part = k0 >= k ? 0 : k - k0 < per ? k - k0 : per;
+  dz.p += k0;
+  wt.p += k0;
+  floatx4 acc[T::kMT][T::kNT];
+  multiply_tile<T, TYPE>(dz, wt, part, i0, j0, lds, acc);
+#pragma unroll
+  for (int i = 0; i < T::kMT; ++i) {
+    const uint64_t row = i0 + lane_row<T>() + i;
+    if (row >= dz.rows) continue;
+    floatx4* o =
+        reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + lane_col<T>());
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y) o[y] = more ? o[y] + acc[i][y] : acc[i][y];
+  }
+}
+
+// dx = the splits' products added in order, times the rows' factors.
+template <int TYPE>
+__global__ __launch_bounds__(256) void loss_dx_join_kernel(const float* from, uint64_t ldd,
+                                                           uint64_t splits, const RowScale* rows,
+                                                           uint64_t count, uint64_t cols,
+                                                           uint16_t* dx, uint64_t lddx) {
+  const uint32_t chunks = uint32_t((cols + 7) / 8);
+  for (uint64_t row = blockIdx.x; row < count; row += gridDim.x) {
+    const float back = rows[row].back;
+    const bool skip = rows[row].skip;
+    for (uint32_t c = threadIdx.x; c < chunks; c += 256) {
+      floatx4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      for (uint64_t s = 0; s < splits; ++s) {
+        const floatx4* v = reinterpret_cast<const floatx4*>(from + (s * count + row) * ldd) + 2 * c;
+        a += v[0];
+        b += v[1];
+      }
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = skip ? 0.0f : (i < 4 ? a[i] : b[i - 4]) * back;
+      store_chunk8<false>(dx + row * lddx, c, uint32_t(cols), narrow8<TYPE>(f));
+    }
+  }
+}
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// A piece's rows of dweight: dzt (rows x k) times xt (cols x k), times what undoes the
+// scale of the largest |dloss|.
+template <class T, int TYPE, int OUT>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dweight_kernel(
+    Matrix16 dzt, Matrix16 xt, uint32_t k, const uint32_t* top, void* to, uint64_t ldo,
+    unsigned tiles_m, unsigned tiles_n) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
+  unsigned ti, tj;
+  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  floatx4 acc[T::kMT][T::kNT];
+  multiply_tile<T, TYPE>(dzt, xt, k, i0, j0, lds, acc);
+  const float back = 1.0f / top_scale(*top);
+  const uint64_t col = j0 + lane_col<T>();
+#pragma unroll
+  for (int i = 0; i < T::kMT; ++i) {
+    const uint64_t row = i0 + lane_row<T>() + i;
+    if (row >= dzt.rows) continue;
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y) acc[i][y] *= back;
+    if constexpr (OUT == ARMX_F32) {
+      float* o = static_cast<float*>(to) + row * ldo + col;
+#pragma unroll
+      for (int y = 0; y < T::kNT; ++y) {
+        if (col + 4 * y + 4 <= xt.rows) {
+          *reinterpret_cast<f32x4u*>(o + 4 * y) = acc[i][y];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + 4 * y + e < xt.rows) o[4 * y + e] = acc[i][y][e];
+        }
+      }
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(to) + row * ldo + col;
+#pragma unroll
+      for (int c = 0; c < T::kCols; c += 8) {
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = narrow2<OUT>(acc[i][c / 4 + e / 2][2 * (e % 2)],
+                              acc[i][c / 4 + e / 2][2 * (e % 2) + 1]);
+        if (col + c + 8 <= xt.rows) {
+          *reinterpret_cast<u32x4*>(o + c) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (col + c + e < xt.rows) o[c + e] = uint16_t(v[e / 2] >> (16 * (e % 2)));
+        }
+      }
+    }
+  }
+}
+
+// dweight of no rows at all.
+__global__ __launch_bounds__(256) void zero_rows_kernel(void* to, uint64_t row_bytes,
+                                                        uint64_t pitch, uint64_t rows) {
+  for (uint64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    for (uint64_t i = threadIdx.x * 2; i < row_bytes; i += 512)
+      *reinterpret_cast<uint16_t*>(static_cast<char*>(to) + row * pitch + i) = 0;
+}
+
+// ---- launches -----------------------------------------------------------------------------
+
+// Rows of dweight's products (its k) up to which a value of dz is kept in two terms.
+constexpr uint64_t kTwoTerms = 128;
+// dz of a piece: at most this many values, but at least kLeastPiece vocabulary rows.
+constexpr uint64_t kPieceValues = uint64_t(1) << 27;
+constexpr uint64_t kLeastPiece = 1024;
+constexpr uint64_t kRoom = 256;   // rows and columns of the largest tile
+
+uint64_t round_up(uint64_t v, uint64_t to) { return ceil_div(v, to) * to; }
+
+class Steps {
+ public:
+  Steps(const armx_config* cfg, hipStream_t stream) : cfg_(cfg), stream_(stream) {}
+  hipError_t run(const void* fn, dim3 grid, int threads, void** args, bool last = false) {
+    const bool first = first_;
+    first_ = false;
+    return launch_kernel(fn, grid, dim3(unsigned(threads)), args, 0, stream_,
+                         cfg_ && first ? static_cast<hipEvent_t>(cfg_->start_event) : nullptr,
+                         cfg_ && last ? static_cast<hipEvent_t>(cfg_->stop_event) : nullptr);
+  }
+
+ private:
+  const armx_config* cfg_;
+  hipStream_t stream_;
+  bool first_ = true;
+};
+
+__global__ void clear_kernel(uint32_t* v) { *v = 0; }
+
+hipError_t transpose(Steps& steps, const uint16_t* from, uint64_t ld, uint64_t rows, uint64_t cols,
+                     uint16_t* to, uint64_t ldt, const int64_t* targets, int64_t ignore,
+                     uint64_t copies) {
+  void* args[] = {&from, &ld, &rows, &cols, &to, &ldt, &targets, &ignore, &copies};
+  return steps.run(reinterpret_cast<const void*>(&transpose_kernel),
+                   dim3(unsigned(ceil_div(rows, 64)), unsigned(ceil_div(cols, 64))), 256, args);
+}
+
+template <int TYPE>
+hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& plan,
+                        const CrossEntropyGrads& grads, void* ws, int cu_count,
+                        const armx_config* cfg, hipStream_t stream) {
+  Steps steps(cfg, stream);
+  char* base = static_cast<char*>(ws);
+  uint32_t* top = reinterpret_cast<uint32_t*>(base + plan.top);
+  RowScale* rows = reinterpret_cast<RowScale*>(base + plan.rows);
+  uint16_t* dz = grads.dx ? reinterpret_cast<uint16_t*>(base + plan.dz) : nullptr;
+  uint16_t* dzt = grads.dweight ? reinterpret_cast<uint16_t*>(base + plan.dzt) : nullptr;
+  uint16_t* xt = reinterpret_cast<uint16_t*>(base + plan.xt);
+  uint16_t* wt = reinterpret_cast<uint16_t*>(base + plan.wt);
+  float* sums = reinterpret_cast<float*>(base + plan.dx);
+  CrossEntropyArgs copy = a;
+  const float *dloss = grads.dloss, *lse = grads.lse;
+  hipError_t e;
+  {
+    void* args[] = {&top};
+    e = steps.run(reinterpret_cast<const void*>(&clear_kernel), dim3(1), 1, args);
+    if (e != hipSuccess) return e;
+  }
+  {
+    void* args[] = {&copy, &dloss, &lse, &rows, &top};
+    e = steps.run(reinterpret_cast<const void*>(&loss_rows_kernel<TYPE>),
+                  dim3(unsigned(ceil_div(a.rows, 4))), 256, args);
+    if (e != hipSuccess) return e;
+  }
+  if (dzt) {
+    e = transpose(steps, a.x, a.ldx, a.rows, a.cols, xt, plan.ldt, a.targets, a.ignore, plan.terms);
+    if (e != hipSuccess) return e;
+  }
+  uint32_t cols = uint32_t(a.cols);
+  const int64_t* targets = a.targets;
+  uint64_t ldz = plan.ldz, ldt = plan.ldt, terms = plan.terms, ldd = plan.ldd;
+  for (uint64_t v0 = 0; v0 < a.vocab; v0 += plan.piece) {
+    const uint64_t count = a.vocab - v0 < plan.piece ? a.vocab - v0 : plan.piece;
+    const bool last = v0 + count == a.vocab;
+    unsigned tiles_m = 0, tiles_n = 0;
+    {
+      Matrix16 x{a.x, a.rows, a.rows > 1 ? a.ldx : 0};
+      Matrix16 w{a.weight + v0 * a.ldw, count, count > 1 ? a.ldw : 0};
+      int64_t first = int64_t(v0);
+      void* args[] = {&x, &w, &cols, &targets, &first, &lse, &rows, &top, &dz, &ldz, &dzt, &ldt,
+                      &terms, &tiles_m, &tiles_n};
+#define ARMX_TILE_CASE(T)                                                         \
+  tiles_m = unsigned(ceil_div(a.rows, uint64_t(T::kBM)));                         \
+  tiles_n = unsigned(ceil_div(count, uint64_t(T::kBN)));                          \
+  e = steps.run(reinterpret_cast<const void*>(&loss_grad_kernel<T, TYPE>),        \
+                dim3(tiles_m * tiles_n), T::kThreads, args, last && !dz && !dzt)
+      ARMX_OF_TILE(choose_tile16(a.rows, count, a.cols, cu_count), ARMX_TILE_CASE);
+#undef ARMX_TILE_CASE
+      if (e != hipSuccess) return e;
+    }
+    if (dz) {
+      e = transpose(steps, a.weight + v0 * a.ldw, a.ldw, count, a.cols, wt, plan.ldz, nullptr, 0, 1);
+      if (e != hipSuccess) return e;
+      Matrix16 mz{dz, a.rows, plan.ldz}, mw{wt, a.cols, plan.ldz};
+      uint32_t k = uint32_t(count);
+      uint32_t per = uint32_t(round_up(ceil_div(count, plan.splits), kStepValues));
+      bool more = v0 != 0;
+      void* args[] = {&mz, &mw, &k, &per, &sums, &ldd, &more, &tiles_m, &tiles_n};
+#define ARMX_TILE_CASE(T)                                                      \
+  tiles_m = unsigned(ceil_div(a.rows, uint64_t(T::kBM)));                      \
+  tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                      \
+  e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T, TYPE>),       \
+                dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args)
+      ARMX_OF_TILE(choose_tile16(a.rows * plan.splits, a.cols, per, cu_count), ARMX_TILE_CASE);
+#undef ARMX_TILE_CASE
+      if (e != hipSuccess) return e;
+    }
+    if (dzt) {
+      Matrix16 mz{dzt, count, plan.ldt}, mx{xt, a.cols, plan.ldt};
+      uint32_t k = uint32_t(a.rows * plan.terms);
+      const uint64_t size = grads.dweight_type == ARMX_F32 ? 4 : 2;
+      void* to = static_cast<char*>(grads.dweight) + v0 * grads.lddw * size;
+      uint64_t ldo = grads.lddw;
+      void* args[] = {&mz, &mx, &k, &top, &to, &ldo, &tiles_m, &tiles_n};
+#define ARMX_TILE_CASE(T)                                                                   \
+  tiles_m = unsigned(ceil_div(count, uint64_t(T::kBM)));                                    \
+  tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                                   \
+  e = steps.run(grads.dweight_type == ARMX_F32                                              \
+                    ? reinterpret_cast<const void*>(&loss_dweight_kernel<T, TYPE, ARMX_F32>) \
+                    : reinterpret_cast<const void*>(&loss_dweight_kernel<T, TYPE, TYPE>),   \
+                dim3(tiles_m * tiles_n), T::kThreads, args, last && !dz)
+      ARMX_OF_TILE(choose_tile16(count, a.cols, k, cu_count), ARMX_TILE_CASE);
+#undef ARMX_TILE_CASE
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (!dz) return hipSuccess;
+  const float* from = sums;
+  uint64_t splits = plan.splits, count = a.rows, all = a.cols, lddx = grads.lddx;
+  const RowScale* scales = rows;
+  uint16_t* dx = grads.dx;
+  void* args[] = {&from, &ldd, &splits, &scales, &count, &all, &dx, &lddx};
+  return steps.run(reinterpret_cast<const void*>(&loss_dx_join_kernel<TYPE>),
+                   dim3(unsigned(count < kMaxGrid ? count : kMaxGrid)), 256, args, true);
+}
+
+}  // namespace
+
+CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, uint64_t cols,
+                                                 bool dx, bool dweight, int cu_count) {
+  CrossEntropyGradPlan p;
+  if (rows == 0 || vocab == 0 || cols == 0) return p;
+  p.piece = kPieceValues / rows / kRoom * kRoom;
+  if (p.piece < kLeastPiece) p.piece = kLeastPiece;
+  // (and the grids of its products and its transpose)
+  const uint64_t most = (uint64_t(1) << 34) / round_up(cols, kRoom) / kRoom * kRoom;
+  if (p.piece > most) p.piece = most;
+  if (p.piece > round_up(vocab, kRoom)) p.piece = round_up(vocab, kRoom);
+  // no larger than what the pieces share evenly
+  p.piece = round_up(ceil_div(vocab, ceil_div(vocab, p.piece)), kRoom);
+  p.ldz = p.piece;
+  p.terms = rows <= kTwoTerms ? 2 : 1;
+  p.ldt = p.terms == 2 ? round_up(2 * rows, 8) : round_up(rows, kRoom);
+  p.ldd = round_up(cols, kRoom);
+  // products for dx of few tiles: parts of the piece in blocks of their own
+  const uint64_t tiles = ceil_div(rows, 128) * ceil_div(cols, 128);
+  p.splits = 1;
+  while (p.splits < 64 && tiles * p.splits < uint64_t(cu_count) &&
+         p.piece / (2 * p.splits) >= 512)
+    p.splits *= 2;
+  size_t at = 0;
+  auto take = [&](size_t& offset, uint64_t bytes) {
+    offset = at;
+    at += size_t(round_up(bytes, 256));
+  };
+  take(p.top, 4);
+  take(p.rows, rows * sizeof(RowScale));
+  if (dx) {
+    take(p.dz, rows * p.ldz * 2);
+    take(p.wt, cols * p.ldz * 2);
+    take(p.dx, p.splits * rows * p.ldd * 4);
+  }
+  if (dweight) {
+    take(p.dzt, p.piece * p.ldt * 2);
+    take(p.xt, cols * p.ldt * 2);
+  }
+  p.ws_bytes = at;
+  return p;
+}
+
+hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& a,
+                                         const CrossEntropyGradPlan& plan,
+                                         const CrossEntropyGrads& grads, void* ws, int cu_count,
+                                         const armx_config* cfg, hipStream_t stream) {
+  if (a.rows == 0) {
+    if (!grads.dweight) return hipSuccess;
+    const uint64_t size = grads.dweight_type == ARMX_F32 ? 4 : 2;
+    void* to = grads.dweight;
+    uint64_t bytes = a.cols * size, pitch = grads.lddw * size, rows = a.vocab;
+    void* args[] = {&to, &bytes, &pitch, &rows};
+    return Steps(cfg, stream).run(reinterpret_cast<const void*>(&zero_rows_kernel),
+                                  dim3(unsigned(rows < kMaxGrid ? rows : kMaxGrid)), 256, args,
+                                  true);
+  }
+  return a.type == ARMX_F16
+             ? launch_grads<ARMX_F16>(a, plan, grads, ws, cu_count, cfg, stream)
+             : launch_grads<ARMX_BF16>(a, plan, grads, ws, cu_count, cfg, stream);
+}
+
+}  // namespace armx

@@ -1,0 +1,231 @@
+// The softmax cross entropy of rows x (hidden states) against the rows of a weight (a
+// vocabulary's output vectors): z = x w^T, lse = log sum over v of exp(z), loss =
+// lse - z[target].  The logits z are made tile by tile in registers and never stored:
+// of each row's 64 columns of a tile its largest z and its sum of exp(z - largest) are
+// kept, and those are joined in order by a second kernel.
+//
+// A row's sums do not depend on the tile that makes them: k runs in order in every
+// tile, a wavefront has 64 columns, and their sum is a balanced tree over them.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "cross_entropy.h"
+#include "device_common.hpp"
+#include "launch.h"
+#include "tile16.hpp"
+#include "tile16_choice.hpp"
+
+namespace armx {
+namespace {
+
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kMinusInf = -__builtin_inff();
+
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2E); }
+
+__device__ __forceinline__ float max_xor16(float v) {
+  auto p = __builtin_amdgcn_permlane16_swap(fbits(v), fbits(v), false, false);
+  return __builtin_fmaxf(bitsf(int(p[0])), bitsf(int(p[1])));
+}
+__device__ __forceinline__ float max_xor32(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(fbits(v), fbits(v), false, false);
+  return __builtin_fmaxf(bitsf(int(p[0])), bitsf(int(p[1])));
+}
+
+struct Part {
+  float top, sum;   // largest z, sum of exp(z - top)
+};
+
+template <class T, int TYPE>
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel(
+    Matrix16 x, Matrix16 w, uint32_t cols, const int64_t* targets, Part* parts, float* hits,
+    unsigned tiles_m, unsigned tiles_n) {
+  static_assert(T::kNT == 4, "a wavefront's columns are one piece");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
+  unsigned ti, tj;
+  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  floatx4 z[T::kMT][T::kNT];
+  multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
+  const uint64_t col = j0 + lane_col<T>();
+  // a wavefront whose columns are all past the vocabulary has nothing to add
+  const uint64_t piece = (j0 + (wave_id() / T::kWM) * kLossPiece) / kLossPiece;
+  if (piece * kLossPiece >= w.rows) return;
+  if (j0 + T::kBN > w.rows) {
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + 4 * y + e >= w.rows) {
+#pragma unroll
+          for (int i = 0; i < T::kMT; ++i) z[i][y][e] = kMinusInf;
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < T::kMT; ++i) {
+    const uint64_t row = i0 + lane_row<T>() + i;
+    float m = kMinusInf;
+#pragma unroll
+    for (int y = 0; y < T::kNT; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = __builtin_fmaxf(m, z[i][y][e]);
+    m = max_xor32(max_xor16(m));
+    const float from = m == kMinusInf ? 0.0f : m;
+    float s[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const floatx4 v = z[i][y];
+      s[y] = (exp_of(v[0] - from) + exp_of(v[1] - from)) +
+             (exp_of(v[2] - from) + exp_of(v[3] - from));
+    }
+    const float sum = add_xor32(add_xor16((s[0] + s[1]) + (s[2] + s[3])));
+    if (row < x.rows) {
+      if (lane_id() < 16) parts[piece * x.rows + row] = Part{m, sum};
+      const int64_t at = targets[row] - int64_t(col);
+      if (at >= 0 && at < T::kCols && targets[row] < int64_t(w.rows)) {
+        float hit = 0.0f;
+#pragma unroll
+        for (int c = 0; c < T::kCols; ++c) hit = at == c ? z[i][c / 4][c % 4] : hit;
+        hits[row] = hit;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float share(float top, float of) {
+  return top == kMinusInf ? 0.0f : exp_of(top - of);
+}
+
+// 16 rows a block: 16 threads take a row's pieces, number p of them p, p + 16, ..., eight
+// at a time, and their sums are joined in order.
+constexpr int kJoinRows = 16, kJoinThreads = 16, kJoinFlight = 8;
+__global__ __launch_bounds__(kJoinRows * kJoinThreads) void cross_entropy_join_kernel(
+    const Part* parts, uint64_t pieces, const float* hits, const int64_t* targets, uint64_t rows,
+    uint64_t vocab, int64_t ignore, float* loss, float* lse) {
+  __shared__ Part of[kJoinThreads][kJoinRows];
+  const uint32_t r = threadIdx.x % kJoinRows, p = threadIdx.x / kJoinRows;
+  const uint64_t row = uint64_t(blockIdx.x) * kJoinRows + r;
+  const uint64_t from = row < rows ? row : rows - 1;
+  Part all = {kMinusInf, 0.0f};
+  for (uint64_t q = p; q < pieces; q += kJoinThreads * kJoinFlight) {
+    Part v[kJoinFlight];
+    float m = all.top;
+#pragma unroll
+    for (int i = 0; i < kJoinFlight; ++i) {
+      const uint64_t qi = q + uint64_t(i) * kJoinThreads;
+      v[i] = parts[(qi < pieces ? qi : q) * rows + from];
+      if (qi >= pieces) v[i] = Part{kMinusInf, 0.0f};
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinFlight; ++i) m = __builtin_fmaxf(m, v[i].top);
+    float s = all.sum * share(all.top, m);
+    // (a piece without a largest has a sum of 0, or of NaNs, which stay)
+#pragma unroll
+    for (int i = 0; i < kJoinFlight; ++i)
+      s += v[i].top == kMinusInf ? v[i].sum : v[i].sum * exp_of(v[i].top - m);
+    all = Part{m, s};
+  }
+  of[p][r] = all;
+  __syncthreads();
+  if (p != 0 || row >= rows) return;
+  float m = kMinusInf;
+  for (int i = 0; i < kJoinThreads; ++i) m = __builtin_fmaxf(m, of[i][r].top);
+  float s = 0.0f;
+  for (int i = 0; i < kJoinThreads; ++i)
+    s += of[i][r].top == kMinusInf ? of[i][r].sum : of[i][r].sum * exp_of(of[i][r].top - m);
+  const float l = m + __builtin_logf(s);
+  const int64_t t = targets[row];
+  lse[row] = l;
+  loss[row] = t == ignore ? 0.0f
+              : t >= 0 && t < int64_t(vocab) ? l - hits[row]
+                                             : __builtin_nanf("");
+}
+
+}  // namespace
+
+Tile16Size tile16_size(int index) {
+  Tile16Size s{0, 0};
+#define ARMX_TILE_CASE(T) s = Tile16Size{T::kBM, T::kBN}
+  ARMX_OF_TILE(index, ARMX_TILE_CASE);
+#undef ARMX_TILE_CASE
+  return s;
+}
+
+// The tile whose estimated time is least: a compute unit makes its tiles one after the
+// other (`resident` at a time), each taking `fixed` and `each` for a step of 64 values
+// of k (us).
+int choose_tile16(uint64_t m, uint64_t n, uint64_t k, int cu_count) {
+  struct Time {
+    int resident;
+    float fixed, each;
+  };
+  constexpr Time times[kTile16s] = {{1, 3.0f, 1.50f}, {1, 3.0f, 0.86f}, {1, 2.6f, 0.52f},
+                                    {2, 2.2f, 0.33f}, {2, 2.0f, 0.22f}, {2, 2.0f, 0.16f}};
+  int best = -1;
+  double least = 0;
+  for (int i = 0; i < kTile16s; ++i) {
+    const Tile16Size s = tile16_size(i);
+    const uint64_t tiles = ceil_div(m, uint64_t(s.bm)) * ceil_div(n, uint64_t(s.bn));
+    if (tiles > 0x7FFFFFFFu / 1024) continue;  // the grid's limit
+    const double per_cu = double(ceil_div(tiles, uint64_t(cu_count)));
+    const double t = double(ceil_div(uint64_t(per_cu), uint64_t(times[i].resident))) *
+                         times[i].fixed +
+                     per_cu * double(ceil_div(k, uint64_t(kStepValues))) * times[i].each;
+    if (best < 0 || t < least) best = i, least = t;
+  }
+  return best;
+}
+
+namespace {
+
+template <int TYPE>
+hipError_t launch_loss(const CrossEntropyArgs& a, const CrossEntropyPlan& plan, float* loss,
+                       float* lse, void* ws, int cu_count, const armx_config* cfg,
+                       hipStream_t stream) {
+  Matrix16 x{a.x, a.rows, a.rows > 1 ? a.ldx : 0}, w{a.weight, a.vocab, a.vocab > 1 ? a.ldw : 0};
+  uint32_t cols = uint32_t(a.cols);
+  const int64_t* targets = a.targets;
+  Part* parts = reinterpret_cast<Part*>(static_cast<char*>(ws) + plan.partials);
+  float* hits = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.hits);
+  unsigned tiles_m = 0, tiles_n = 0;
+  void* args[] = {&x, &w, &cols, &targets, &parts, &hits, &tiles_m, &tiles_n};
+  hipError_t e = hipErrorInvalidValue;
+#define ARMX_TILE_CASE(T)                                                                      \
+  tiles_m = unsigned(ceil_div(a.rows, uint64_t(T::kBM)));                                      \
+  tiles_n = unsigned(ceil_div(a.vocab, uint64_t(T::kBN)));                                     \
+  e = launch_kernel(reinterpret_cast<const void*>(&cross_entropy_kernel<T, TYPE>),             \
+                    dim3(tiles_m * tiles_n), dim3(T::kThreads), args, 0, stream,               \
+                    cfg ? static_cast<hipEvent_t>(cfg->start_event) : nullptr, nullptr)
+  ARMX_OF_TILE(choose_tile16(a.rows, a.vocab, a.cols, cu_count), ARMX_TILE_CASE);
+#undef ARMX_TILE_CASE
+  if (e != hipSuccess) return e;
+  const Part* from = parts;
+  uint64_t pieces = plan.pieces, rows = a.rows, vocab = a.vocab;
+  const float* found = hits;
+  int64_t ignore = a.ignore;
+  void* join[] = {&from, &pieces, &found, &targets, &rows, &vocab, &ignore, &loss, &lse};
+  return launch_kernel(reinterpret_cast<const void*>(&cross_entropy_join_kernel),
+                       dim3(unsigned(ceil_div(rows, uint64_t(kJoinRows)))),
+                       dim3(kJoinRows * kJoinThreads), join, 0, stream, nullptr,
+                       cfg ? static_cast<hipEvent_t>(cfg->stop_event) : nullptr);
+}
+
+}  // namespace
+
+CrossEntropyPlan plan_cross_entropy(uint64_t rows, uint64_t vocab) {
+  CrossEntropyPlan p;
+  p.pieces = ceil_div(vocab, kLossPiece);
+  p.hits = size_t(p.pieces * rows * sizeof(Part));
+  p.ws_bytes = p.hits + size_t(rows * sizeof(float));
+  return p;
+}
+
+hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPlan& plan,
+                                float* loss, float* lse, void* ws, int cu_count,
+                                const armx_config* cfg, hipStream_t stream) {
+  return a.type == ARMX_F16 ? launch_loss<ARMX_F16>(a, plan, loss, lse, ws, cu_count, cfg, stream)
+                            : launch_loss<ARMX_BF16>(a, plan, loss, lse, ws, cu_count, cfg, stream);
+}
+
+}  // namespace armx

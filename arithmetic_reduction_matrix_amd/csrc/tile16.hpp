@@ -1,0 +1,331 @@
+// Tiles of products of 16-bit matrices whose rows both lie along the sum, by
+// v_mfma_f32_16x16x32_{f16,bf16}, summed in binary32.  Each source that includes it
+// gets its own.
+//
+// Operand layout: lane l of a wavefront supplies row l % 16 of its 16-row operand tile
+// and the 8 consecutive values of k-group l / 16, one 16-byte piece.  The rows of b go
+// in as the MFMA's first operand and those of a as its second, so that lane l ends with
+// the product's row l % 16 and the 4 consecutive columns 4 (l / 16) .. + 3.
+//
+// Which rows of a and b make up an operand tile is free.  Row r of operand tile x of a
+// wavefront's kMT is its row r kMT + x, and row 4 q + e of operand tile y of b's kNT is
+// its column 4 (q kNT + y) + e: lane (q, r) ends with kMT consecutive rows of 4 kNT
+// consecutive columns, whole pieces of either order of the product.
+//
+// Steps of 64 values of k (128 bytes, a line) go from memory straight to LDS
+// (buffer_load ... lds) into one of NS buffers, NS - 1 steps ahead of the one that is
+// multiplied.  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
+// tile keeps its piece c in slot c ^ swizzle(r), so that the 16 lanes of a 16-byte LDS
+// read, whose rows are 128 bytes apart, meet no bank twice.  The load writes LDS in
+// lane order, so the swizzle is made on the memory side: the lane that fills slot s of
+// row r fetches piece s ^ swizzle(r).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.hpp"
+
+namespace armx {
+namespace {
+
+using namespace dev;
+
+#define ARMX_INLINE __attribute__((always_inline))
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <int TYPE>
+__device__ __forceinline__ floatx4 mfma16(u32x4 x, u32x4 y, floatx4 acc) {
+  if constexpr (TYPE == ARMX_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, x),
+                                                  __builtin_bit_cast(half8, y), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
+                                                   __builtin_bit_cast(bf16x8, y), acc, 0, 0, 0);
+}
+
+// A matrix of 16-bit values, `k` of each row counting.  `ld` (values, a multiple of 8)
+// is at most kMaxTileLd, so that a tile's rows are reached by 32-bit offsets.
+constexpr uint64_t kMaxTileLd = uint64_t(1) << 22;
+struct Matrix16 {
+  const uint16_t* p;
+  uint64_t rows, ld;
+};
+
+// Rows from row0 on as a range-checked buffer that ends with the 32-bit word of the
+// last row's last value: reads past it return zeros without a memory access.
+constexpr int kTileBuffer = 0x00020000;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const Matrix16& m, uint64_t k,
+                                                            uint64_t row0) {
+  uint64_t left = row0 < m.rows ? (m.rows - 1 - row0) * m.ld * 2 + (k + 1) / 2 * 4 : 0;
+  if (left > 0xFFFFFFF0u) left = 0xFFFFFFF0u;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(m.p + (left ? row0 * m.ld : 0)),
+                                           0, int(uint32_t(left)), kTileBuffer);
+}
+
+// The first `keep` of a lane's 8 values (keep <= 0: none), the others zero.
+__device__ __forceinline__ u32x4 keep_values(u32x4 v, int keep) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = keep - 2 * i;
+    v[i] &= n >= 2 ? 0xFFFFFFFFu : n <= 0 ? 0u : 0xFFFFu;
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+using Yes = Int<1>;
+using No = Int<0>;
+
+constexpr int kStepBytes = 128, kStepValues = 64;
+
+// A block makes BM x BN of the product with WM x WN wavefronts and NS buffers.
+template <int BM, int BN, int WM, int WN, int NS>
+struct Tile16 {
+  static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
+  static constexpr int kNT = BN / WN / 16;
+  static constexpr int kRows = kMT, kCols = 4 * kNT;   // a lane's part of the product
+  static constexpr int kLoadsA = BM / 8 / kWaves;  // wavefront loads per step
+  static constexpr int kLoadsB = BN / 8 / kWaves;
+  static constexpr int kStage = (BM + BN) * kStepBytes;
+  static constexpr int kLdsBytes = NS * kStage;
+  // wavefronts per SIMD that the LDS leaves room for, at most 2 (of 256 registers)
+  static constexpr int kResident = 160 * 1024 / kLdsBytes * kWaves / 4;
+  static constexpr int kPerSimd = kResident < 1 ? 1 : kResident < 2 ? kResident : 2;
+  static_assert(kLoadsA * 8 * kWaves == BM && kLoadsB * 8 * kWaves == BN, "whole loads");
+  static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
+  static_assert(NS >= 2 && NS <= 4, "the last steps are written out");
+  static_assert(kMT <= 16 && kNT <= 16, "operand tiles");
+};
+
+typedef __attribute__((address_space(3))) int8_t tile_lds_byte;
+
+// 16 bytes per lane from `rows` into LDS at `lds` + 16 lane.  Written as asm so that
+// the compiler, which cannot tell the buffers apart, does not wait for these loads
+// before every read of LDS; nothing comes back in registers, and wait_loads() and a
+// barrier stand between these writes and their reads.  The load reads M0, which needs a
+// wait state after its scalar write; the compiler puts none inside an asm string.  (M0
+// is a reserved register, which a clobber list cannot name; the compiler uses it for
+// nothing else here.)
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rows, uint32_t lds,
+                                           uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(rows)
+               : "memory");
+}
+
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
+  return *reinterpret_cast<const u32x4 __attribute__((address_space(3)))*>(at);
+}
+
+// vmcnt(N): all but this wavefront's last N loads into LDS have landed
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the count's six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+// Which tile a block makes: every XCD takes a contiguous range of ids, and ids run down
+// kTileGroup rows of tiles before the next column, so that blocks running at the same
+// time on one XCD share operand rows in its L2.
+constexpr unsigned kTileGroup = 4;
+__device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned tiles_n,
+                                        unsigned& ti, unsigned& tj) {
+  const unsigned per = kTileGroup * tiles_n, grp = id / per, first = grp * kTileGroup;
+  const unsigned rows = tiles_m - first < kTileGroup ? tiles_m - first : kTileGroup;
+  const unsigned in = id - grp * per;
+  ti = first + in % rows;
+  tj = in / rows;
+}
+
+// acc = the tile at (i0, j0) of a b^T over k values, rows and columns past the
+// matrices' undefined.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
+// barrier.  Every thread of the block takes part.
+template <class T, int TYPE>
+__device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16& mb, uint32_t k,
+                                              uint64_t i0, uint64_t j0, int8_t* lds,
+                                              floatx4 (&acc)[T::kMT][T::kNT]) {
+  constexpr int kMT = T::kMT, kNT = T::kNT, NS = T::kNS;
+  const int lane = lane_id(), w = wave_id();
+  const uint32_t ring = uint32_t(reinterpret_cast<uintptr_t>((tile_lds_byte*)lds));
+  uint32_t base = ring;
+  auto next = [&](uint32_t at) ARMX_INLINE {
+    return at == ring + (NS - 1) * T::kStage ? ring : at + T::kStage;
+  };
+  const __amdgpu_buffer_rsrc_t a = tile_rows(ma, k, i0), b = tile_rows(mb, k, j0);
+  // rows past the matrix are read from its last row
+  const uint32_t last_a = uint32_t(ma.rows - 1 - i0 < T::kBM ? ma.rows - 1 - i0 : T::kBM - 1);
+  const uint32_t last_b = uint32_t(mb.rows - 1 - j0 < T::kBN ? mb.rows - 1 - j0 : T::kBN - 1);
+  // byte offsets of the pieces that this lane brings into its slots of LDS rows
+  uint32_t off_a[T::kLoadsA], off_b[T::kLoadsB];
+#pragma unroll
+  for (int x = 0; x < T::kLoadsA; ++x) {
+    const uint32_t slot = (w * T::kLoadsA + x) * 8 + (lane >> 3);
+    const uint32_t in = slot % (16 * kMT), r = in % 16;
+    const uint32_t row = slot / (16 * kMT) * (16 * kMT) + r * kMT + in / 16;
+    off_a[x] = (row < last_a ? row : last_a) * uint32_t(ma.ld * 2) +
+               ((uint32_t(lane) & 7) ^ swizzle(r)) * 16;
+  }
+#pragma unroll
+  for (int x = 0; x < T::kLoadsB; ++x) {
+    const uint32_t slot = (w * T::kLoadsB + x) * 8 + (lane >> 3);
+    const uint32_t in = slot % (16 * kNT), r = in % 16;
+    const uint32_t row =
+        slot / (16 * kNT) * (16 * kNT) + r / 4 * (4 * kNT) + in / 16 * 4 + r % 4;
+    off_b[x] = (row < last_b ? row : last_b) * uint32_t(mb.ld * 2) +
+               ((uint32_t(lane) & 7) ^ swizzle(r)) * 16;
+  }
+  // wavefront load x of the step at byte k0, into the buffer at `to`
+  auto stage_one = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    if (x < T::kLoadsA) {
+      lds_load16(a, to + (w * T::kLoadsA + x) * 1024, off_a[x] + k0);
+    } else {
+      x -= T::kLoadsA;
+      lds_load16(b, to + T::kBM * kStepBytes + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
+    }
+  };
+  constexpr int kLoads = T::kLoadsA + T::kLoadsB;
+  auto stage = [&](uint32_t to, uint32_t k0) ARMX_INLINE {
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) stage_one(to, k0, x);
+  };
+  // all but the block's last `steps` steps of loads have landed and all its reads are done
+  auto sync = [&](auto steps) ARMX_INLINE {
+    wait_loads<decltype(steps)::value * kLoads>();
+    if constexpr (T::kWaves > 1)
+      __syncthreads();
+    else
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  // operand registers of half a step (32 values of k): lane l reads row l % 16 of each
+  // operand tile, piece 4 half + l / 16
+  const uint32_t r = lane & 15, g = lane >> 4;
+  uint32_t at_a[2], at_b[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t in = r * kStepBytes + ((4 * h + g) ^ swizzle(r)) * 16;
+    at_a[h] = (w % T::kWM) * (kMT * 16 * kStepBytes) + in;
+    at_b[h] = (T::kBM + (w / T::kWM) * (kNT * 16)) * kStepBytes + in;
+  }
+  u32x4 fa[2][kMT], fb[2][kNT];
+  constexpr int kReads = kMT + kNT;
+  // Where this lane reads half h of the buffer at `from`; opaque to the compiler, so
+  // that it keeps two addresses and puts the rest into the reads' offsets.
+  struct Place {
+    uint32_t a, b;
+  };
+  auto place = [&](uint32_t from, int h) ARMX_INLINE {
+    Place at = {from + at_a[h], from + at_b[h]};
+    asm("" : "+v"(at.a));
+    asm("" : "+v"(at.b));
+    return at;
+  };
+  // read j of half h, in the order in which its products need them
+  auto fetch = [&](Place at, int h, int j) ARMX_INLINE {
+    if (j < kNT)
+      fb[h][j] = lds_read16(at.b + j * 16 * kStepBytes);
+    else
+      fa[h][j - kNT] = lds_read16(at.a + (j - kNT) * 16 * kStepBytes);
+  };
+  auto fetch_half = [&](uint32_t from, int h) ARMX_INLINE {
+    const Place at = place(from, h);
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) {
+      fetch(at, h, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // values past k are cut from both operands (what stands there may be a NaN)
+  auto mask_half = [&](uint32_t k0, int h) ARMX_INLINE {
+    const int keep = int(k) - int(k0 + 32 * h + 8 * g);
+#pragma unroll
+    for (int x = 0; x < kMT; ++x) fa[h][x] = keep_values(fa[h][x], keep);
+#pragma unroll
+    for (int y = 0; y < kNT; ++y) fb[h][y] = keep_values(fb[h][y], keep);
+  };
+#pragma unroll
+  for (int x = 0; x < kMT; ++x)
+#pragma unroll
+    for (int y = 0; y < kNT; ++y) acc[x][y] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply_row = [&](int h, int x) ARMX_INLINE {
+#pragma unroll
+    for (int y = 0; y < kNT; ++y) acc[x][y] = mfma16<TYPE>(fb[h][y], fa[h][x], acc[x][y]);
+  };
+  auto multiply = [&](int h) ARMX_INLINE {
+#pragma unroll
+    for (int x = 0; x < kMT; ++x) multiply_row(h, x);
+  };
+  // The products of one half, with the other's operands (h) read from `from` and, with
+  // SEND, the loads of the step at byte k0 into `to` spread between them.
+  auto multiply_and_fetch = [&](int h, uint32_t from, auto send, uint32_t to, uint32_t k0)
+      ARMX_INLINE {
+    constexpr int kPer = (kLoads + kMT - 1) / kMT;
+    constexpr int kPerR = (kReads + kMT - 1) / kMT;
+    const Place at = place(from, h);
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+      if constexpr (send.value) {
+#pragma unroll
+        for (int j = i * kPer; j < (i + 1) * kPer; ++j)
+          if (j < kLoads) stage_one(to, k0, j);
+      }
+#pragma unroll
+      for (int j = i * kPerR; j < (i + 1) * kPerR; ++j)
+        if (j < kReads) fetch(at, h, j);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply_row(1 - h, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // A step but the last (its first half's operands already in registers): the second
+  // half's are read while the first is multiplied; then, after the barrier that ends
+  // all reading of this buffer and finds the next one filled (`out`: steps sent for
+  // behind that one), the step NS on is sent for into it (SEND) and the next step's
+  // first half read under the second half's products.
+  auto step = [&](auto send, auto out, uint32_t s) ARMX_INLINE {
+    multiply_and_fetch(1, base, No{}, 0, 0);
+    sync(out);
+    const uint32_t other = next(base);
+    multiply_and_fetch(0, other, send, base, (s + NS) * kStepBytes);
+    base = other;
+  };
+  if (k == 0) return;
+  const uint32_t steps = (k + kStepValues - 1) / kStepValues;
+  uint32_t s = 0;
+  if (steps >= NS) {
+#pragma unroll
+    for (int t = 0; t < NS; ++t) stage(ring + t * T::kStage, t * kStepBytes);
+    sync(Int<NS - 1>{});
+  } else {
+    for (uint32_t t = 0; t < steps; ++t) stage(ring + t * T::kStage, t * kStepBytes);
+    sync(No{});
+  }
+  fetch_half(base, 0);
+  for (; steps - s > NS; ++s) step(Yes{}, Int<NS - 2>{}, s);
+  // the last steps; what is still out shrinks with them
+  if constexpr (NS > 3)
+    if (steps - s > 3) step(No{}, Int<NS - 2>{}, s), ++s;
+  if constexpr (NS > 2)
+    if (steps - s > 2) step(No{}, Int<1>{}, s), ++s;
+  if (steps - s > 1) step(No{}, No{}, s), ++s;
+  // (one half after the other: the registers do not hold both beside the masks)
+  const bool cut = k % kStepValues != 0;
+  if (cut) mask_half(s * kStepValues, 0);
+  multiply(0);
+  fetch_half(base, 1);
+  if (cut) mask_half(s * kStepValues, 1);
+  multiply(1);
+}
+
+}  // namespace
+}  // namespace armx

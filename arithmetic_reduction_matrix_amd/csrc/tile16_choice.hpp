@@ -1,0 +1,45 @@
+// The tiles that the products of 16-bit matrices are made of, and launches of them.
+#pragma once
+
+#include "cross_entropy.h"
+#include "launch.h"
+#include "tile16.hpp"
+
+namespace armx {
+namespace {
+
+typedef Tile16<256, 256, 2, 4, 2> Tile0;
+typedef Tile16<128, 256, 2, 4, 3> Tile1;
+typedef Tile16<128, 128, 2, 2, 4> Tile2;
+typedef Tile16<64, 128, 2, 2, 3> Tile3;
+typedef Tile16<32, 128, 1, 2, 4> Tile4;
+typedef Tile16<16, 128, 1, 2, 4> Tile5;
+constexpr int kTile16s = 6;
+
+// Calls CASE(T) for tile number `index`.
+#define ARMX_OF_TILE(index, CASE) \
+  do {                            \
+    switch (index) {              \
+      case 0: CASE(Tile0); break; \
+      case 1: CASE(Tile1); break; \
+      case 2: CASE(Tile2); break; \
+      case 3: CASE(Tile3); break; \
+      case 4: CASE(Tile4); break; \
+      case 5: CASE(Tile5); break; \
+    }                             \
+  } while (0)
+
+inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// The first row and column of the product that a lane of a wavefront holds, in its tile.
+template <class T>
+__device__ __forceinline__ uint32_t lane_row() {
+  return (wave_id() % T::kWM) * (T::kBM / T::kWM) + (lane_id() & 15) * T::kRows;
+}
+template <class T>
+__device__ __forceinline__ uint32_t lane_col() {
+  return (wave_id() / T::kWM) * (T::kBN / T::kWN) + (lane_id() >> 4) * T::kCols;
+}
+
+}  // namespace
+}  // namespace armx

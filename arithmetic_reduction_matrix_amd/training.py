@@ -15,10 +15,11 @@ from typing import NamedTuple
 import torch
 
 from . import Config, _event_handle, lib
-from .layer import _binding, _done
+from .layer import _TYPES, _binding, _done
 
-__all__ = ["dropout_rows", "layer_norm_rows", "layer_norm_rows_backward", "Dropout", "LayerNorm",
-           "LayerNormGrads"]
+__all__ = ["dropout_rows", "layer_norm_rows", "layer_norm_rows_backward", "cross_entropy_rows",
+           "cross_entropy_rows_backward", "Dropout", "LayerNorm", "LayerNormGrads",
+           "CrossEntropy", "CrossEntropyGrads"]
 
 
 class Dropout(NamedTuple):
@@ -56,6 +57,18 @@ class LayerNormGrads(NamedTuple):
     dresidual: torch.Tensor | None
 
 
+class CrossEntropy(NamedTuple):
+    """float32 ``loss`` of every row and ``lse``, the log of its sum of exponentials."""
+    loss: torch.Tensor
+    lse: torch.Tensor
+
+
+class CrossEntropyGrads(NamedTuple):
+    """Gradients of a loss's hidden states and of its weight (None if not wanted)."""
+    dx: torch.Tensor | None
+    dweight: torch.Tensor | None
+
+
 class _DropoutArgs(ctypes.Structure):
     """Mirror of ``armx_dropout``."""
 
@@ -71,8 +84,19 @@ lib.layer_norm_rows.argtypes = [_vp, _sz, _vp, _sz, _vp, _vp, _ci, _sz, _sz, _cf
 lib.layer_norm_rows_backward.argtypes = [_vp, _sz, _vp, _sz, _vp, _vp, _vp, _vp, _sz, _ci, _sz,
                                          _sz, _dropp, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _sz,
                                          _cfgp, _vp]
-for _f in (lib.dropout_rows, lib.layer_norm_rows, lib.layer_norm_rows_backward):
+_i64 = ctypes.c_int64
+lib.cross_entropy_rows.argtypes = [_vp, _sz, _vp, _sz, _vp, _ci, _sz, _sz, _sz, _i64, _vp, _vp,
+                                   _vp, _sz, _cfgp, _vp]
+lib.cross_entropy_rows_backward.argtypes = [_vp, _vp, _sz, _vp, _sz, _vp, _vp, _ci, _sz, _sz, _sz,
+                                            _i64, _vp, _sz, _vp, _sz, _ci, _vp, _sz, _cfgp, _vp]
+lib.armx_cross_entropy_workspace_bytes.argtypes = [_sz, _sz, _sz]
+lib.armx_cross_entropy_backward_workspace_bytes.argtypes = [_sz, _sz, _sz, _ci, _ci]
+for _f in (lib.dropout_rows, lib.layer_norm_rows, lib.layer_norm_rows_backward,
+           lib.cross_entropy_rows, lib.cross_entropy_rows_backward):
     _f.restype = ctypes.c_int
+for _f in (lib.armx_cross_entropy_workspace_bytes,
+           lib.armx_cross_entropy_backward_workspace_bytes):
+    _f.restype = _sz
 
 
 def dropout_rows(x: torch.Tensor, dropout: Dropout, *, residual: torch.Tensor | None = None,
@@ -124,3 +148,44 @@ def layer_norm_rows_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
                                                    _event_handle(start_event),
                                                    _event_handle(stop_event)),
                  "layer_norm_rows_backward", LayerNormGrads)
+
+
+def cross_entropy_rows(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
+                       ignore_index: int = -100, loss: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       start_event=None, stop_event=None) -> CrossEntropy:
+    """Softmax cross entropy of every row of ``x`` (rows, cols; float16 or bfloat16)
+    against the vocabulary of ``weight`` (vocab, cols): the loss of the logits
+    ``x @ weight.T``, which are never stored, at ``targets`` (int64), and the log of their
+    sums of exponentials, which ``cross_entropy_rows_backward`` takes (both float32).
+
+    Rows whose target is ``ignore_index`` have loss 0 (the mean is ``loss.sum()`` over the
+    count of the others); another target outside the vocabulary gives NaN.  A row's loss
+    depends on that row and the weight only."""
+    return _done(_binding.cross_entropy_rows(x, weight, targets, ignore_index, loss, lse,
+                                             workspace, _event_handle(start_event),
+                                             _event_handle(stop_event)),
+                 "cross_entropy_rows", CrossEntropy)
+
+
+def cross_entropy_rows_backward(dloss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                                targets: torch.Tensor, lse: torch.Tensor, *,
+                                ignore_index: int = -100, need_dx: bool = True,
+                                need_dweight: bool = True, out: torch.Tensor | None = None,
+                                dweight: torch.Tensor | None = None,
+                                dweight_dtype: torch.dtype | None = None,
+                                workspace: torch.Tensor | None = None, start_event=None,
+                                stop_event=None) -> CrossEntropyGrads:
+    """Gradients of ``cross_entropy_rows``: ``dloss`` (float32) is the gradient of every
+    row's loss, ``lse`` as it returned them.  Returns dx (of x's type; ``out`` receives
+    it) and dweight (x's type, or float32 by ``dweight_dtype`` or by ``dweight``), each
+    None if not wanted.  The logits are made again, a piece of the vocabulary at a time;
+    without ``workspace`` one is taken from the allocator for this call (about 0.6 GB of
+    pieces and transposes at 4096 rows of 4096 values)."""
+    code = None if dweight_dtype is None else _TYPES.get(dweight_dtype, 3)
+    return _done(_binding.cross_entropy_rows_backward(dloss, x, weight, targets, lse,
+                                                      ignore_index, need_dx, need_dweight, out,
+                                                      dweight, code, workspace,
+                                                      _event_handle(start_event),
+                                                      _event_handle(stop_event)),
+                 "cross_entropy_rows_backward", CrossEntropyGrads)

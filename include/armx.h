@@ -638,6 +638,75 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
                              size_t ldr, float* dweight, float* dbias, void* ws,
                              size_t ws_bytes, const armx_config* cfg, void* stream);
 
+/*
+ * cross_entropy_rows -- the softmax cross entropy of rows against a vocabulary: with
+ * z[r][v] = sum over c of x[r][c] * weight[v][c],
+ *   lse[r]  = log of the sum over v of exp(z[r][v])
+ *   loss[r] = lse[r] - z[r][targets[r]], or 0 where targets[r] == ignore_index
+ * all in binary32 (products of 16-bit values are exact, the sums are those of the matrix
+ * units).  No z is stored: a tile of them at a time is made and summed up.  A row's loss
+ * does not depend on how many rows there are (batch invariance).
+ *
+ * x        device, rows x cols, ARMX_F16 or ARMX_BF16 (hidden states).
+ * weight   device, vocab x cols of the same type (the output layer's).
+ * targets  device, rows int64, 8-byte aligned.  One that is neither ignore_index nor
+ *          from 0 to vocab - 1 gives NaN, for its row's loss only.
+ * loss, lse  device, rows binary32 each.  lse is written for ignored rows too; what
+ *          their x holds reaches nothing else.
+ * ws       device workspace, 256-byte aligned, of armx_cross_entropy_workspace_bytes
+ *          bytes (8 for every row and 64 vocabulary rows, and 4 a row); it needs no
+ *          zeros and none are left.
+ * vocab and cols are at least 1 (ARMX_ERR_SHAPE), cols at most 2^21, rows 2^21, vocab
+ * 2^30, pitches 2^22, and ceil(rows / 256) * ceil(vocab / 256) at most 2097151.
+ * Rows that all start at multiples of 128 bytes are read fastest.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
+ */
+int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw,
+                       const int64_t* targets, int type, size_t rows, size_t vocab, size_t cols,
+                       int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                       const armx_config* cfg, void* stream);
+
+/*
+ * cross_entropy_rows_backward -- gradients of cross_entropy_rows: with
+ *   dz[r][v] = dloss[r] * (exp(z[r][v] - lse[r]) - (v == targets[r])), 0 for all of an
+ *              ignored row,
+ *   dx[r][c]      = sum over v of dz[r][v] * weight[v][c], rounded once to `type`
+ *   dweight[v][c] = sum over r of dz[r][v] * x[r][c], rounded once to `dweight_type`.
+ * A piece of the vocabulary at a time its z is made again and its dz kept as 16-bit
+ * values in the workspace, scaled by rows so that neither binary16's range nor a row's
+ * largest value costs accuracy; sums are in binary32.
+ *
+ * dloss    device, rows binary32 (the mean over rows: 1 / rows each, say, times a loss
+ *          scale where 16-bit gradients need one).  What it holds for ignored rows
+ *          reaches nothing, nor does their x.
+ * lse      device, rows binary32, as cross_entropy_rows wrote them.
+ * dx       device, rows x cols of `type`, or NULL (not wanted).
+ * dweight  device, vocab x cols, or NULL; rows 16-byte aligned in pitches of a
+ *          multiple of 8; zeros when rows == 0.
+ * dweight_type  `type`, or ARMX_F32.
+ * A target that is neither ignore_index nor from 0 to vocab - 1, or a dloss that is not
+ * finite, gives NaN for its row of dx and for all of dweight.
+ * ws       as above, of armx_cross_entropy_backward_workspace_bytes bytes; NULL when
+ *          that is 0.
+ * Sizes as for cross_entropy_rows, and ceil(rows / 256) * ceil(cols / 256) at most
+ * 2097151.  A row of dx, and of dweight, may depend in its last bit on the row count and
+ * the device's compute-unit count; nothing depends on timing.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}; dx and dweight
+ * both NULL is ARMX_ERR_NULL.
+ */
+int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
+                                const void* weight, size_t ldw, const int64_t* targets,
+                                const float* lse, int type, size_t rows, size_t vocab,
+                                size_t cols, int64_t ignore_index, void* dx, size_t lddx,
+                                void* dweight, size_t lddw, int dweight_type, void* ws,
+                                size_t ws_bytes, const armx_config* cfg, void* stream);
+
+/* Workspace bytes of the two; (size_t)-1 for sizes that they refuse.  `dx`, `dweight`:
+ * whether each is wanted (not NULL).  Without a device 256 compute units are assumed. */
+size_t armx_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols);
+size_t armx_cross_entropy_backward_workspace_bytes(size_t rows, size_t vocab, size_t cols,
+                                                   int dx, int dweight);
+
 /* Operation codes for armx_workspace_bytes. */
 #define ARMX_OP_SUM 0
 #define ARMX_OP_ROWS 1
