@@ -90,32 +90,57 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, cons
   }
   if (lane_id() == 0) {
     rows[row] = s;
-    atomicMax(top, __builtin_bit_cast(uint32_t, s.dloss) & 0x7FFFFFFFu);
+    // most rows find one at least as large there (4096 rows 58 -> XX us)
+    const uint32_t size = __builtin_bit_cast(uint32_t, s.dloss) & 0x7FFFFFFFu;
+    if (size > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+      atomicMax(top, size);
   }
 }
 
-// to[c][r] = from[r][c], r < rows, c < cols, in 64 x 64 tiles; `copies` of them side by
-// side, and zeros for rows that are ignored (targets may be null).
+// to[c][r] = from[r][c], r < rows, c < cols, in 64 x 64 tiles: 16 bytes a thread on both
+// sides, turned in LDS; zeros for rows that are ignored (targets may be null) and up to
+// the next multiple of 8.  Two copies stand side by side, without zeros behind them.
+template <int COPIES>
 __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* from, uint64_t ld,
                                                         uint64_t rows, uint64_t cols,
                                                         uint16_t* to, uint64_t ldt,
-                                                        const int64_t* targets, int64_t ignore,
-                                                        uint64_t copies) {
-  __shared__ uint16_t tile[64][66];
+                                                        const int64_t* targets, int64_t ignore) {
+  __shared__ uint32_t tile[64][33];
   const uint64_t r0 = uint64_t(blockIdx.x) * 64, c0 = uint64_t(blockIdx.y) * 64;
-  const uint32_t j = threadIdx.x % 64, i0 = threadIdx.x / 64;
-#pragma unroll 4
-  for (uint32_t i = i0; i < 64; i += 4) {
-    const uint64_t r = r0 + i, c = c0 + j;
-    const bool in = r < rows && c < cols && !(targets && targets[r] == ignore);
-    tile[i][j] = in ? from[r * ld + c] : uint16_t(0);
+  const uint32_t chunk = threadIdx.x % 8, line = threadIdx.x / 8;
+  u32x4 v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t r = r0 + line + 32 * i;
+    const bool in = r < rows && !(targets && targets[r] == ignore);
+    v[i] = in ? load8_masked(from + r * ld, c0 + chunk * 8, cols, 0) : u32x4{0, 0, 0, 0};
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) tile[line + 32 * i][chunk * 4 + e] = v[i][e];
   __syncthreads();
-#pragma unroll 4
-  for (uint32_t i = i0; i < 64; i += 4) {
-    const uint64_t c = c0 + i, r = r0 + j;
-    if (r >= rows || c >= cols) continue;
-    for (uint64_t q = 0; q < copies; ++q) to[c * ldt + q * rows + r] = tile[j][i];
+  // (a row of LDS has 33 words, so the 8 rows and 8 pairs of columns of 64 lanes fall on
+  // banks of their own)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t j = line + 32 * i, r = chunk * 8;
+    const uint64_t c = c0 + j;
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = tile[r + e][j / 2] >> (16 * (j % 2)) & 0xFFFFu;
+    if (c >= cols || r0 + r >= rows) continue;
+    if constexpr (COPIES == 1) {
+      *reinterpret_cast<u32x4*>(to + c * ldt + r0 + r) =
+          u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (r0 + r + e < rows) {
+          to[c * ldt + r0 + r + e] = uint16_t(h[e]);
+          to[c * ldt + rows + r0 + r + e] = uint16_t(h[e]);
+        }
+    }
   }
 }
 
@@ -131,22 +156,42 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   unsigned ti, tj;
   tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  const float all = top_scale(*top);
   floatx4 z[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
   const uint64_t row0 = i0 + lane_row<T>(), col = j0 + lane_col<T>();
-  const float all = top_scale(*top);
-  float each[T::kMT];
+  // the rows' values in flight together, before the first store (which the compiler
+  // keeps later loads behind)
+  RowScale row_scale[T::kMT];
+  float row_lse[T::kMT];
+  int64_t row_at[T::kMT];
 #pragma unroll
   for (int i = 0; i < T::kMT; ++i) {
     const uint64_t row = row0 + i < x.rows ? row0 + i : x.rows - 1;
-    const RowScale s = rows[row];
-    const float l = lse[row];
-    const int64_t at = targets[row] - first - int64_t(col);
-    each[i] = s.dloss * all;
+    row_scale[i] = rows[row];
+    row_lse[i] = lse[row] * kLog2E;
+    row_at[i] = targets[row] - first - int64_t(col);
+  }
+  float each[T::kMT];
 #pragma unroll
-    for (int c = 0; c < T::kCols; ++c) {
-      const float v = exp_of(z[i][c / 4][c % 4] - l) - (at == c ? 1.0f : 0.0f);
-      z[i][c / 4][c % 4] = s.skip ? 0.0f : v;
+  for (int i = 0; i < T::kMT; ++i) {
+    const RowScale s = row_scale[i];
+    const float l = row_lse[i];
+    each[i] = s.dloss * all;
+    // (the product's rounding, 2^-24 of lse, is far below the 16 bits to come)
+#pragma unroll
+    for (int c = 0; c < T::kCols; ++c)
+      z[i][c / 4][c % 4] =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][c / 4][c % 4], kLog2E, -l));
+    // few wavefronts have a row's target among their columns, or an ignored row
+    const int64_t at = row_at[i];
+    if (at >= 0 && at < T::kCols) {
+#pragma unroll
+      for (int c = 0; c < T::kCols; ++c) z[i][c / 4][c % 4] -= at == c ? 1.0f : 0.0f;
+    }
+    if (s.skip) {
+#pragma unroll
+      for (int c = 0; c < T::kCols; ++c) z[i][c / 4][c % 4] = 0.0f;
     }
     if (dz && row0 + i < x.rows) {
 #pragma unroll
@@ -156,7 +201,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
         for (int e = 0; e < 4; ++e)
           v[e] = narrow2<TYPE>(z[i][c / 4 + e / 2][2 * (e % 2)] * s.scale,
                                z[i][c / 4 + e / 2][2 * (e % 2) + 1] * s.scale);
-        *reinterpret_cast<u32x4*>(dz + row * ldz + col + c) = v;
+        *reinterpret_cast<u32x4*>(dz + (row0 + i) * ldz + col + c) = v;
       }
     }
   }
@@ -215,14 +260,31 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
   wt.p += k0;
   floatx4 acc[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(dz, wt, part, i0, j0, lds, acc);
+  const uint64_t row0 = i0 + lane_row<T>();
+  auto at = [&](int i) ARMX_INLINE {
+    const uint64_t row = row0 + i < dz.rows ? row0 + i : dz.rows - 1;
+    return reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + lane_col<T>());
+  };
+  constexpr int kTogether = T::kMT < 4 ? T::kMT : 4;
 #pragma unroll
-  for (int i = 0; i < T::kMT; ++i) {
-    const uint64_t row = i0 + lane_row<T>() + i;
-    if (row >= dz.rows) continue;
-    floatx4* o =
-        reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + lane_col<T>());
+  for (int i0 = 0; i0 < T::kMT; i0 += kTogether) {
+    if (more) {
+      floatx4 old[kTogether][T::kNT];
 #pragma unroll
-    for (int y = 0; y < T::kNT; ++y) o[y] = more ? o[y] + acc[i][y] : acc[i][y];
+      for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+        for (int y = 0; y < T::kNT; ++y) old[i][y] = at(i0 + i)[y];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+        for (int y = 0; y < T::kNT; ++y) acc[i0 + i][y] += old[i][y];
+    }
+#pragma unroll
+    for (int i = i0; i < i0 + kTogether; ++i) {
+      if (row0 + i >= dz.rows) continue;
+#pragma unroll
+      for (int y = 0; y < T::kNT; ++y) at(i)[y] = acc[i][y];
+    }
   }
 }
 
@@ -263,9 +325,9 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dweight_kernel(
   unsigned ti, tj;
   tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
+  const float back = 1.0f / top_scale(*top);
   floatx4 acc[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(dzt, xt, k, i0, j0, lds, acc);
-  const float back = 1.0f / top_scale(*top);
   const uint64_t col = j0 + lane_col<T>();
 #pragma unroll
   for (int i = 0; i < T::kMT; ++i) {
@@ -347,8 +409,9 @@ __global__ void clear_kernel(uint32_t* v) { *v = 0; }
 hipError_t transpose(Steps& steps, const uint16_t* from, uint64_t ld, uint64_t rows, uint64_t cols,
                      uint16_t* to, uint64_t ldt, const int64_t* targets, int64_t ignore,
                      uint64_t copies) {
-  void* args[] = {&from, &ld, &rows, &cols, &to, &ldt, &targets, &ignore, &copies};
-  return steps.run(reinterpret_cast<const void*>(&transpose_kernel),
+  void* args[] = {&from, &ld, &rows, &cols, &to, &ldt, &targets, &ignore};
+  return steps.run(copies == 1 ? reinterpret_cast<const void*>(&transpose_kernel<1>)
+                               : reinterpret_cast<const void*>(&transpose_kernel<2>),
                    dim3(unsigned(ceil_div(rows, 64)), unsigned(ceil_div(cols, 64))), 256, args);
 }
 
@@ -465,9 +528,11 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   if (p.piece > round_up(vocab, kRoom)) p.piece = round_up(vocab, kRoom);
   // no larger than what the pieces share evenly
   p.piece = round_up(ceil_div(vocab, ceil_div(vocab, p.piece)), kRoom);
-  p.ldz = p.piece;
+  // A line more than whole tiles: rows that lie a power of two apart are in few of the
+  // caches' channels (4096 x 4096 x 32768 917 us, with a line more 767).
+  p.ldz = p.piece + kStepValues;
   p.terms = rows <= kTwoTerms ? 2 : 1;
-  p.ldt = p.terms == 2 ? round_up(2 * rows, 8) : round_up(rows, kRoom);
+  p.ldt = (p.terms == 2 ? round_up(2 * rows, kStepValues) : round_up(rows, kRoom)) + kStepValues;
   p.ldd = round_up(cols, kRoom);
   // products for dx of few tiles: parts of the piece in blocks of their own
   const uint64_t tiles = ceil_div(rows, 128) * ceil_div(cols, 128);

@@ -62,6 +62,14 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel
           for (int i = 0; i < T::kMT; ++i) z[i][y][e] = kMinusInf;
         }
   }
+  // the rows' targets in flight together, before the first store (which the compiler
+  // keeps later loads behind)
+  int64_t target[T::kMT];
+#pragma unroll
+  for (int i = 0; i < T::kMT; ++i) {
+    const uint64_t row = i0 + lane_row<T>() + i;
+    target[i] = targets[row < x.rows ? row : x.rows - 1];
+  }
 #pragma unroll
   for (int i = 0; i < T::kMT; ++i) {
     const uint64_t row = i0 + lane_row<T>() + i;
@@ -82,8 +90,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel
     const float sum = add_xor32(add_xor16((s[0] + s[1]) + (s[2] + s[3])));
     if (row < x.rows) {
       if (lane_id() < 16) parts[piece * x.rows + row] = Part{m, sum};
-      const int64_t at = targets[row] - int64_t(col);
-      if (at >= 0 && at < T::kCols && targets[row] < int64_t(w.rows)) {
+      const int64_t at = target[i] - int64_t(col);
+      if (at >= 0 && at < T::kCols && target[i] < int64_t(w.rows)) {
         float hit = 0.0f;
 #pragma unroll
         for (int c = 0; c < T::kCols; ++c) hit = at == c ? z[i][c / 4][c % 4] : hit;

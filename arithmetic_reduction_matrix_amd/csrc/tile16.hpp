@@ -13,8 +13,13 @@
 // consecutive columns, whole pieces of either order of the product.
 //
 // Steps of 64 values of k (128 bytes, a line) go from memory straight to LDS
-// (buffer_load ... lds) into one of NS buffers, NS - 1 steps ahead of the one that is
-// multiplied.  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
+// (buffer_load ... lds) into rings of buffers, NS steps ahead of the one that is
+// multiplied.  The half of a step (32 values) that is multiplied next is read from LDS
+// under the products of the one before, so a step's buffers are free again in its middle;
+// there one operand's loads of the step NS on are sent, and the other's, whose ring has
+// one buffer more, already under the first half: loads are spread over the whole step.
+// (256 x 256, both operands' loads in the second half of a step: 4096 x 32768 x 4096 806
+// us, 4096 x 4096 x 32768 763; spread 779 and 744.)  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
 // tile keeps its piece c in slot c ^ swizzle(r), so that the 16 lanes of a 16-byte LDS
 // read, whose rows are 128 bytes apart, meet no bank twice.  The load writes LDS in
 // lane order, so the swizzle is made on the memory side: the lane that fills slot s of
@@ -86,18 +91,22 @@ using No = Int<0>;
 
 constexpr int kStepBytes = 128, kStepValues = 64;
 
-// A block makes BM x BN of the product with WM x WN wavefronts and NS buffers.
-template <int BM, int BN, int WM, int WN, int NS>
+// A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of an operand
+// have a buffer, and of one of the two (b with MORE_B) one step more, so that its loads
+// need not wait for the middle of a step.
+template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true>
 struct Tile16 {
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
+  static constexpr bool kMoreB = MORE_B;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
   static constexpr int kNT = BN / WN / 16;
   static constexpr int kRows = kMT, kCols = 4 * kNT;   // a lane's part of the product
   static constexpr int kLoadsA = BM / 8 / kWaves;  // wavefront loads per step
   static constexpr int kLoadsB = BN / 8 / kWaves;
-  static constexpr int kStage = (BM + BN) * kStepBytes;
-  static constexpr int kLdsBytes = NS * kStage;
+  static constexpr int kStageA = BM * kStepBytes, kStageB = BN * kStepBytes;
+  static constexpr int kNA = NS + (MORE_B ? 0 : 1), kNB = NS + (MORE_B ? 1 : 0);
+  static constexpr int kLdsBytes = kNA * kStageA + kNB * kStageB;
   // wavefronts per SIMD that the LDS leaves room for, at most 2 (of 256 registers)
   static constexpr int kResident = 160 * 1024 / kLdsBytes * kWaves / 4;
   static constexpr int kPerSimd = kResident < 1 ? 1 : kResident < 2 ? kResident : 2;
@@ -157,10 +166,14 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
                                               floatx4 (&acc)[T::kMT][T::kNT]) {
   constexpr int kMT = T::kMT, kNT = T::kNT, NS = T::kNS;
   const int lane = lane_id(), w = wave_id();
-  const uint32_t ring = uint32_t(reinterpret_cast<uintptr_t>((tile_lds_byte*)lds));
-  uint32_t base = ring;
-  auto next = [&](uint32_t at) ARMX_INLINE {
-    return at == ring + (NS - 1) * T::kStage ? ring : at + T::kStage;
+  const uint32_t ring_a = uint32_t(reinterpret_cast<uintptr_t>((tile_lds_byte*)lds));
+  const uint32_t ring_b = ring_a + T::kNA * T::kStageA;
+  uint32_t base_a = ring_a, base_b = ring_b;
+  auto next_a = [&](uint32_t at) ARMX_INLINE {
+    return at == ring_a + (T::kNA - 1) * T::kStageA ? ring_a : at + T::kStageA;
+  };
+  auto next_b = [&](uint32_t at) ARMX_INLINE {
+    return at == ring_b + (T::kNB - 1) * T::kStageB ? ring_b : at + T::kStageB;
   };
   const __amdgpu_buffer_rsrc_t a = tile_rows(ma, k, i0), b = tile_rows(mb, k, j0);
   // rows past the matrix are read from its last row
@@ -185,23 +198,37 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     off_b[x] = (row < last_b ? row : last_b) * uint32_t(mb.ld * 2) +
                ((uint32_t(lane) & 7) ^ swizzle(r)) * 16;
   }
-  // wavefront load x of the step at byte k0, into the buffer at `to`
-  auto stage_one = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
-    if (x < T::kLoadsA) {
-      lds_load16(a, to + (w * T::kLoadsA + x) * 1024, off_a[x] + k0);
-    } else {
-      x -= T::kLoadsA;
-      lds_load16(b, to + T::kBM * kStepBytes + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
-    }
+  // wavefront load x of an operand's step at byte k0, into the buffer at `to`
+  auto send_a = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    lds_load16(a, to + (w * T::kLoadsA + x) * 1024, off_a[x] + k0);
+  };
+  auto send_b = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    lds_load16(b, to + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
   };
   constexpr int kLoads = T::kLoadsA + T::kLoadsB;
-  auto stage = [&](uint32_t to, uint32_t k0) ARMX_INLINE {
-#pragma unroll
-    for (int x = 0; x < kLoads; ++x) stage_one(to, k0, x);
+  constexpr int kFirst = T::kMoreB ? T::kLoadsB : T::kLoadsA, kSecond = kLoads - kFirst;
+  auto send_first = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    if constexpr (T::kMoreB)
+      send_b(to, k0, x);
+    else
+      send_a(to, k0, x);
   };
-  // all but the block's last `steps` steps of loads have landed and all its reads are done
-  auto sync = [&](auto steps) ARMX_INLINE {
-    wait_loads<decltype(steps)::value * kLoads>();
+  auto send_second = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
+    if constexpr (T::kMoreB)
+      send_a(to, k0, x);
+    else
+      send_b(to, k0, x);
+  };
+  auto stage = [&](uint32_t t) ARMX_INLINE {
+#pragma unroll
+    for (int x = 0; x < T::kLoadsA; ++x) send_a(ring_a + t * T::kStageA, t * kStepBytes, x);
+#pragma unroll
+    for (int x = 0; x < T::kLoadsB; ++x) send_b(ring_b + t * T::kStageB, t * kStepBytes, x);
+  };
+  // all but the wavefront's last `loads` loads have landed and all the block's reads are
+  // done
+  auto sync = [&](auto loads) ARMX_INLINE {
+    wait_loads<decltype(loads)::value>();
     if constexpr (T::kWaves > 1)
       __syncthreads();
     else
@@ -215,7 +242,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
   for (int h = 0; h < 2; ++h) {
     const uint32_t in = r * kStepBytes + ((4 * h + g) ^ swizzle(r)) * 16;
     at_a[h] = (w % T::kWM) * (kMT * 16 * kStepBytes) + in;
-    at_b[h] = (T::kBM + (w / T::kWM) * (kNT * 16)) * kStepBytes + in;
+    at_b[h] = (w / T::kWM) * (kNT * 16 * kStepBytes) + in;
   }
   u32x4 fa[2][kMT], fb[2][kNT];
   constexpr int kReads = kMT + kNT;
@@ -224,8 +251,8 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
   struct Place {
     uint32_t a, b;
   };
-  auto place = [&](uint32_t from, int h) ARMX_INLINE {
-    Place at = {from + at_a[h], from + at_b[h]};
+  auto place = [&](uint32_t from_a, uint32_t from_b, int h) ARMX_INLINE {
+    Place at = {from_a + at_a[h], from_b + at_b[h]};
     asm("" : "+v"(at.a));
     asm("" : "+v"(at.b));
     return at;
@@ -237,8 +264,8 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     else
       fa[h][j - kNT] = lds_read16(at.a + (j - kNT) * 16 * kStepBytes);
   };
-  auto fetch_half = [&](uint32_t from, int h) ARMX_INLINE {
-    const Place at = place(from, h);
+  auto fetch_half = [&](int h) ARMX_INLINE {
+    const Place at = place(base_a, base_b, h);
 #pragma unroll
     for (int j = 0; j < kReads; ++j) {
       fetch(at, h, j);
@@ -265,20 +292,15 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
 #pragma unroll
     for (int x = 0; x < kMT; ++x) multiply_row(h, x);
   };
-  // The products of one half, with the other's operands (h) read from `from` and, with
-  // SEND, the loads of the step at byte k0 into `to` spread between them.
-  auto multiply_and_fetch = [&](int h, uint32_t from, auto send, uint32_t to, uint32_t k0)
-      ARMX_INLINE {
-    constexpr int kPer = (kLoads + kMT - 1) / kMT;
+  // The products of one half, with the other's operands (h) read from `at` and COUNT
+  // loads sent between them.
+  auto multiply_and_fetch = [&](int h, Place at, auto count, auto send) ARMX_INLINE {
+    constexpr int kCount = decltype(count)::value;
     constexpr int kPerR = (kReads + kMT - 1) / kMT;
-    const Place at = place(from, h);
 #pragma unroll
     for (int i = 0; i < kMT; ++i) {
-      if constexpr (send.value) {
 #pragma unroll
-        for (int j = i * kPer; j < (i + 1) * kPer; ++j)
-          if (j < kLoads) stage_one(to, k0, j);
-      }
+      for (int j = kCount * i / kMT; j < kCount * (i + 1) / kMT; ++j) send(j);
 #pragma unroll
       for (int j = i * kPerR; j < (i + 1) * kPerR; ++j)
         if (j < kReads) fetch(at, h, j);
@@ -288,41 +310,50 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     }
   };
   // A step but the last (its first half's operands already in registers): the second
-  // half's are read while the first is multiplied; then, after the barrier that ends
-  // all reading of this buffer and finds the next one filled (`out`: steps sent for
-  // behind that one), the step NS on is sent for into it (SEND) and the next step's
-  // first half read under the second half's products.
+  // half's are read while the first is multiplied, and with SEND the step NS on is sent
+  // for into the spare buffer of the ring that has one; then, after the barrier that ends
+  // all reading of this step's buffers and finds the next one's filled (all but `out`
+  // loads), into this one's of the other ring, while the next step's first half is read
+  // under the second half's products.
+  uint32_t spare = T::kMoreB ? ring_b + (T::kNB - 1) * T::kStageB
+                             : ring_a + (T::kNA - 1) * T::kStageA;
   auto step = [&](auto send, auto out, uint32_t s) ARMX_INLINE {
-    multiply_and_fetch(1, base, No{}, 0, 0);
+    constexpr bool kSend = decltype(send)::value;
+    const uint32_t k0 = (s + NS) * kStepBytes;
+    multiply_and_fetch(1, place(base_a, base_b, 1), Int<kSend ? kFirst : 0>{},
+                       [&](int x) ARMX_INLINE { send_first(spare, k0, x); });
     sync(out);
-    const uint32_t other = next(base);
-    multiply_and_fetch(0, other, send, base, (s + NS) * kStepBytes);
-    base = other;
+    const uint32_t old_a = base_a, old_b = base_b;
+    base_a = next_a(base_a);
+    base_b = next_b(base_b);
+    spare = T::kMoreB ? old_b : old_a;
+    multiply_and_fetch(0, place(base_a, base_b, 0), Int<kSend ? kSecond : 0>{},
+                       [&](int x) ARMX_INLINE { send_second(T::kMoreB ? old_a : old_b, k0, x); });
   };
   if (k == 0) return;
   const uint32_t steps = (k + kStepValues - 1) / kStepValues;
   uint32_t s = 0;
   if (steps >= NS) {
 #pragma unroll
-    for (int t = 0; t < NS; ++t) stage(ring + t * T::kStage, t * kStepBytes);
-    sync(Int<NS - 1>{});
+    for (int t = 0; t < NS; ++t) stage(t);
+    sync(Int<(NS - 1) * kLoads>{});
   } else {
-    for (uint32_t t = 0; t < steps; ++t) stage(ring + t * T::kStage, t * kStepBytes);
+    for (uint32_t t = 0; t < steps; ++t) stage(t);
     sync(No{});
   }
-  fetch_half(base, 0);
-  for (; steps - s > NS; ++s) step(Yes{}, Int<NS - 2>{}, s);
+  fetch_half(0);
+  for (; steps - s > NS; ++s) step(Yes{}, Int<(NS - 2) * kLoads + kFirst>{}, s);
   // the last steps; what is still out shrinks with them
   if constexpr (NS > 3)
-    if (steps - s > 3) step(No{}, Int<NS - 2>{}, s), ++s;
+    if (steps - s > 3) step(No{}, Int<2 * kLoads>{}, s), ++s;
   if constexpr (NS > 2)
-    if (steps - s > 2) step(No{}, Int<1>{}, s), ++s;
+    if (steps - s > 2) step(No{}, Int<kLoads>{}, s), ++s;
   if (steps - s > 1) step(No{}, No{}, s), ++s;
   // (one half after the other: the registers do not hold both beside the masks)
   const bool cut = k % kStepValues != 0;
   if (cut) mask_half(s * kStepValues, 0);
   multiply(0);
-  fetch_half(base, 1);
+  fetch_half(1);
   if (cut) mask_half(s * kStepValues, 1);
   multiply(1);
 }

@@ -9,11 +9,11 @@ namespace armx {
 namespace {
 
 typedef Tile16<256, 256, 2, 4, 2> Tile0;
-typedef Tile16<128, 256, 2, 4, 3> Tile1;
-typedef Tile16<128, 128, 2, 2, 4> Tile2;
-typedef Tile16<64, 128, 2, 2, 3> Tile3;
-typedef Tile16<32, 128, 1, 2, 4> Tile4;
-typedef Tile16<16, 128, 1, 2, 4> Tile5;
+typedef Tile16<128, 256, 2, 4, 3, false> Tile1;
+typedef Tile16<128, 128, 2, 2, 2> Tile2;
+typedef Tile16<64, 128, 2, 2, 2> Tile3;
+typedef Tile16<32, 128, 1, 2, 3> Tile4;
+typedef Tile16<16, 128, 1, 2, 3> Tile5;
 constexpr int kTile16s = 6;
 
 // Calls CASE(T) for tile number `index`.
