@@ -378,6 +378,11 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(void* to, uint64_t row_b
 
 // ---- launches -----------------------------------------------------------------------------
 
+// The largest tile of dx, whose products are long: wavefronts of 64 x 128 in place of 128 x
+// 64 (4096 x 4096 x 32768 715 -> 691 us; 32768 x 4096 x 4096, whose results they store in
+// shorter pieces, 764 -> 782).
+typedef Tile16<256, 256, 4, 2, 2, true, true> LongTile;
+
 // Rows of dweight's products (its k) up to which a value of dz is kept in two terms.
 constexpr uint64_t kTwoTerms = 128;
 // dz of a piece: at most this many values, but at least kLeastPiece vocabulary rows.
@@ -481,7 +486,12 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                      \
   e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T, TYPE>),       \
                 dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args)
-      ARMX_OF_TILE(choose_tile16(a.rows * plan.splits, a.cols, per, cu_count), ARMX_TILE_CASE);
+      const int tile = choose_tile16(a.rows * plan.splits, a.cols, per, cu_count);
+      if (tile == 0) {
+        ARMX_TILE_CASE(LongTile);
+      } else {
+        ARMX_OF_TILE(tile, ARMX_TILE_CASE);
+      }
 #undef ARMX_TILE_CASE
       if (e != hipSuccess) return e;
     }

@@ -19,7 +19,8 @@
 // there one operand's loads of the step NS on are sent, and the other's, whose ring has
 // one buffer more, already under the first half: loads are spread over the whole step.
 // (256 x 256, both operands' loads in the second half of a step: 4096 x 32768 x 4096 806
-// us, 4096 x 4096 x 32768 763; spread 779 and 744.)  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
+// us, 4096 x 4096 x 32768 763; spread 779 and 744; and with the two wavefronts of a SIMD
+// taking turns, TURNS, 763 and 715.)  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
 // tile keeps its piece c in slot c ^ swizzle(r), so that the 16 lanes of a 16-byte LDS
 // read, whose rows are 128 bytes apart, meet no bank twice.  The load writes LDS in
 // lane order, so the swizzle is made on the memory side: the lane that fills slot s of
@@ -94,10 +95,10 @@ constexpr int kStepBytes = 128, kStepValues = 64;
 // A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of an operand
 // have a buffer, and of one of the two (b with MORE_B) one step more, so that its loads
 // need not wait for the middle of a step.
-template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true>
+template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true, bool TURNS = false>
 struct Tile16 {
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
-  static constexpr bool kMoreB = MORE_B;
+  static constexpr bool kMoreB = MORE_B, kTurns = TURNS;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
   static constexpr int kNT = BN / WN / 16;
@@ -114,6 +115,7 @@ struct Tile16 {
   static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
   static_assert(NS >= 2 && NS <= 4, "the last steps are written out");
   static_assert(kMT <= 16 && kNT <= 16, "operand tiles");
+  static_assert(!TURNS || (kWaves == 8 && NS == 2 && MORE_B), "two wavefronts a SIMD, in turns");
 };
 
 typedef __attribute__((address_space(3))) int8_t tile_lds_byte;
@@ -244,6 +246,110 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     at_a[h] = (w % T::kWM) * (kMT * 16 * kStepBytes) + in;
     at_b[h] = (w / T::kWM) * (kNT * 16 * kStepBytes) + in;
   }
+#pragma unroll
+  for (int x = 0; x < kMT; ++x)
+#pragma unroll
+    for (int y = 0; y < kNT; ++y) acc[x][y] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (k == 0) return;
+  const uint32_t steps = (k + kStepValues - 1) / kStepValues;
+  const bool cut = k % kStepValues != 0;
+  if constexpr (T::kTurns) {
+    // The two wavefronts of a SIMD take turns: between two barriers one reads its
+    // operands of half a step and sends loads, while the other multiplies, which it does
+    // at a higher priority; the second group of four is a barrier behind the first.
+    //
+    // Reads of a step's buffers by both groups end a barrier after the first one's second
+    // half, so from the next step on they may be filled again: a's loads of step u + 1 are
+    // sent in the first half of step u (two buffers), b's of step u + 2 in its second
+    // (three).  Every wavefront waits for its own loads before the barrier behind which
+    // the first group reads step u + 1: all but b's of step u + 2.
+    u32x4 fa[kMT], fb[kNT];
+    const bool second = w >= T::kWaves / 2;
+    auto barrier = [&]() ARMX_INLINE {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto read = [&](int h) ARMX_INLINE {
+      // (opaque to the compiler, so that it keeps two addresses and puts the rest into the
+      // reads' offsets)
+      uint32_t from_a = base_a + at_a[h], from_b = base_b + at_b[h];
+      asm("" : "+v"(from_a));
+      asm("" : "+v"(from_b));
+#pragma unroll
+      for (int y = 0; y < kNT; ++y) fb[y] = lds_read16(from_b + y * 16 * kStepBytes);
+#pragma unroll
+      for (int x = 0; x < kMT; ++x) fa[x] = lds_read16(from_a + x * 16 * kStepBytes);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // the reads are done, and values past k cut from both operands (what stands there may
+    // be a NaN)
+    auto have = [&](uint32_t u, int h) ARMX_INLINE {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (cut && u + 1 == steps) {
+        const int keep = int(k) - int(u * kStepValues + 32 * h + 8 * g);
+#pragma unroll
+        for (int x = 0; x < kMT; ++x) fa[x] = keep_values(fa[x], keep);
+#pragma unroll
+        for (int y = 0; y < kNT; ++y) fb[y] = keep_values(fb[y], keep);
+      }
+    };
+    auto multiply = [&]() ARMX_INLINE {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int x = 0; x < kMT; ++x)
+#pragma unroll
+        for (int y = 0; y < kNT; ++y) acc[x][y] = mfma16<TYPE>(fb[y], fa[x], acc[x][y]);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    auto landed = [&](uint32_t u) ARMX_INLINE {
+      if (u + 2 < steps)
+        wait_loads<T::kLoadsB>();
+      else
+        wait_loads<0>();
+    };
+#pragma unroll
+    for (int x = 0; x < T::kLoadsA; ++x) send_a(ring_a, 0, x);
+#pragma unroll
+    for (int x = 0; x < T::kLoadsB; ++x) send_b(ring_b, 0, x);
+    if (steps > 1) {
+#pragma unroll
+      for (int x = 0; x < T::kLoadsB; ++x) send_b(ring_b + T::kStageB, kStepBytes, x);
+      wait_loads<T::kLoadsB>();
+    } else {
+      wait_loads<0>();
+    }
+    barrier();
+    if (second) barrier();
+    for (uint32_t u = 0; u < steps; ++u) {
+      read(0);
+      if (u + 1 < steps) {
+        const uint32_t to = next_a(base_a);
+#pragma unroll
+        for (int x = 0; x < T::kLoadsA; ++x) send_a(to, (u + 1) * kStepBytes, x);
+      }
+      have(u, 0);
+      barrier();
+      multiply();
+      barrier();
+      read(1);
+      if (u + 2 < steps) {
+        const uint32_t to = next_b(next_b(base_b));
+#pragma unroll
+        for (int x = 0; x < T::kLoadsB; ++x) send_b(to, (u + 2) * kStepBytes, x);
+      }
+      have(u, 1);
+      if (second) landed(u);
+      barrier();
+      multiply();
+      if (!second) landed(u);
+      barrier();
+      base_a = next_a(base_a);
+      base_b = next_b(base_b);
+    }
+    if (!second) barrier();
+    return;
+  }
   u32x4 fa[2][kMT], fb[2][kNT];
   constexpr int kReads = kMT + kNT;
   // Where this lane reads half h of the buffer at `from`; opaque to the compiler, so
@@ -280,10 +386,6 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
 #pragma unroll
     for (int y = 0; y < kNT; ++y) fb[h][y] = keep_values(fb[h][y], keep);
   };
-#pragma unroll
-  for (int x = 0; x < kMT; ++x)
-#pragma unroll
-    for (int y = 0; y < kNT; ++y) acc[x][y] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply_row = [&](int h, int x) ARMX_INLINE {
 #pragma unroll
     for (int y = 0; y < kNT; ++y) acc[x][y] = mfma16<TYPE>(fb[h][y], fa[h][x], acc[x][y]);
@@ -330,8 +432,6 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     multiply_and_fetch(0, place(base_a, base_b, 0), Int<kSend ? kSecond : 0>{},
                        [&](int x) ARMX_INLINE { send_second(T::kMoreB ? old_a : old_b, k0, x); });
   };
-  if (k == 0) return;
-  const uint32_t steps = (k + kStepValues - 1) / kStepValues;
   uint32_t s = 0;
   if (steps >= NS) {
 #pragma unroll
@@ -350,7 +450,6 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     if (steps - s > 2) step(No{}, Int<kLoads>{}, s), ++s;
   if (steps - s > 1) step(No{}, No{}, s), ++s;
   // (one half after the other: the registers do not hold both beside the masks)
-  const bool cut = k % kStepValues != 0;
   if (cut) mask_half(s * kStepValues, 0);
   multiply(0);
   fetch_half(1);

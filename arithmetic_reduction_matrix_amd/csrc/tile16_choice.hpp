@@ -8,7 +8,7 @@
 namespace armx {
 namespace {
 
-typedef Tile16<256, 256, 2, 4, 2> Tile0;
+typedef Tile16<256, 256, 2, 4, 2, true, true> Tile0;
 typedef Tile16<128, 256, 2, 4, 3, false> Tile1;
 typedef Tile16<128, 128, 2, 2, 2> Tile2;
 typedef Tile16<64, 128, 2, 2, 2> Tile3;
