@@ -123,7 +123,7 @@ int check_dropout(const armx_dropout* d, uint64_t rows, armx::DropoutArgs* out) 
 
 // Sizes of the cross entropy: 32-bit offsets in a tile's rows, and grids.
 constexpr uint64_t kMaxLossRows = uint64_t(1) << 21, kMaxLossCols = uint64_t(1) << 21;
-constexpr uint64_t kMaxLossVocab = uint64_t(1) << 30, kMaxLossLd = uint64_t(1) << 22;
+constexpr uint64_t kMaxLossVocab = uint64_t(1) << 28, kMaxLossLd = uint64_t(1) << 22;
 
 int check_loss_sizes(uint64_t rows, uint64_t vocab, uint64_t cols, bool backward) {
   if (rows > kMaxLossRows || vocab > kMaxLossVocab || cols > kMaxLossCols) return ARMX_ERR_SHAPE;

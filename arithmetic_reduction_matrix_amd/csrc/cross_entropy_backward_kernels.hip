@@ -83,7 +83,8 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, cons
       // rounding does not turn over)
       const float rest = __builtin_fmaxf(1.0f - exp_of(z - lse[row]), 0x1p-14f);
       s.scale = kRowScale / rest;
-      s.back = s.dloss * (rest / kRowScale);
+      // (an infinite dloss makes infinities of both signs in dz, whose sums are NaNs)
+      s.back = s.dloss - s.dloss == 0.0f ? s.dloss * (rest / kRowScale) : __builtin_nanf("");
     } else {
       s.scale = s.dloss = s.back = __builtin_nanf("");
     }

@@ -657,7 +657,7 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
  *          bytes (8 for every row and 64 vocabulary rows, and 4 a row); it needs no
  *          zeros and none are left.
  * vocab and cols are at least 1 (ARMX_ERR_SHAPE), cols at most 2^21, rows 2^21, vocab
- * 2^30, pitches 2^22, and ceil(rows / 256) * ceil(vocab / 256) at most 2097151.
+ * 2^28, pitches 2^22, and ceil(rows / 256) * ceil(vocab / 256) at most 2097151.
  * Rows that all start at multiples of 128 bytes are read fastest.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
  */
