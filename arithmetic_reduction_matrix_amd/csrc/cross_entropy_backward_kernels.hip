@@ -34,6 +34,8 @@ constexpr float kRowScale = 0x1p14f, kTopScale = 0x1p15f;
 
 __device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2E); }
 
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3), aligned(4)));
+
 // What a row of dz is made with: by rows (exp(z - lse) - onehot) * scale, by columns
 // (exp(z - lse) - onehot) * dloss * that of the largest |dloss|; the row of dx is what
 // comes out times `back`.  A row that is ignored has zeros, and one whose target is not
@@ -221,6 +223,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
                                    z[i + 1][c / 4][c % 4] * each[i + 1]);
         if constexpr (T::kMT == 2) *reinterpret_cast<uint32_t*>(to) = v[0];
         if constexpr (T::kMT == 4) *reinterpret_cast<u32x2*>(to) = u32x2{v[0], v[1]};
+        if constexpr (T::kMT == 6) *reinterpret_cast<u32x3*>(to) = u32x3{v[0], v[1], v[2]};
         if constexpr (T::kMT == 8)
           *reinterpret_cast<u32x4*>(to) = u32x4{v[0], v[1], v[2], v[3]};
       }
@@ -266,7 +269,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
     const uint64_t row = row0 + i < dz.rows ? row0 + i : dz.rows - 1;
     return reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + lane_col<T>());
   };
-  constexpr int kTogether = T::kMT < 4 ? T::kMT : 4;
+  constexpr int kTogether = T::kMT % 4 == 0 ? 4 : T::kMT % 2 == 0 ? 2 : 1;
 #pragma unroll
   for (int i0 = 0; i0 < T::kMT; i0 += kTogether) {
     if (more) {
@@ -389,7 +392,7 @@ constexpr uint64_t kTwoTerms = 128;
 // dz of a piece: at most this many values, but at least kLeastPiece vocabulary rows.
 constexpr uint64_t kPieceValues = uint64_t(1) << 27;
 constexpr uint64_t kLeastPiece = 1024;
-constexpr uint64_t kRoom = 256;   // rows and columns of the largest tile
+constexpr uint64_t kRoom = kLargestTile;
 
 uint64_t round_up(uint64_t v, uint64_t to) { return ceil_div(v, to) * to; }
 
@@ -543,7 +546,8 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   // caches' channels (4096 x 4096 x 32768 917 us, with a line more 767).
   p.ldz = p.piece + kStepValues;
   p.terms = rows <= kTwoTerms ? 2 : 1;
-  p.ldt = (p.terms == 2 ? round_up(2 * rows, kStepValues) : round_up(rows, kRoom)) + kStepValues;
+  // with one term a tile's rows past the last are written too
+  p.ldt = round_up(p.terms == 2 ? 2 * rows : rows + kRoom - 1, kStepValues) + kStepValues;
   p.ldd = round_up(cols, kRoom);
   // products for dx of few tiles: parts of the piece in blocks of their own
   const uint64_t tiles = ceil_div(rows, 128) * ceil_div(cols, 128);

@@ -160,26 +160,43 @@ Tile16Size tile16_size(int index) {
   return s;
 }
 
-// The tile whose estimated time is least: a compute unit makes its tiles one after the
-// other (`resident` at a time), each taking `fixed` and `each` for a step of 64 values
-// of k (us).
+// The tile whose estimated time is least.  A compute unit that makes q tiles runs them in
+// rounds of at most `resident` blocks; a round takes `fixed` (its first loads, its
+// results) and, per step of 64 values of k, `alone` or, with several blocks on the unit,
+// `each` of them if that is more.  The constants (us) are fitted to times of each tile on
+// MI355X over 137 products of 1 to 4096 rows, 256 to 131072 columns and lengths of 64 to
+// 32064 with 16-bit results; over those the tile that they choose is 2.4% behind the
+// fastest of fourteen on average, and 53% at worst (515 x 1000 x 8192, which no caller
+// makes in one part).  Each pays where it is chosen (us, it and the best of the others):
+// 256 x 256 at 4096 x 131072 x 128 386 (424); 192 x 256 at 777 x 50001 x 2056 227 (232);
+// 256 x 128 at 515 x 32003 x 1000 63 (64); 128 x 128 at 32003 x 4096 x 128 77 (86);
+// 64 x 128 at 1 x 50001 x 8192 143 (149); 32 x 128 at 200 x 4096 x 16384 96 (117);
+// 16 x 128 at 8 x 32768 x 1024 13.2 (13.4); 16 x 64 at 515 x 1000 x 8192 32 (42).
 int choose_tile16(uint64_t m, uint64_t n, uint64_t k, int cu_count) {
   struct Time {
     int resident;
-    float fixed, each;
+    float fixed, alone, each;
   };
-  constexpr Time times[kTile16s] = {{1, 3.0f, 1.50f}, {1, 3.0f, 0.86f}, {1, 2.6f, 0.52f},
-                                    {2, 2.2f, 0.33f}, {2, 2.0f, 0.22f}, {2, 2.0f, 0.16f}};
+  constexpr Time times[kTile16s] = {
+      {1, 6.10f, 1.21f, 1.21f}, {1, 3.90f, 1.08f, 1.08f}, {1, 3.29f, 0.73f, 0.73f},
+      {2, 2.32f, 0.52f, 0.55f}, {2, 1.78f, 0.11f, 0.41f}, {2, 1.38f, 0.34f, 0.37f},
+      {2, 1.19f, 0.25f, 0.29f}, {3, 1.04f, 0.20f, 0.16f}};
   int best = -1;
   double least = 0;
   for (int i = 0; i < kTile16s; ++i) {
     const Tile16Size s = tile16_size(i);
     const uint64_t tiles = ceil_div(m, uint64_t(s.bm)) * ceil_div(n, uint64_t(s.bn));
     if (tiles > 0x7FFFFFFFu / 1024) continue;  // the grid's limit
-    const double per_cu = double(ceil_div(tiles, uint64_t(cu_count)));
-    const double t = double(ceil_div(uint64_t(per_cu), uint64_t(times[i].resident))) *
-                         times[i].fixed +
-                     per_cu * double(ceil_div(k, uint64_t(kStepValues))) * times[i].each;
+    const uint64_t per_cu = ceil_div(tiles, uint64_t(cu_count));
+    const double steps = double(ceil_div(k, uint64_t(kStepValues)));
+    auto round = [&](uint64_t blocks) {
+      const double together = double(blocks) * times[i].each;
+      return blocks == 0 ? 0.0
+                         : times[i].fixed +
+                               steps * (together > times[i].alone ? together : times[i].alone);
+    };
+    const double t = double(per_cu / times[i].resident) * round(times[i].resident) +
+                     round(per_cu % times[i].resident);
     if (best < 0 || t < least) best = i, least = t;
   }
   return best;

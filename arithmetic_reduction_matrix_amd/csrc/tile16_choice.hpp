@@ -9,12 +9,15 @@ namespace armx {
 namespace {
 
 typedef Tile16<256, 256, 2, 4, 2, true, true> Tile0;
-typedef Tile16<128, 256, 2, 4, 3, false> Tile1;
-typedef Tile16<128, 128, 2, 2, 2> Tile2;
-typedef Tile16<64, 128, 2, 2, 2> Tile3;
-typedef Tile16<32, 128, 1, 2, 3> Tile4;
-typedef Tile16<16, 128, 1, 2, 3> Tile5;
-constexpr int kTile16s = 6;
+typedef Tile16<192, 256, 2, 4, 2> Tile1;
+typedef Tile16<256, 128, 4, 2, 3> Tile2;
+typedef Tile16<128, 128, 2, 2, 2> Tile3;
+typedef Tile16<64, 128, 2, 2, 2> Tile4;
+typedef Tile16<32, 128, 1, 2, 3> Tile5;
+typedef Tile16<16, 128, 1, 2, 3> Tile6;
+typedef Tile16<16, 64, 1, 1, 4> Tile7;
+constexpr int kTile16s = 8;
+constexpr uint64_t kLargestTile = 256;   // rows and columns
 
 // Calls CASE(T) for tile number `index`.
 #define ARMX_OF_TILE(index, CASE) \
@@ -26,6 +29,8 @@ constexpr int kTile16s = 6;
       case 3: CASE(Tile3); break; \
       case 4: CASE(Tile4); break; \
       case 5: CASE(Tile5); break; \
+      case 6: CASE(Tile6); break; \
+      case 7: CASE(Tile7); break; \
     }                             \
   } while (0)
 
