@@ -53,7 +53,7 @@ __device__ __forceinline__ float top_scale(uint32_t top_bits) {
 }
 
 // A row's scales, a wavefront each; the largest |dloss| (bits, NaNs largest) in *top,
-// which is 0 before.
+// which is 0 before (null: not wanted).
 template <int TYPE>
 __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, const float* dloss,
                                                         const float* lse, RowScale* rows,
@@ -93,9 +93,9 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, cons
   }
   if (lane_id() == 0) {
     rows[row] = s;
-    // most rows find one at least as large there (4096 rows 58 -> XX us)
+    // most rows find one at least as large there (4096 rows 58 -> 35 us)
     const uint32_t size = __builtin_bit_cast(uint32_t, s.dloss) & 0x7FFFFFFFu;
-    if (size > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+    if (top && size > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
       atomicMax(top, size);
   }
 }
@@ -103,12 +103,15 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, cons
 // to[c][r] = from[r][c], r < rows, c < cols, in 64 x 64 tiles: 16 bytes a thread on both
 // sides, turned in LDS; zeros for rows that are ignored (targets may be null) and up to
 // the next multiple of 8.  Two copies stand side by side, without zeros behind them.
+// `clear`: set to 0 on the way, for the kernel behind (may be null).
 template <int COPIES>
 __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* from, uint64_t ld,
                                                         uint64_t rows, uint64_t cols,
                                                         uint16_t* to, uint64_t ldt,
-                                                        const int64_t* targets, int64_t ignore) {
+                                                        const int64_t* targets, int64_t ignore,
+                                                        uint32_t* clear) {
   __shared__ uint32_t tile[64][33];
+  if (clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear = 0;
   const uint64_t r0 = uint64_t(blockIdx.x) * 64, c0 = uint64_t(blockIdx.y) * 64;
   const uint32_t chunk = threadIdx.x % 8, line = threadIdx.x / 8;
   u32x4 v[2];
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   unsigned ti, tj;
   tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
-  const float all = top_scale(*top);
+  const float all = top ? top_scale(*top) : 0.0f;
   floatx4 z[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
   const uint64_t row0 = i0 + lane_row<T>(), col = j0 + lane_col<T>();
@@ -413,12 +416,10 @@ class Steps {
   bool first_ = true;
 };
 
-__global__ void clear_kernel(uint32_t* v) { *v = 0; }
-
 hipError_t transpose(Steps& steps, const uint16_t* from, uint64_t ld, uint64_t rows, uint64_t cols,
                      uint16_t* to, uint64_t ldt, const int64_t* targets, int64_t ignore,
-                     uint64_t copies) {
-  void* args[] = {&from, &ld, &rows, &cols, &to, &ldt, &targets, &ignore};
+                     uint64_t copies, uint32_t* clear) {
+  void* args[] = {&from, &ld, &rows, &cols, &to, &ldt, &targets, &ignore, &clear};
   return steps.run(copies == 1 ? reinterpret_cast<const void*>(&transpose_kernel<1>)
                                : reinterpret_cast<const void*>(&transpose_kernel<2>),
                    dim3(unsigned(ceil_div(rows, 64)), unsigned(ceil_div(cols, 64))), 256, args);
@@ -440,19 +441,17 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   CrossEntropyArgs copy = a;
   const float *dloss = grads.dloss, *lse = grads.lse;
   hipError_t e;
-  {
-    void* args[] = {&top};
-    e = steps.run(reinterpret_cast<const void*>(&clear_kernel), dim3(1), 1, args);
+  if (dzt) {
+    e = transpose(steps, a.x, a.ldx, a.rows, a.cols, xt, plan.ldt, a.targets, a.ignore, plan.terms,
+                  top);
     if (e != hipSuccess) return e;
+  } else {
+    top = nullptr;   // dweight's
   }
   {
     void* args[] = {&copy, &dloss, &lse, &rows, &top};
     e = steps.run(reinterpret_cast<const void*>(&loss_rows_kernel<TYPE>),
                   dim3(unsigned(ceil_div(a.rows, 4))), 256, args);
-    if (e != hipSuccess) return e;
-  }
-  if (dzt) {
-    e = transpose(steps, a.x, a.ldx, a.rows, a.cols, xt, plan.ldt, a.targets, a.ignore, plan.terms);
     if (e != hipSuccess) return e;
   }
   uint32_t cols = uint32_t(a.cols);
@@ -478,7 +477,8 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
       if (e != hipSuccess) return e;
     }
     if (dz) {
-      e = transpose(steps, a.weight + v0 * a.ldw, a.ldw, count, a.cols, wt, plan.ldz, nullptr, 0, 1);
+      e = transpose(steps, a.weight + v0 * a.ldw, a.ldw, count, a.cols, wt, plan.ldz, nullptr, 0, 1,
+                    nullptr);
       if (e != hipSuccess) return e;
       Matrix16 mz{dz, a.rows, plan.ldz}, mw{wt, a.cols, plan.ldz};
       uint32_t k = uint32_t(count);

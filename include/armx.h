@@ -654,7 +654,8 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
  * loss, lse  device, rows binary32 each.  lse is written for ignored rows too; what
  *          their x holds reaches nothing else.
  * ws       device workspace, 256-byte aligned, of armx_cross_entropy_workspace_bytes
- *          bytes (8 for every row and 64 vocabulary rows, and 4 a row); it needs no
+ *          bytes (8 for every row, their count rounded up to 8, and 64 vocabulary
+ *          rows, and 4 a row); it needs no
  *          zeros and none are left.
  * vocab and cols are at least 1 (ARMX_ERR_SHAPE), cols at most 2^21, rows 2^21, vocab
  * 2^28, pitches 2^22, and ceil(rows / 256) * ceil(vocab / 256) at most 2097151.

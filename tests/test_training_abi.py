@@ -133,7 +133,7 @@ def test_cross_entropy_refusals():
         assert loss(**kw) == -2, kw
     assert loss(type=2) == -3 and all(loss(c=cfg(**b)) == -3 for b in BAD_CONFIGS)
     need = lib.armx_cross_entropy_workspace_bytes(4, 100, 64)
-    assert need == 2 * 4 * 8 + 4 * 4 and loss(ws_bytes=need - 1) == -4
+    assert need == 2 * 8 * 8 + 4 * 4 and loss(ws_bytes=need - 1) == -4
     for kw in (*BAD_LOSS_SIZES, dict(ldx=56), dict(ldw=56), dict(ldx=(1 << 22) + 8),
                dict(ldw=(1 << 22) + 8)):
         assert loss(**kw) == -5, kw
