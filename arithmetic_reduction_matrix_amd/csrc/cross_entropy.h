@@ -38,7 +38,7 @@ struct CrossEntropyGradPlan {
   uint64_t splits = 0;    // parts of a piece whose products for dx stand apart
   uint64_t ldd = 0;       // floats between rows of those products
   // byte offsets in the workspace
-  size_t top = 0, rows = 0, dz = 0, dzt = 0, xt = 0, wt = 0, dx = 0;
+  size_t top = 0, rows = 0, dz = 0, dzt = 0, xt = 0, dx = 0;
   size_t ws_bytes = 0;
 };
 

@@ -249,12 +249,13 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   }
 }
 
-// The part of dx that a piece of the vocabulary makes: dz (rows x k) times wt (cols x k),
-// k in `splits` parts of `per` whose products stand apart; added to what is there after
-// the first piece.  `to` has whole tiles of room for columns.
+// The part of dx that a piece of the vocabulary makes: dz (rows x k) times the piece's rows
+// of w (k x cols), k in `splits` parts of `per` whose products stand apart; added to what
+// is there after the first piece.  `to` has whole tiles of room for columns.
 template <class T, int TYPE>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
-    Matrix16 dz, Matrix16 wt, uint32_t k, uint32_t per, float* to, uint64_t ldd, bool more,
+    Matrix16 dz, Matrix16 w, uint64_t cols, uint32_t k, uint32_t per, float* to, uint64_t ldd,
+    bool more,
     unsigned tiles_m, unsigned tiles_n) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   const unsigned id = unsigned(xcd_block_id()), split = id / (tiles_m * tiles_n);
@@ -264,9 +265,11 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
   const uint32_t k0 = split * per;
   const uint32_t part = k0 >= k ? 0 : k - k0 < per ? k - k0 : per;
   dz.p += k0;
-  wt.p += k0;
+  w.p += uint64_t(k0) * w.ld;
+  w.rows = part;
   floatx4 acc[T::kMT][T::kNT];
-  multiply_tile<T, TYPE>(dz, wt, part, i0, j0, lds, acc);
+  multiply_tile<T, TYPE>(dz, w, part, i0, j0, lds, acc, cols);
+  const uint32_t q = lane_id() >> 4;
   const uint64_t row0 = i0 + lane_row<T>();
   auto at = [&](int i) ARMX_INLINE {
     const uint64_t row = row0 + i < dz.rows ? row0 + i : dz.rows - 1;
@@ -280,7 +283,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
 #pragma unroll
       for (int i = 0; i < kTogether; ++i)
 #pragma unroll
-        for (int y = 0; y < T::kNT; ++y) old[i][y] = at(i0 + i)[y];
+        for (int y = 0; y < T::kNT; ++y) old[i][y] = at(i0 + i)[across_quad(y, q)];
 #pragma unroll
       for (int i = 0; i < kTogether; ++i)
 #pragma unroll
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
     for (int i = i0; i < i0 + kTogether; ++i) {
       if (row0 + i >= dz.rows) continue;
 #pragma unroll
-      for (int y = 0; y < T::kNT; ++y) at(i)[y] = acc[i][y];
+      for (int y = 0; y < T::kNT; ++y) at(i)[across_quad(y, q)] = acc[i][y];
     }
   }
 }
@@ -385,11 +388,6 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(void* to, uint64_t row_b
 
 // ---- launches -----------------------------------------------------------------------------
 
-// The largest tile of dx, whose products are long: wavefronts of 64 x 128 in place of 128 x
-// 64 (4096 x 4096 x 32768 715 -> 691 us; 32768 x 4096 x 4096, whose results they store in
-// shorter pieces, 764 -> 782).
-typedef Tile16<256, 256, 4, 2, 2, true, true> LongTile;
-
 // Rows of dweight's products (its k) up to which a value of dz is kept in two terms.
 constexpr uint64_t kTwoTerms = 128;
 // dz of a piece: at most this many values, but at least kLeastPiece vocabulary rows.
@@ -436,7 +434,6 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   uint16_t* dz = grads.dx ? reinterpret_cast<uint16_t*>(base + plan.dz) : nullptr;
   uint16_t* dzt = grads.dweight ? reinterpret_cast<uint16_t*>(base + plan.dzt) : nullptr;
   uint16_t* xt = reinterpret_cast<uint16_t*>(base + plan.xt);
-  uint16_t* wt = reinterpret_cast<uint16_t*>(base + plan.wt);
   float* sums = reinterpret_cast<float*>(base + plan.dx);
   CrossEntropyArgs copy = a;
   const float *dloss = grads.dloss, *lse = grads.lse;
@@ -477,25 +474,18 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
       if (e != hipSuccess) return e;
     }
     if (dz) {
-      e = transpose(steps, a.weight + v0 * a.ldw, a.ldw, count, a.cols, wt, plan.ldz, nullptr, 0, 1,
-                    nullptr);
-      if (e != hipSuccess) return e;
-      Matrix16 mz{dz, a.rows, plan.ldz}, mw{wt, a.cols, plan.ldz};
+      Matrix16 mz{dz, a.rows, plan.ldz}, mw{a.weight + v0 * a.ldw, count, a.ldw};
       uint32_t k = uint32_t(count);
+      uint64_t across = a.cols;
       uint32_t per = uint32_t(round_up(ceil_div(count, plan.splits), kStepValues));
       bool more = v0 != 0;
-      void* args[] = {&mz, &mw, &k, &per, &sums, &ldd, &more, &tiles_m, &tiles_n};
+      void* args[] = {&mz, &mw, &across, &k, &per, &sums, &ldd, &more, &tiles_m, &tiles_n};
 #define ARMX_TILE_CASE(T)                                                      \
   tiles_m = unsigned(ceil_div(a.rows, uint64_t(T::kBM)));                      \
   tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                      \
-  e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T, TYPE>),       \
+  e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T::Across, TYPE>), \
                 dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args)
-      const int tile = choose_tile16(a.rows * plan.splits, a.cols, per, cu_count);
-      if (tile == 0) {
-        ARMX_TILE_CASE(LongTile);
-      } else {
-        ARMX_OF_TILE(tile, ARMX_TILE_CASE);
-      }
+      ARMX_OF_TILE(choose_tile16(a.rows * plan.splits, a.cols, per, cu_count), ARMX_TILE_CASE);
 #undef ARMX_TILE_CASE
       if (e != hipSuccess) return e;
     }
@@ -564,7 +554,6 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   take(p.rows, rows * sizeof(RowScale));
   if (dx) {
     take(p.dz, rows * p.ldz * 2);
-    take(p.wt, cols * p.ldz * 2);
     take(p.dx, p.splits * rows * p.ldd * 4);
   }
   if (dweight) {

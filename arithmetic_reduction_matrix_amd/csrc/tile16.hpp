@@ -95,10 +95,13 @@ constexpr int kStepBytes = 128, kStepValues = 64;
 // A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of an operand
 // have a buffer, and of one of the two (b with MORE_B) one step more, so that its loads
 // need not wait for the middle of a step.
-template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true, bool TURNS = false>
+// ACROSS: b's rows lie across the sum, so that its transpose is multiplied.
+template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true, bool TURNS = false,
+          bool ACROSS = false>
 struct Tile16 {
+  typedef Tile16<BM, BN, WM, WN, NS, MORE_B, TURNS, true> Across;
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
-  static constexpr bool kMoreB = MORE_B, kTurns = TURNS;
+  static constexpr bool kMoreB = MORE_B, kTurns = TURNS, kAcross = ACROSS;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
   static constexpr int kNT = BN / WN / 16;
@@ -114,11 +117,14 @@ struct Tile16 {
   static_assert(kLoadsA * 8 * kWaves == BM && kLoadsB * 8 * kWaves == BN, "whole loads");
   static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
   static_assert(NS >= 2 && NS <= 4, "the last steps are written out");
+  static constexpr int kRowB = 2 * BN;   // bytes of a row of b's step that lies across
   static_assert(kMT <= 16 && kNT <= 16, "operand tiles");
+  static_assert(!ACROSS || (kNT == 4 && (BN == 256 || BN == 128 || BN == 64)), "swizzles");
   static_assert(!TURNS || (kWaves == 8 && NS == 2 && MORE_B), "two wavefronts a SIMD, in turns");
 };
 
 typedef __attribute__((address_space(3))) int8_t tile_lds_byte;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes per lane from `rows` into LDS at `lds` + 16 lane.  Written as asm so that
 // the compiler, which cannot tell the buffers apart, does not wait for these loads
@@ -138,6 +144,28 @@ __device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rows, uint32_t
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
   return *reinterpret_cast<const u32x4 __attribute__((address_space(3)))*>(at);
 }
+
+// 16 lanes, each with the address of 4 values: lane 4 j + c of the 16 those of row j of
+// column quad c, say; lane 4 c + e receives column e of quad c, rows 0 to 3.
+__device__ __forceinline__ uint64_t lds_read_across(uint32_t at) {
+  return __builtin_bit_cast(
+      uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    reinterpret_cast<s16x4 __attribute__((address_space(3)))*>(at)));
+}
+
+// Rows of b that lie across: 64 of a step, BN values each, pieces of 16 bytes.  A row keeps
+// its piece p in slot p ^ across_swizzle(row).  A read of 4 values a lane serves 32 lanes at
+// a time: 4 quads c of 8 rows, 0 to 3 and 8 to 11 (or 16 and 8 on), of which those of even
+// c lie in one half of their pieces and those of odd c in the other (across_quad); c's high
+// bit is bit 2 of the slot, and the rows' three bits go into the others.
+template <class T>
+__device__ __forceinline__ uint32_t across_swizzle(uint32_t row) {
+  const uint32_t third = (row >> 3) & 1;
+  if constexpr (T::kBN == 64) return ((row >> 1) & 1) | third << 1;   // two rows in 256 bytes
+  return (row & 3) | third << 3;
+}
+// Which 4 of a lane's 16 columns operand tile y holds, in lane group q.
+__device__ __forceinline__ uint32_t across_quad(uint32_t y, uint32_t q) { return y ^ (q & 1); }
 
 // vmcnt(N): all but this wavefront's last N loads into LDS have landed
 template <int N>
@@ -160,27 +188,46 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned 
 }
 
 // acc = the tile at (i0, j0) of a b^T over k values, rows and columns past the
-// matrices' undefined.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
+// matrices' undefined.  ACROSS: of a b over the rows of b, of which there are at least k
+// or that end where zeros are to be read, and whose columns are `across`; a lane's columns
+// are in the order of across_quad.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
 // barrier.  Every thread of the block takes part.
 template <class T, int TYPE>
 __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16& mb, uint32_t k,
                                               uint64_t i0, uint64_t j0, int8_t* lds,
-                                              floatx4 (&acc)[T::kMT][T::kNT]) {
+                                              floatx4 (&acc)[T::kMT][T::kNT],
+                                              uint64_t across = 0) {
   constexpr int kMT = T::kMT, kNT = T::kNT, NS = T::kNS;
   const int lane = lane_id(), w = wave_id();
   const uint32_t ring_a = uint32_t(reinterpret_cast<uintptr_t>((tile_lds_byte*)lds));
   const uint32_t ring_b = ring_a + T::kNA * T::kStageA;
   uint32_t base_a = ring_a, base_b = ring_b;
-  auto next_a = [&](uint32_t at) ARMX_INLINE {
+  auto after_a = [&](uint32_t at) ARMX_INLINE {
     return at == ring_a + (T::kNA - 1) * T::kStageA ? ring_a : at + T::kStageA;
   };
-  auto next_b = [&](uint32_t at) ARMX_INLINE {
+  auto after_b = [&](uint32_t at) ARMX_INLINE {
     return at == ring_b + (T::kNB - 1) * T::kStageB ? ring_b : at + T::kStageB;
   };
-  const __amdgpu_buffer_rsrc_t a = tile_rows(ma, k, i0), b = tile_rows(mb, k, j0);
+  const __amdgpu_buffer_rsrc_t a = tile_rows(ma, k, i0);
+  const __amdgpu_buffer_rsrc_t b = T::kAcross ? a : tile_rows(mb, k, j0);
+  // across: the next step's rows of b, whose steps are sent in order, and the bytes from
+  // there on
+  const uint16_t* next_b = mb.p + j0;
+  const uint64_t step_b = uint64_t(kStepValues) * mb.ld * 2;
+  uint64_t left_b =
+      T::kAcross && mb.rows ? (mb.rows - 1) * mb.ld * 2 + (across - j0 + 1) / 2 * 4 : 0;
+  __amdgpu_buffer_rsrc_t rows_b = b;
+  auto take_b = [&]() ARMX_INLINE {
+    rows_b = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(next_b), 0,
+        int(uint32_t(left_b < 0xFFFFFFF0u ? left_b : 0xFFFFFFF0u)), kTileBuffer);
+    next_b += step_b / 2;
+    left_b = left_b > step_b ? left_b - step_b : 0;
+  };
   // rows past the matrix are read from its last row
   const uint32_t last_a = uint32_t(ma.rows - 1 - i0 < T::kBM ? ma.rows - 1 - i0 : T::kBM - 1);
-  const uint32_t last_b = uint32_t(mb.rows - 1 - j0 < T::kBN ? mb.rows - 1 - j0 : T::kBN - 1);
+  const uint32_t last_b =
+      T::kAcross ? 0u : uint32_t(mb.rows - 1 - j0 < T::kBN ? mb.rows - 1 - j0 : T::kBN - 1);
   // byte offsets of the pieces that this lane brings into its slots of LDS rows
   uint32_t off_a[T::kLoadsA], off_b[T::kLoadsB];
 #pragma unroll
@@ -193,6 +240,12 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
   }
 #pragma unroll
   for (int x = 0; x < T::kLoadsB; ++x) {
+    if constexpr (T::kAcross) {
+      const uint32_t byte = (w * T::kLoadsB + x) * 1024 + lane * 16, row = byte / T::kRowB;
+      off_b[x] = row * uint32_t(mb.ld * 2) +
+                 (byte % T::kRowB / 16 ^ across_swizzle<T>(row)) * 16;
+      continue;
+    }
     const uint32_t slot = (w * T::kLoadsB + x) * 8 + (lane >> 3);
     const uint32_t in = slot % (16 * kNT), r = in % 16;
     const uint32_t row =
@@ -205,7 +258,12 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     lds_load16(a, to + (w * T::kLoadsA + x) * 1024, off_a[x] + k0);
   };
   auto send_b = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
-    lds_load16(b, to + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
+    if constexpr (T::kAcross) {
+      if (x == 0) take_b();
+      lds_load16(rows_b, to + (w * T::kLoadsB + x) * 1024, off_b[x]);
+    } else {
+      lds_load16(b, to + (w * T::kLoadsB + x) * 1024, off_b[x] + k0);
+    }
   };
   constexpr int kLoads = T::kLoadsA + T::kLoadsB;
   constexpr int kFirst = T::kMoreB ? T::kLoadsB : T::kLoadsA, kSecond = kLoads - kFirst;
@@ -246,6 +304,25 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     at_a[h] = (w % T::kWM) * (kMT * 16 * kStepBytes) + in;
     at_b[h] = (w / T::kWM) * (kNT * 16 * kStepBytes) + in;
   }
+  // across: lane 4 j + c of its 16 reads row 8 g + j (and 4 on), column quad c of tile y
+  uint32_t at_across[kNT];
+  if constexpr (T::kAcross) {
+    const uint32_t j = r / 4, c = r % 4, row = 8 * g + j;
+#pragma unroll
+    for (int y = 0; y < kNT; ++y) {
+      const uint32_t byte = (w / T::kWM) * (kNT * 32) + c * (8 * kNT) + across_quad(y, c) * 8;
+      at_across[y] = row * T::kRowB + (byte / 16 ^ across_swizzle<T>(row)) * 16 + byte % 16;
+    }
+  }
+  auto read_b = [&](uint32_t from, int h, int y) ARMX_INLINE {
+    if constexpr (T::kAcross) {
+      const uint32_t at = from + at_across[y] + h * 32 * T::kRowB;
+      const uint64_t low = lds_read_across(at), high = lds_read_across(at + 4 * T::kRowB);
+      return u32x4{uint32_t(low), uint32_t(low >> 32), uint32_t(high), uint32_t(high >> 32)};
+    } else {
+      return lds_read16(from + y * 16 * kStepBytes);
+    }
+  };
 #pragma unroll
   for (int x = 0; x < kMT; ++x)
 #pragma unroll
@@ -273,17 +350,17 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     auto read = [&](int h) ARMX_INLINE {
       // (opaque to the compiler, so that it keeps two addresses and puts the rest into the
       // reads' offsets)
-      uint32_t from_a = base_a + at_a[h], from_b = base_b + at_b[h];
+      uint32_t from_a = base_a + at_a[h], from_b = base_b + (T::kAcross ? 0 : at_b[h]);
       asm("" : "+v"(from_a));
       asm("" : "+v"(from_b));
 #pragma unroll
-      for (int y = 0; y < kNT; ++y) fb[y] = lds_read16(from_b + y * 16 * kStepBytes);
+      for (int y = 0; y < kNT; ++y) fb[y] = read_b(from_b, h, y);
 #pragma unroll
       for (int x = 0; x < kMT; ++x) fa[x] = lds_read16(from_a + x * 16 * kStepBytes);
       __builtin_amdgcn_sched_barrier(0);
     };
     // the reads are done, and values past k cut from both operands (what stands there may
-    // be a NaN)
+    // be a NaN; across, b has zeros there)
     auto have = [&](uint32_t u, int h) ARMX_INLINE {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (cut && u + 1 == steps) {
@@ -291,7 +368,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
 #pragma unroll
         for (int x = 0; x < kMT; ++x) fa[x] = keep_values(fa[x], keep);
 #pragma unroll
-        for (int y = 0; y < kNT; ++y) fb[y] = keep_values(fb[y], keep);
+        for (int y = 0; y < kNT; ++y) fb[y] = T::kAcross ? fb[y] : keep_values(fb[y], keep);
       }
     };
     auto multiply = [&]() ARMX_INLINE {
@@ -324,7 +401,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     for (uint32_t u = 0; u < steps; ++u) {
       read(0);
       if (u + 1 < steps) {
-        const uint32_t to = next_a(base_a);
+        const uint32_t to = after_a(base_a);
 #pragma unroll
         for (int x = 0; x < T::kLoadsA; ++x) send_a(to, (u + 1) * kStepBytes, x);
       }
@@ -334,7 +411,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
       barrier();
       read(1);
       if (u + 2 < steps) {
-        const uint32_t to = next_b(next_b(base_b));
+        const uint32_t to = after_b(after_b(base_b));
 #pragma unroll
         for (int x = 0; x < T::kLoadsB; ++x) send_b(to, (u + 2) * kStepBytes, x);
       }
@@ -344,8 +421,8 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
       multiply();
       if (!second) landed(u);
       barrier();
-      base_a = next_a(base_a);
-      base_b = next_b(base_b);
+      base_a = after_a(base_a);
+      base_b = after_b(base_b);
     }
     if (!second) barrier();
     return;
@@ -358,7 +435,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     uint32_t a, b;
   };
   auto place = [&](uint32_t from_a, uint32_t from_b, int h) ARMX_INLINE {
-    Place at = {from_a + at_a[h], from_b + at_b[h]};
+    Place at = {from_a + at_a[h], from_b + (T::kAcross ? 0 : at_b[h])};
     asm("" : "+v"(at.a));
     asm("" : "+v"(at.b));
     return at;
@@ -366,7 +443,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
   // read j of half h, in the order in which its products need them
   auto fetch = [&](Place at, int h, int j) ARMX_INLINE {
     if (j < kNT)
-      fb[h][j] = lds_read16(at.b + j * 16 * kStepBytes);
+      fb[h][j] = read_b(at.b, h, j);
     else
       fa[h][j - kNT] = lds_read16(at.a + (j - kNT) * 16 * kStepBytes);
   };
@@ -384,7 +461,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
 #pragma unroll
     for (int x = 0; x < kMT; ++x) fa[h][x] = keep_values(fa[h][x], keep);
 #pragma unroll
-    for (int y = 0; y < kNT; ++y) fb[h][y] = keep_values(fb[h][y], keep);
+    for (int y = 0; y < kNT; ++y) fb[h][y] = T::kAcross ? fb[h][y] : keep_values(fb[h][y], keep);
   };
   auto multiply_row = [&](int h, int x) ARMX_INLINE {
 #pragma unroll
@@ -426,8 +503,8 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
                        [&](int x) ARMX_INLINE { send_first(spare, k0, x); });
     sync(out);
     const uint32_t old_a = base_a, old_b = base_b;
-    base_a = next_a(base_a);
-    base_b = next_b(base_b);
+    base_a = after_a(base_a);
+    base_b = after_b(base_b);
     spare = T::kMoreB ? old_b : old_a;
     multiply_and_fetch(0, place(base_a, base_b, 0), Int<kSend ? kSecond : 0>{},
                        [&](int x) ARMX_INLINE { send_second(T::kMoreB ? old_a : old_b, k0, x); });
