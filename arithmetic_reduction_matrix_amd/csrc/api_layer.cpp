@@ -347,6 +347,7 @@ int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
   a.rows = rows, a.cols = cols;
   a.ldx = ldx, a.ldr = ldr, a.ldo = ldo, a.lds = lds;
   a.eps = eps, a.type = type;
+  a.inv_cols = float(1.0 / double(cols));
   a.drop = dropout != nullptr;
   log_rows("layer_norm_rows", rows, cols, type);
   return hip_status(armx::launch_layer_norm(a, cfg, s));
@@ -397,6 +398,7 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
   a.partials = static_cast<float*>(ws);
   a.rows = rows, a.cols = cols;
   a.ldy = ldy, a.ldh = ldh, a.ldd = ldd, a.ldx = ldx, a.ldr = ldr;
+  a.inv_cols = float(1.0 / double(cols));
   a.type = type;
   a.drop = dropout != nullptr;
   log_rows("layer_norm_rows_backward", rows, cols, type);

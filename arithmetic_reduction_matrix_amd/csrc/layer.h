@@ -105,6 +105,7 @@ struct LayerNormArgs {
   uint64_t rows = 0, cols = 0;
   uint64_t ldx = 0, ldr = 0, ldo = 0, lds = 0;
   float eps = 0;
+  float inv_cols = 0;  // 1 / cols, rounded
   int type = ARMX_F16;
   bool drop = false;
   DropoutArgs dropout{};
@@ -124,6 +125,7 @@ struct LayerNormBackwardArgs {
   float* partials = nullptr;  // blocks x 2 x pitch, when the plan has a workspace
   uint64_t rows = 0, cols = 0;
   uint64_t ldy = 0, ldh = 0, ldd = 0, ldx = 0, ldr = 0;
+  float inv_cols = 0;
   int type = ARMX_F16;
   bool drop = false;
   DropoutArgs dropout{};

@@ -24,6 +24,19 @@
 namespace armx {
 namespace {
 
+// How a row lies on threads: as row_shape, but rows of more than `from` and up to 512
+// chunks with two chunks a thread, so that half as many wavefronts take and join their
+// parts (us, one / two: norm of 8192 x 4096 34 / 24, with residual and dropout 55 / 50,
+// 16384 x 2048 30 / 23 and 51 / 47, but 32768 x 1024 28 / 57 on one wavefront a block;
+// gradients of 9000 x 3728 with all 82 / 73, but 16384 x 2048 66 / 72).
+RowShape two_chunks(uint64_t cols, uint64_t from) {
+  const uint64_t n = (cols + kRowVec - 1) / kRowVec;
+  if (n > from && n <= 512) return {int((n + 127) / 128) * 64, 2};
+  return row_shape(cols);
+}
+RowShape norm_shape(uint64_t cols) { return two_chunks(cols, 128); }
+RowShape grad_shape(uint64_t cols) { return two_chunks(cols, 256); }
+
 // What reaches the norm.
 constexpr int kPlain = 0;     // x
 constexpr int kResidual = 1;  // x + residual
@@ -78,7 +91,8 @@ struct Moments {
   }
   template <int TYPE>
   __device__ __forceinline__ static void run(const u32x4 (&h)[L::kChunks], uint32_t cols,
-                                             Lds* lds, int turn, float& mean, float& m2) {
+                                             float inv_cols, Lds* lds, int turn, float& mean,
+                                             float& m2) {
     constexpr int C = L::kChunks;
     const int wave = L::kTpr ? 0 : wave_id();
     float s = 0.0f;
@@ -88,7 +102,8 @@ struct Moments {
       widen8<TYPE>(h[j], f);   // trimmed: zeros past the row
       s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
     }
-    const float n = part(cols, wave), each = 1.0f / n;
+    // (m is near the mean and no more, so the quick reciprocal does)
+    const float n = part(cols, wave), each = __builtin_amdgcn_rcpf(n);
     const float m = lane_tree(s, kLevels) * each;
     float q = 0.0f, e = 0.0f;
 #pragma unroll
@@ -96,11 +111,21 @@ struct Moments {
       float f[8];
       widen8<TYPE>(h[j], f);
       const int in = in_chunk(cols, j * L::threads() + L::lane());
+      if (cols % 8 == 0) {   // whole chunks: in one with no values all differences are 0
+        const float from = in > 0 ? m : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = i < in ? f[i] - m : 0.0f;
-        q = __builtin_fmaf(d, d, q);
-        e += d;
+        for (int i = 0; i < 8; ++i) {
+          const float d = f[i] - from;
+          q = __builtin_fmaf(d, d, q);
+          e += d;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float d = i < in ? f[i] - m : 0.0f;
+          q = __builtin_fmaf(d, d, q);
+          e += d;
+        }
       }
     }
     q = lane_tree(q, kLevels);
@@ -119,7 +144,7 @@ struct Moments {
       float off = 0.0f;
 #pragma unroll 4
       for (int w = 1; w < waves; ++w) off = __builtin_fmaf(part(cols, w), l.mean[w] - first, off);
-      mean = first + off / float(cols);
+      mean = first + off * inv_cols;
       m2 = 0.0f;
 #pragma unroll 4
       for (int w = 0; w < waves; ++w) {
@@ -130,10 +155,10 @@ struct Moments {
   }
 };
 
-__device__ __forceinline__ float inv_std_of(float m2, uint64_t cols, float eps) {
+__device__ __forceinline__ float inv_std_of(float m2, float inv_cols, float eps) {
   // (a part's deviations may come out a rounding below 0 where they are none)
-  const float v = m2 / float(cols);
-  return 1.0f / __builtin_sqrtf((v < 0.0f ? 0.0f : v) + eps);
+  const float v = m2 * inv_cols;
+  return __builtin_amdgcn_rsqf((v < 0.0f ? 0.0f : v) + eps);
 }
 
 template <int TYPE>
@@ -186,8 +211,12 @@ __global__ __launch_bounds__(L::kMax) void layer_norm_kernel(LayerNormArgs k) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   const Dropper drop(k.dropout);
   u32x4 w[C], b[C];
-  load_weight<L>(k.weight, cols, w);
-  load_weight<L>(k.bias, k.bias ? cols : 0, b);
+  // (the registers of 1024 threads do not hold them beside the row's sums)
+  constexpr bool kEarly = L::kMax < 1024;
+  if constexpr (kEarly) {
+    load_weight<L>(k.weight, cols, w);
+    load_weight<L>(k.bias, k.bias ? cols : 0, b);
+  }
   int turn = 0;
   // every thread of a block makes the same number of rounds (barriers)
   for (uint64_t base = uint64_t(blockIdx.x) * L::kRows; base < k.rows;
@@ -196,9 +225,13 @@ __global__ __launch_bounds__(L::kMax) void layer_norm_kernel(LayerNormArgs k) {
     u32x4 h[C];
     load_sums<TYPE, IN, STREAM, L>(k, drop, base, IN == kPlain ? nullptr : k.sum_out, k.lds, h);
     float mean, m2;
-    Moments<L>::template run<TYPE>(h, cols, lds, turn, mean, m2);
+    Moments<L>::template run<TYPE>(h, cols, k.inv_cols, lds, turn, mean, m2);
     if (row >= k.rows) continue;
-    const float inv = inv_std_of(m2, k.cols, k.eps);
+    const float inv = inv_std_of(m2, k.inv_cols, k.eps);
+    if constexpr (!kEarly) {
+      load_weight<L>(k.weight, cols, w);
+      load_weight<L>(k.bias, k.bias ? cols : 0, b);
+    }
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t c = j * L::threads() + L::lane();
@@ -277,14 +310,14 @@ __global__ __launch_bounds__(1024) void layer_norm_loop_kernel(LayerNormArgs k) 
       mean = __builtin_fmaf(d, float(in) / all, mean);
       n = all;
     }
-    const float first = block_sum(n * mean, part[0]) / float(cols);
+    const float first = block_sum(n * mean, part[0]) * k.inv_cols;
     const float d = mean - first;
     m2 = block_sum(__builtin_fmaf(n * d, d, m2), part[1]);
     // what the first mean's rounding left
     const float e = block_sum(n * d, part[2]);
-    mean = first + e / float(cols);
-    m2 -= e * (e / float(cols));
-    const float inv = inv_std_of(m2, k.cols, k.eps);
+    mean = first + e * k.inv_cols;
+    m2 -= e * (e * k.inv_cols);
+    const float inv = inv_std_of(m2, k.inv_cols, k.eps);
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
       // from sum_out (where this thread wrote it), so that outputs may stand where
       // inputs did
@@ -314,7 +347,8 @@ __global__ __launch_bounds__(1024) void dropout_loop_kernel(LayerNormArgs k) {
 template <int TYPE, int IN, bool NORM>
 hipError_t launch_typed(const LayerNormArgs& a, const armx_config* cfg, hipStream_t stream) {
   const RowShape s =
-      for_pitch(row_shape(a.cols), a.residual && a.ldr > a.ldx ? a.ldr : a.ldx);
+      for_pitch(NORM ? norm_shape(a.cols) : row_shape(a.cols),
+                a.residual && a.ldr > a.ldx ? a.ldr : a.ldx);
   const bool stream_out = a.rows * a.cols >= kStreamValues;
   const void* fn = nullptr;
 #define ARMX_ROWS_CASE(...)                                                                      \
@@ -443,8 +477,8 @@ __device__ __forceinline__ void store_grads(const LayerNormBackwardArgs& k, cons
                                             const u32x4 (&dy)[C], const u32x4 (&h)[C],
                                             const u32x4 (&ds)[C], const u32x4 (&w)[C]) {
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-  a /= float(k.cols);
-  b /= float(k.cols);
+  a *= k.inv_cols;
+  b *= k.inv_cols;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const uint32_t c = j * L::threads() + L::lane();
@@ -745,8 +779,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_loop_kernel(LayerNor
       }
     }
     PairCombine<L>::run(a, b, lds, turn);
-    a /= float(k.cols);
-    b /= float(k.cols);
+    a *= k.inv_cols;
+    b *= k.inv_cols;
     const RowWords dr(k.dsum ? k.dsum + row * k.ldd : nullptr, GRAD != kAlone && k.dsum ? cols : 0);
     for (uint32_t c0 = threadIdx.x; c0 < chunks; c0 += 4096) {
       u32x4 y[4], h[4], w[4], d[4];
@@ -897,6 +931,13 @@ hipError_t launch_grad(const LayerNormBackwardArgs& a, const NormBackwardPlan& p
 NormBackwardPlan plan_layer_norm_backward(uint64_t rows, uint64_t cols, int cu_count) {
   NormBackwardPlan p = plan_norm_backward(rows, cols, cu_count);
   p.ws_bytes *= 2;
+  const RowShape s = grad_shape(cols);
+  if (p.apart || s.threads == p.shape.threads) return p;
+  p.shape = s;
+  p.block = block_threads(s);
+  const uint64_t most = uint64_t(cu_count) * ((511 + p.block) / p.block);
+  p.blocks = rows < most ? rows : most;   // a row at a time
+  p.ws_bytes = size_t(2 * p.blocks * p.pitch * sizeof(float));
   return p;
 }
 

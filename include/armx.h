@@ -592,8 +592,9 @@ int dropout_rows(const void* x, size_t ldx, const void* residual, size_t ldr, in
  *              or NULL.
  * out and sum_out may each be x or residual themselves (same pointer and pitch), not
  * both the same one; nothing else may overlap.  A NaN or an infinity in a row's h makes
- * NaNs in that row, and so does a sum of squared deviations past binary32's range
- * where it is infinite less infinite (otherwise inv is 0).
+ * NaNs in that row, and so may a sum of squared deviations past binary32's range
+ * (magnitudes of 2^60 and more).  Squares below its normal range (deviations under
+ * 2^-63) lose bits or count as 0, which counts where eps is below 2^-100.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other than the
  * two, an eps that is negative or NaN, a p outside 0 .. 1, or an out that starts where
  * sum_out does is ARMX_ERR_CONFIG.
