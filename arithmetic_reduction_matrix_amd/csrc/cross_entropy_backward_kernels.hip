@@ -52,51 +52,71 @@ __device__ __forceinline__ float top_scale(uint32_t top_bits) {
   return top < 0x1p-105f ? 0x1p120f : kTopScale / top;
 }
 
-// A row's scales, a wavefront each; the largest |dloss| (bits, NaNs largest) in *top,
-// which is 0 before (null: not wanted).
+// Rows' scales, kRowsEach for each of a block's wavefronts; the largest |dloss| (bits, NaNs
+// largest) in *top, which is 0 before (null: not wanted).  (With an addition to *top for
+// every row 4096 rows of 4096 values took 58 us, of which now ROWFIG.)
+constexpr int kRowsEach = 4;
 template <int TYPE>
 __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, const float* dloss,
                                                         const float* lse, RowScale* rows,
                                                         uint32_t* top) {
-  const uint64_t row = uint64_t(blockIdx.x) * 4 + wave_id();
-  if (row >= k.rows) return;
-  const uint64_t bits = uint64_t(k.targets[row]);   // the same in all lanes
-  const int64_t t = int64_t(
-      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(bits >> 32)))) << 32 |
-      uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(bits)))));
-  RowScale s = {0.0f, 0.0f, 0.0f, 1u};
-  if (t != k.ignore) {
-    s.skip = 0;
-    s.dloss = dloss[row];
-    if (t >= 0 && t < int64_t(k.vocab)) {
-      const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-      const RowWords xr(k.x + row * k.ldx, cols), wr(k.weight + uint64_t(t) * k.ldw, cols);
-      float z = 0.0f;
-      for (uint32_t c = lane_id(); c < chunks; c += 64) {
-        float f[8], g[8];
-        widen8<TYPE>(xr.load(c), f);
-        widen8<TYPE>(wr.load(c), g);
+  __shared__ uint32_t most[4];
+  uint32_t largest = 0;
+  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
+#pragma unroll 1
+  for (int i = 0; i < kRowsEach; ++i) {
+    const uint64_t row = (uint64_t(blockIdx.x) * 4 + wave_id()) * kRowsEach + i;
+    if (row >= k.rows) break;
+    const uint64_t bits = uint64_t(k.targets[row]);   // the same in all lanes
+    const int64_t t = int64_t(
+        uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(bits >> 32)))) << 32 |
+        uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(bits)))));
+    RowScale s = {0.0f, 0.0f, 0.0f, 1u};
+    if (t != k.ignore) {
+      s.skip = 0;
+      s.dloss = dloss[row];
+      if (t >= 0 && t < int64_t(k.vocab)) {
+        const RowWords xr(k.x + row * k.ldx, cols), wr(k.weight + uint64_t(t) * k.ldw, cols);
+        float z = 0.0f;
+        for (uint32_t c = lane_id(); c < chunks; c += 256) {
+          u32x4 a[4], b[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          z = c * 8 + i < cols ? __builtin_fmaf(f[i], g[i], z) : z;
+          for (int j = 0; j < 4; ++j) {
+            a[j] = xr.load(c + 64 * j);   // zeros past the row
+            b[j] = wr.load(c + 64 * j);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float f[8], g[8];
+            widen8<TYPE>(a[j], f);
+            widen8<TYPE>(b[j], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              z = (c + 64 * j) * 8 + e < cols ? __builtin_fmaf(f[e], g[e], z) : z;
+          }
+        }
+        z = lane_tree_full(z);
+        // (one that is nearly sure of its target keeps a scale that the logit's own
+        // rounding does not turn over)
+        const float rest = __builtin_fmaxf(1.0f - exp_of(z - lse[row]), 0x1p-14f);
+        s.scale = kRowScale / rest;
+        // (an infinite dloss makes infinities of both signs in dz, whose sums are NaNs)
+        s.back = s.dloss - s.dloss == 0.0f ? s.dloss * (rest / kRowScale) : __builtin_nanf("");
+      } else {
+        s.scale = s.dloss = s.back = __builtin_nanf("");
       }
-      z = lane_tree_full(z);
-      // (one that is nearly sure of its target keeps a scale that the logit's own
-      // rounding does not turn over)
-      const float rest = __builtin_fmaxf(1.0f - exp_of(z - lse[row]), 0x1p-14f);
-      s.scale = kRowScale / rest;
-      // (an infinite dloss makes infinities of both signs in dz, whose sums are NaNs)
-      s.back = s.dloss - s.dloss == 0.0f ? s.dloss * (rest / kRowScale) : __builtin_nanf("");
-    } else {
-      s.scale = s.dloss = s.back = __builtin_nanf("");
     }
-  }
-  if (lane_id() == 0) {
-    rows[row] = s;
-    // most rows find one at least as large there (4096 rows 58 -> 35 us)
+    if (lane_id() == 0) rows[row] = s;
     const uint32_t size = __builtin_bit_cast(uint32_t, s.dloss) & 0x7FFFFFFFu;
-    if (top && size > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-      atomicMax(top, size);
+    largest = size > largest ? size : largest;
+  }
+  if (!top) return;
+  if (lane_id() == 0) most[wave_id()] = largest;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 4; ++i) largest = most[i] > largest ? most[i] : largest;
+    if (largest > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+      atomicMax(top, largest);
   }
 }
 
@@ -165,18 +185,18 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   const float all = top ? top_scale(*top) : 0.0f;
   floatx4 z[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
-  const uint64_t row0 = i0 + lane_row<T>(), col = j0 + lane_col<T>();
+  const uint64_t row0 = i0 + lane_row<T>(), col = j0 + wave_col<T>();
   // the rows' values in flight together, before the first store (which the compiler
   // keeps later loads behind)
   RowScale row_scale[T::kMT];
   float row_lse[T::kMT];
-  int64_t row_at[T::kMT];
+  uint32_t row_at[T::kMT];
 #pragma unroll
   for (int i = 0; i < T::kMT; ++i) {
     const uint64_t row = row0 + i < x.rows ? row0 + i : x.rows - 1;
     row_scale[i] = rows[row];
     row_lse[i] = lse[row] * kLog2E;
-    row_at[i] = targets[row] - first - int64_t(col);
+    row_at[i] = column_index(targets[row] - first - int64_t(col));
   }
   float each[T::kMT];
 #pragma unroll
@@ -190,10 +210,10 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
       z[i][c / 4][c % 4] =
           __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][c / 4][c % 4], kLog2E, -l));
     // few wavefronts have a row's target among their columns, or an ignored row
-    const int64_t at = row_at[i];
-    if (at >= 0 && at < T::kCols) {
+    const uint32_t at = row_at[i];
+    if (at < T::kCols) {
 #pragma unroll
-      for (int c = 0; c < T::kCols; ++c) z[i][c / 4][c % 4] -= at == c ? 1.0f : 0.0f;
+      for (int c = 0; c < T::kCols; ++c) z[i][c / 4][c % 4] -= at == uint32_t(c) ? 1.0f : 0.0f;
     }
     if (s.skip) {
 #pragma unroll
@@ -207,7 +227,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
         for (int e = 0; e < 4; ++e)
           v[e] = narrow2<TYPE>(z[i][c / 4 + e / 2][2 * (e % 2)] * s.scale,
                                z[i][c / 4 + e / 2][2 * (e % 2) + 1] * s.scale);
-        *reinterpret_cast<u32x4*>(dz + (row0 + i) * ldz + col + c) = v;
+        *reinterpret_cast<u32x4*>(dz + (row0 + i) * ldz + col + lane_column(c)) = v;
       }
     }
   }
@@ -215,7 +235,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   if (terms == 1) {
 #pragma unroll
     for (int c = 0; c < T::kCols; ++c) {
-      uint16_t* to = dzt + (col + c) * ldt + row0;
+      uint16_t* to = dzt + (col + lane_column(c)) * ldt + row0;
       if constexpr (T::kMT == 1) {
         *to = uint16_t(narrow2<TYPE>(z[0][c / 4][c % 4] * each[0], 0.0f));
       } else {
@@ -241,7 +261,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
         const uint32_t high = narrow2<TYPE>(v, 0.0f);
         float f[8];
         widen8<TYPE>(u32x4{high, 0, 0, 0}, f);
-        uint16_t* to = dzt + (col + c) * ldt + row0 + i;
+        uint16_t* to = dzt + (col + lane_column(c)) * ldt + row0 + i;
         to[0] = uint16_t(high);
         to[x.rows] = uint16_t(narrow2<TYPE>(v - f[0], 0.0f));
       }
@@ -273,7 +293,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
   const uint64_t row0 = i0 + lane_row<T>();
   auto at = [&](int i) ARMX_INLINE {
     const uint64_t row = row0 + i < dz.rows ? row0 + i : dz.rows - 1;
-    return reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + lane_col<T>());
+    return reinterpret_cast<floatx4*>(to + (split * dz.rows + row) * ldd + j0 + wave_col<T>()) + q;
   };
   constexpr int kTogether = T::kMT % 4 == 0 ? 4 : T::kMT % 2 == 0 ? 2 : 1;
 #pragma unroll
@@ -283,7 +303,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
 #pragma unroll
       for (int i = 0; i < kTogether; ++i)
 #pragma unroll
-        for (int y = 0; y < T::kNT; ++y) old[i][y] = at(i0 + i)[across_quad(y, q)];
+        for (int y = 0; y < T::kNT; ++y) old[i][y] = at(i0 + i)[4 * y];
 #pragma unroll
       for (int i = 0; i < kTogether; ++i)
 #pragma unroll
@@ -293,7 +313,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
     for (int i = i0; i < i0 + kTogether; ++i) {
       if (row0 + i >= dz.rows) continue;
 #pragma unroll
-      for (int y = 0; y < T::kNT; ++y) at(i)[across_quad(y, q)] = acc[i][y];
+      for (int y = 0; y < T::kNT; ++y) at(i)[4 * y] = acc[i][y];
     }
   }
 }
@@ -338,7 +358,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dweight_kernel(
   const float back = 1.0f / top_scale(*top);
   floatx4 acc[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(dzt, xt, k, i0, j0, lds, acc);
-  const uint64_t col = j0 + lane_col<T>();
+  const uint64_t col = j0 + wave_col<T>();
 #pragma unroll
   for (int i = 0; i < T::kMT; ++i) {
     const uint64_t row = i0 + lane_row<T>() + i;
@@ -346,32 +366,34 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dweight_kernel(
 #pragma unroll
     for (int y = 0; y < T::kNT; ++y) acc[i][y] *= back;
     if constexpr (OUT == ARMX_F32) {
-      float* o = static_cast<float*>(to) + row * ldo + col;
+      float* o = static_cast<float*>(to) + row * ldo;
 #pragma unroll
       for (int y = 0; y < T::kNT; ++y) {
-        if (col + 4 * y + 4 <= xt.rows) {
-          *reinterpret_cast<f32x4u*>(o + 4 * y) = acc[i][y];
+        const uint64_t c = col + lane_column(4 * y);
+        if (c + 4 <= xt.rows) {
+          *reinterpret_cast<f32x4u*>(o + c) = acc[i][y];
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (col + 4 * y + e < xt.rows) o[4 * y + e] = acc[i][y][e];
+            if (c + e < xt.rows) o[c + e] = acc[i][y][e];
         }
       }
     } else {
-      uint16_t* o = static_cast<uint16_t*>(to) + row * ldo + col;
+      uint16_t* o = static_cast<uint16_t*>(to) + row * ldo;
 #pragma unroll
-      for (int c = 0; c < T::kCols; c += 8) {
+      for (int h = 0; h < T::kCols; h += 8) {
+        const uint64_t c = col + lane_column(h);
         u32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          v[e] = narrow2<OUT>(acc[i][c / 4 + e / 2][2 * (e % 2)],
-                              acc[i][c / 4 + e / 2][2 * (e % 2) + 1]);
-        if (col + c + 8 <= xt.rows) {
+          v[e] = narrow2<OUT>(acc[i][h / 4 + e / 2][2 * (e % 2)],
+                              acc[i][h / 4 + e / 2][2 * (e % 2) + 1]);
+        if (c + 8 <= xt.rows) {
           *reinterpret_cast<u32x4*>(o + c) = v;
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (col + c + e < xt.rows) o[c + e] = uint16_t(v[e / 2] >> (16 * (e % 2)));
+            if (c + e < xt.rows) o[c + e] = uint16_t(v[e / 2] >> (16 * (e % 2)));
         }
       }
     }
@@ -448,7 +470,7 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   {
     void* args[] = {&copy, &dloss, &lse, &rows, &top};
     e = steps.run(reinterpret_cast<const void*>(&loss_rows_kernel<TYPE>),
-                  dim3(unsigned(ceil_div(a.rows, 4))), 256, args);
+                  dim3(unsigned(ceil_div(a.rows, 4 * kRowsEach))), 256, args);
     if (e != hipSuccess) return e;
   }
   uint32_t cols = uint32_t(a.cols);

@@ -5,7 +5,7 @@
 // kept, and those are joined in order by a second kernel.
 //
 // A row's sums do not depend on the tile that makes them: k runs in order in every
-// tile, a wavefront has 64 columns, and their sum is a balanced tree over them.
+// tile, a wavefront has 64 columns, and their sum is one tree over them.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -55,16 +55,16 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
   floatx4 z[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);
-  const uint64_t col = j0 + lane_col<T>();
+  const uint64_t col = j0 + wave_col<T>();
   // a wavefront whose columns are all past the vocabulary has nothing to add
-  const uint64_t piece = (j0 + (wave_id() / T::kWM) * kLossPiece) / kLossPiece;
+  const uint64_t piece = col / kLossPiece;
   if (piece * kLossPiece >= w.rows) return;
   if (j0 + T::kBN > w.rows) {
 #pragma unroll
     for (int y = 0; y < T::kNT; ++y)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (col + 4 * y + e >= w.rows) {
+        if (col + lane_column(4 * y + e) >= w.rows) {
 #pragma unroll
           for (int i = 0; i < T::kMT; ++i) z[i][y][e] = kMinusInf;
         }
@@ -97,11 +97,11 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel
     const float sum = add_xor32(add_xor16((s[0] + s[1]) + (s[2] + s[3])));
     if (row < x.rows) {
       if (lane_id() < 16) parts[part_of(piece, pieces, row)] = Part{m, sum};
-      const int64_t at = target[i] - int64_t(col);
-      if (at >= 0 && at < T::kCols && target[i] < int64_t(w.rows)) {
+      const uint32_t at = column_index(target[i] - int64_t(col));
+      if (at < T::kCols && target[i] < int64_t(w.rows)) {
         float hit = 0.0f;
 #pragma unroll
-        for (int c = 0; c < T::kCols; ++c) hit = at == c ? z[i][c / 4][c % 4] : hit;
+        for (int c = 0; c < T::kCols; ++c) hit = at == uint32_t(c) ? z[i][c / 4][c % 4] : hit;
         hits[row] = hit;
       }
     }

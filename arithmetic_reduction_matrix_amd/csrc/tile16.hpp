@@ -8,9 +8,12 @@
 // the product's row l % 16 and the 4 consecutive columns 4 (l / 16) .. + 3.
 //
 // Which rows of a and b make up an operand tile is free.  Row r of operand tile x of a
-// wavefront's kMT is its row r kMT + x, and row 4 q + e of operand tile y of b's kNT is
-// its column 4 (q kNT + y) + e: lane (q, r) ends with kMT consecutive rows of 4 kNT
-// consecutive columns, whole pieces of either order of the product.
+// wavefront's kMT is its row r kMT + x, and row 4 q + e of operand tile y of b's 4 is its
+// column 32 (y / 2) + 8 q + 4 (y % 2) + e: lane (q, r) ends with kMT consecutive rows of
+// two runs of 8 columns (lane_column), whole 16-byte pieces of either order of the product
+// in 16 bits, of which 4 lanes write 64 bytes in a row at once.  (With one run of 16, whose
+// halves they wrote in turn, 131072 x 4096 x 32 260 us, now MAPFIG.)  Of products written
+// in 32 bits (ACROSS) it is column 16 y + 4 q + e.
 //
 // Steps of 64 values of k (128 bytes, a line) go from memory straight to LDS
 // (buffer_load ... lds) into rings of buffers, NS steps ahead of the one that is
@@ -118,8 +121,9 @@ struct Tile16 {
   static_assert(kLdsBytes <= 160 * 1024, "a compute unit's LDS");
   static_assert(NS >= 2 && NS <= 4, "the last steps are written out");
   static constexpr int kRowB = 2 * BN;   // bytes of a row of b's step that lies across
-  static_assert(kMT <= 16 && kNT <= 16, "operand tiles");
-  static_assert(!ACROSS || (kNT == 4 && (BN == 256 || BN == 128 || BN == 64)), "swizzles");
+  static_assert(kMT <= 16, "operand tiles");
+  static_assert(kNT == 4, "lane_column");
+  static_assert(BN == 256 || BN == 128 || BN == 64, "across_swizzle");
   static_assert(!TURNS || (kWaves == 8 && NS == 2 && MORE_B), "two wavefronts a SIMD, in turns");
 };
 
@@ -155,17 +159,14 @@ __device__ __forceinline__ uint64_t lds_read_across(uint32_t at) {
 
 // Rows of b that lie across: 64 of a step, BN values each, pieces of 16 bytes.  A row keeps
 // its piece p in slot p ^ across_swizzle(row).  A read of 4 values a lane serves 32 lanes at
-// a time: 4 quads c of 8 rows, 0 to 3 and 8 to 11 (or 16 and 8 on), of which those of even
-// c lie in one half of their pieces and those of odd c in the other (across_quad); c's high
-// bit is bit 2 of the slot, and the rows' three bits go into the others.
+// a time: 32 bytes each of 8 rows, 0 to 3 and 8 to 11 (or 16 and 8 on), which the rows'
+// bits lead to different banks.
 template <class T>
 __device__ __forceinline__ uint32_t across_swizzle(uint32_t row) {
   const uint32_t third = (row >> 3) & 1;
-  if constexpr (T::kBN == 64) return ((row >> 1) & 1) | third << 1;   // two rows in 256 bytes
-  return (row & 3) | third << 3;
+  if constexpr (T::kBN == 64) return (((row >> 1) & 1) | third << 1) << 1;   // two rows in 256 bytes
+  return ((row & 3) | third << 2) << 1;
 }
-// Which 4 of a lane's 16 columns operand tile y holds, in lane group q.
-__device__ __forceinline__ uint32_t across_quad(uint32_t y, uint32_t q) { return y ^ (q & 1); }
 
 // vmcnt(N): all but this wavefront's last N loads into LDS have landed
 template <int N>
@@ -189,8 +190,7 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned 
 
 // acc = the tile at (i0, j0) of a b^T over k values, rows and columns past the
 // matrices' undefined.  ACROSS: of a b over the rows of b, of which there are at least k
-// or that end where zeros are to be read, and whose columns are `across`; a lane's columns
-// are in the order of across_quad.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
+// or that end where zeros are to be read, and whose columns are `across`.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
 // barrier.  Every thread of the block takes part.
 template <class T, int TYPE>
 __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16& mb, uint32_t k,
@@ -248,8 +248,8 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     }
     const uint32_t slot = (w * T::kLoadsB + x) * 8 + (lane >> 3);
     const uint32_t in = slot % (16 * kNT), r = in % 16;
-    const uint32_t row =
-        slot / (16 * kNT) * (16 * kNT) + r / 4 * (4 * kNT) + in / 16 * 4 + r % 4;
+    const uint32_t row = slot / (16 * kNT) * (16 * kNT) + in / 32 * 32 + r / 4 * 8 +
+                         in / 16 % 2 * 4 + r % 4;
     off_b[x] = (row < last_b ? row : last_b) * uint32_t(mb.ld * 2) +
                ((uint32_t(lane) & 7) ^ swizzle(r)) * 16;
   }
@@ -310,7 +310,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     const uint32_t j = r / 4, c = r % 4, row = 8 * g + j;
 #pragma unroll
     for (int y = 0; y < kNT; ++y) {
-      const uint32_t byte = (w / T::kWM) * (kNT * 32) + c * (8 * kNT) + across_quad(y, c) * 8;
+      const uint32_t byte = (w / T::kWM) * (kNT * 32) + y * 32 + c * 8;
       at_across[y] = row * T::kRowB + (byte / 16 ^ across_swizzle<T>(row)) * 16 + byte % 16;
     }
   }

@@ -36,14 +36,24 @@ constexpr uint64_t kLargestTile = 256;   // rows and columns
 
 inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
-// The first row and column of the product that a lane of a wavefront holds, in its tile.
+// The first row of the product that a lane of a wavefront holds, in its tile, and the first
+// column of the wavefront.
 template <class T>
 __device__ __forceinline__ uint32_t lane_row() {
   return (wave_id() % T::kWM) * (T::kBM / T::kWM) + (lane_id() & 15) * T::kRows;
 }
 template <class T>
-__device__ __forceinline__ uint32_t lane_col() {
-  return (wave_id() / T::kWM) * (T::kBN / T::kWN) + (lane_id() >> 4) * T::kCols;
+__device__ __forceinline__ uint32_t wave_col() {
+  return (wave_id() / T::kWM) * (T::kBN / T::kWN);
+}
+// A lane's column c of 16 (value c % 4 of operand tile c / 4), in its wavefront's 64.
+__device__ __forceinline__ uint32_t lane_column(uint32_t c) {
+  return c / 8 * 32 + uint32_t(lane_id() >> 4) * 8 + c % 8;
+}
+// Which of a lane's columns is column `at` of its wavefront; 16 or more: none.
+__device__ __forceinline__ uint32_t column_index(int64_t at) {
+  const bool mine = at >= 0 && at < 64 && uint32_t(at) / 8 % 4 == uint32_t(lane_id() >> 4);
+  return mine ? uint32_t(at) / 32 * 8 + uint32_t(at) % 8 : 16u;
 }
 
 }  // namespace

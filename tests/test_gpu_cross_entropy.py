@@ -243,7 +243,10 @@ def test_results_apart_and_in_32_bits(rows, vocab, cols, dtype):
     assert a.dweight is None and torch.equal(a.dx, both.dx)
     assert b.dx is None and b.dweight.dtype == torch.float32
     check_grads(b, dloss, x, w, t, lse)
-    assert torch.equal(b.dweight.to(dtype), both.dweight)
+    # the same sums times the same factor: in 16 bits the product is rounded to half a
+    # step, once (the multiplication's result need not pass through 32 bits), in 32 by U
+    off = (both.dweight.double() - b.dweight.double()).abs()
+    assert torch.all(off <= (HALF[dtype] + 2 * U) * b.dweight.double().abs() + FLOOR[dtype])
 
 
 def test_a_row_does_not_depend_on_the_others():
