@@ -36,6 +36,7 @@ struct CrossEntropyGradPlan {
   uint64_t terms = 0;     // 16-bit terms that stand for a value of dz's transpose
   uint64_t ldt = 0;       // values between rows of it and of x's transpose
   uint64_t splits = 0;    // parts of a piece whose products for dx stand apart
+  int dx_tile = 0;        // and what they are made of
   uint64_t ldd = 0;       // floats between rows of those products
   // byte offsets in the workspace
   size_t top = 0, rows = 0, dz = 0, dzt = 0, xt = 0, dx = 0;
@@ -64,6 +65,12 @@ hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& args,
 
 // Which of the tiles below a product of m x n over k takes.
 int choose_tile16(uint64_t m, uint64_t n, uint64_t k, int cu_count);
+// And with k in parts (powers of two up to `most`) whose products, in 32 bits, are joined.
+struct Split16 {
+  int tile = 0;
+  uint64_t splits = 1;
+};
+Split16 choose_split16(uint64_t m, uint64_t n, uint64_t k, int cu_count, uint64_t most);
 struct Tile16Size {
   int bm, bn;
 };

@@ -54,7 +54,7 @@ __device__ __forceinline__ float top_scale(uint32_t top_bits) {
 
 // Rows' scales, kRowsEach for each of a block's wavefronts; the largest |dloss| (bits, NaNs
 // largest) in *top, which is 0 before (null: not wanted).  (With an addition to *top for
-// every row 4096 rows of 4096 values took 58 us, of which now ROWFIG.)
+// every row 4096 rows of 4096 values took 58 us, now 13.4.)
 constexpr int kRowsEach = 4;
 template <int TYPE>
 __global__ __launch_bounds__(256) void loss_rows_kernel(CrossEntropyArgs k, const float* dloss,
@@ -318,28 +318,43 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
   }
 }
 
-// dx = the splits' products added in order, times the rows' factors.
+// dx = the splits' products added in order, times the rows' factors; 8 columns a thread,
+// whose products of 4 splits are in flight at once.  (One block for all of a row: dx of
+// 1 x 32768 x 1024 43.6 us, now 37.8.)
+constexpr int kJoinChunks = 64;
 template <int TYPE>
-__global__ __launch_bounds__(256) void loss_dx_join_kernel(const float* from, uint64_t ldd,
-                                                           uint64_t splits, const RowScale* rows,
-                                                           uint64_t count, uint64_t cols,
-                                                           uint16_t* dx, uint64_t lddx) {
+__global__ __launch_bounds__(kJoinChunks) void loss_dx_join_kernel(
+    const float* from, uint64_t ldd, uint64_t splits, const RowScale* rows, uint64_t count,
+    uint64_t cols, uint16_t* dx, uint64_t lddx) {
   const uint32_t chunks = uint32_t((cols + 7) / 8);
+  const uint32_t c = blockIdx.y * kJoinChunks + threadIdx.x;
+  if (c >= chunks) return;
   for (uint64_t row = blockIdx.x; row < count; row += gridDim.x) {
     const float back = rows[row].back;
     const bool skip = rows[row].skip;
-    for (uint32_t c = threadIdx.x; c < chunks; c += 256) {
-      floatx4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      for (uint64_t s = 0; s < splits; ++s) {
-        const floatx4* v = reinterpret_cast<const floatx4*>(from + (s * count + row) * ldd) + 2 * c;
-        a += v[0];
-        b += v[1];
-      }
-      float f[8];
+    floatx4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+    auto at = [&](uint64_t s) ARMX_INLINE {
+      return reinterpret_cast<const floatx4*>(from + (s * count + row) * ldd) + 2 * c;
+    };
+    for (uint64_t s = 0; s < splits; s += 4) {
+      floatx4 v[4][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = skip ? 0.0f : (i < 4 ? a[i] : b[i - 4]) * back;
-      store_chunk8<false>(dx + row * lddx, c, uint32_t(cols), narrow8<TYPE>(f));
+      for (int i = 0; i < 4; ++i) {
+        const floatx4* p = at(s + i < splits ? s + i : s);
+        v[i][0] = p[0];
+        v[i][1] = p[1];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s + i < splits) {
+          a += v[i][0];
+          b += v[i][1];
+        }
     }
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = skip ? 0.0f : (i < 4 ? a[i] : b[i - 4]) * back;
+    store_chunk8<false>(dx + row * lddx, c, uint32_t(cols), narrow8<TYPE>(f));
   }
 }
 
@@ -415,6 +430,7 @@ constexpr uint64_t kTwoTerms = 128;
 // dz of a piece: at most this many values, but at least kLeastPiece vocabulary rows.
 constexpr uint64_t kPieceValues = uint64_t(1) << 27;
 constexpr uint64_t kLeastPiece = 1024;
+constexpr uint64_t kMostSplits = 64;
 constexpr uint64_t kRoom = kLargestTile;
 
 uint64_t round_up(uint64_t v, uint64_t to) { return ceil_div(v, to) * to; }
@@ -507,7 +523,7 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                      \
   e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T::Across, TYPE>), \
                 dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args)
-      ARMX_OF_TILE(choose_tile16(a.rows * plan.splits, a.cols, per, cu_count), ARMX_TILE_CASE);
+      ARMX_OF_TILE(plan.dx_tile, ARMX_TILE_CASE);
 #undef ARMX_TILE_CASE
       if (e != hipSuccess) return e;
     }
@@ -536,8 +552,11 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   const RowScale* scales = rows;
   uint16_t* dx = grads.dx;
   void* args[] = {&from, &ldd, &splits, &scales, &count, &all, &dx, &lddx};
+  const uint64_t across = ceil_div(all, 8 * kJoinChunks);
+  const uint64_t most = kMaxGrid * 1024 / kJoinChunks / across;
   return steps.run(reinterpret_cast<const void*>(&loss_dx_join_kernel<TYPE>),
-                   dim3(unsigned(count < kMaxGrid ? count : kMaxGrid)), 256, args, true);
+                   dim3(unsigned(count < most ? count : most), unsigned(across)), kJoinChunks,
+                   args, true);
 }
 
 }  // namespace
@@ -561,12 +580,12 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   // with one term a tile's rows past the last are written too
   p.ldt = round_up(p.terms == 2 ? 2 * rows : rows + kRoom - 1, kStepValues) + kStepValues;
   p.ldd = round_up(cols, kRoom);
-  // products for dx of few tiles: parts of the piece in blocks of their own
-  const uint64_t tiles = ceil_div(rows, 128) * ceil_div(cols, 128);
-  p.splits = 1;
-  while (p.splits < 64 && tiles * p.splits < uint64_t(cu_count) &&
-         p.piece / (2 * p.splits) >= 512)
-    p.splits *= 2;
+  // Of few tiles, parts of the piece in blocks of their own: tile and parts are chosen
+  // together.  (Parts up to a block of 128 x 128 for every compute unit, and their tile after
+  // that: dx of 256 x 131072 x 4096 666 us, now 530; of 1024 x 32768 x 4096 550, now 450.)
+  const Split16 dx_of = choose_split16(rows, cols, p.piece, cu_count, kMostSplits);
+  p.splits = dx_of.splits;
+  p.dx_tile = dx_of.tile;
   size_t at = 0;
   auto take = [&](size_t& offset, uint64_t bytes) {
     offset = at;

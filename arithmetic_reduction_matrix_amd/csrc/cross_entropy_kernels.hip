@@ -179,44 +179,62 @@ Tile16Size tile16_size(int index) {
   return s;
 }
 
-// The tile whose estimated time is least.  A compute unit that makes q tiles runs them in
-// rounds of at most `resident` blocks; a round takes `fixed` (its first loads, its
-// results) and, per step of 64 values of k, `alone` or, with several blocks on the unit,
-// `each` of them if that is more.  The constants (us) are fitted to times of each tile on
-// MI355X over 137 products of 1 to 4096 rows, 256 to 131072 columns and lengths of 64 to
-// 32064 with 16-bit results; over those the tile that they choose is 2.4% behind the
-// fastest of fourteen on average, and 53% at worst (515 x 1000 x 8192, which no caller
-// makes in one part).  Each pays where it is chosen (us, it and the best of the others):
-// 256 x 256 at 4096 x 131072 x 128 386 (424); 192 x 256 at 777 x 50001 x 2056 227 (232);
-// 256 x 128 at 515 x 32003 x 1000 63 (64); 128 x 128 at 32003 x 4096 x 128 77 (86);
-// 64 x 128 at 1 x 50001 x 8192 143 (149); 32 x 128 at 200 x 4096 x 16384 96 (117);
-// 16 x 128 at 8 x 32768 x 1024 13.2 (13.4); 16 x 64 at 515 x 1000 x 8192 32 (42).
-int choose_tile16(uint64_t m, uint64_t n, uint64_t k, int cu_count) {
+namespace {
+
+// The estimated time of a product's tiles (us), each of `steps` steps of 64 values of k.  A
+// compute unit that makes q tiles runs them in rounds of at most `resident` blocks; a round
+// takes `fixed` (its first loads, its results) and, per step, `alone` or, with several blocks
+// on the unit, `each` of them if that is more.
+//
+// The constants are fitted to times of each tile on MI355X over 335 products of 1 to 131072
+// rows, 256 to 131072 columns and lengths of 16 to 32064 with 16-bit results; over those the
+// tile that they choose is 2.5% behind the fastest on average, and 32% at worst
+// (33 x 16384 x 2056).  Each pays where it is chosen (us, it and the best of the others):
+// 256 x 256 at 1024 x 32003 x 2056 132 (163); 192 x 256 at 384 x 32003 x 1000 37 (41);
+// 256 x 128 at 777 x 8192 x 8192 104 (119); 128 x 128 at 2048 x 32003 x 128 41 (52);
+// 64 x 128 at 256 x 8192 x 4096 35 (41); 32 x 128 at 128 x 8192 x 512 6.2 (6.2); 16 x 128 at 1024 x 1000 x 64 4.5 (4.9); 16 x 64 at
+// 16 x 4096 x 8192 29 (43).
+double tile16_time(int index, uint64_t tiles, uint64_t k, int cu_count) {
   struct Time {
     int resident;
     float fixed, alone, each;
   };
   constexpr Time times[kTile16s] = {
-      {1, 6.10f, 1.21f, 1.21f}, {1, 3.90f, 1.08f, 1.08f}, {1, 3.29f, 0.73f, 0.73f},
-      {2, 2.32f, 0.52f, 0.55f}, {2, 1.78f, 0.11f, 0.41f}, {2, 1.38f, 0.34f, 0.37f},
-      {2, 1.19f, 0.25f, 0.29f}, {3, 1.04f, 0.20f, 0.16f}};
-  int best = -1;
-  double least = 0;
+      {1, 7.25f, 1.21f, 1.21f}, {1, 4.66f, 1.07f, 1.07f}, {1, 3.74f, 0.73f, 0.73f},
+      {2, 2.66f, 0.36f, 0.52f}, {2, 1.81f, 0.31f, 0.37f}, {2, 1.46f, 0.38f, 0.30f},
+      {2, 1.16f, 0.28f, 0.24f}, {3, 1.08f, 0.27f, 0.12f}};
+  const Time t = times[index];
+  const uint64_t per_cu = ceil_div(tiles, uint64_t(cu_count));
+  const double steps = double(ceil_div(k, uint64_t(kStepValues)));
+  auto round = [&](uint64_t blocks) {
+    const double together = double(blocks) * t.each;
+    return blocks == 0 ? 0.0 : t.fixed + steps * (together > t.alone ? together : t.alone);
+  };
+  return double(per_cu / t.resident) * round(t.resident) + round(per_cu % t.resident);
+}
+
+constexpr uint64_t kLeastSplit = 512;   // values of k in a part
+
+}  // namespace
+
+int choose_tile16(uint64_t m, uint64_t n, uint64_t k, int cu_count) {
+  return choose_split16(m, n, k, cu_count, 1).tile;
+}
+
+Split16 choose_split16(uint64_t m, uint64_t n, uint64_t k, int cu_count, uint64_t most) {
+  Split16 best;
+  double least = -1;
   for (int i = 0; i < kTile16s; ++i) {
     const Tile16Size s = tile16_size(i);
     const uint64_t tiles = ceil_div(m, uint64_t(s.bm)) * ceil_div(n, uint64_t(s.bn));
-    if (tiles > 0x7FFFFFFFu / 1024) continue;  // the grid's limit
-    const uint64_t per_cu = ceil_div(tiles, uint64_t(cu_count));
-    const double steps = double(ceil_div(k, uint64_t(kStepValues)));
-    auto round = [&](uint64_t blocks) {
-      const double together = double(blocks) * times[i].each;
-      return blocks == 0 ? 0.0
-                         : times[i].fixed +
-                               steps * (together > times[i].alone ? together : times[i].alone);
-    };
-    const double t = double(per_cu / times[i].resident) * round(times[i].resident) +
-                     round(per_cu % times[i].resident);
-    if (best < 0 || t < least) best = i, least = t;
+    for (uint64_t splits = 1; splits <= most; splits *= 2) {
+      if (tiles * splits > 0x7FFFFFFFu / 1024) break;  // the grid's limit
+      if (splits > 1 && k / splits < kLeastSplit) break;
+      // (a product is written and read again to be joined, at 4.9 TB/s)
+      const double join = most > 1 ? double(splits) * double(m) * double(n) * 8 / 4.9e6 : 0;
+      const double t = tile16_time(i, tiles * splits, ceil_div(k, splits), cu_count) + join;
+      if (least < 0 || t < least) best = Split16{i, splits}, least = t;
+    }
   }
   return best;
 }

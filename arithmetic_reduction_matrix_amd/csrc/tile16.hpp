@@ -12,8 +12,8 @@
 // column 32 (y / 2) + 8 q + 4 (y % 2) + e: lane (q, r) ends with kMT consecutive rows of
 // two runs of 8 columns (lane_column), whole 16-byte pieces of either order of the product
 // in 16 bits, of which 4 lanes write 64 bytes in a row at once.  (With one run of 16, whose
-// halves they wrote in turn, 131072 x 4096 x 32 260 us, now MAPFIG.)  Of products written
-// in 32 bits (ACROSS) it is column 16 y + 4 q + e.
+// halves they wrote in turn, 131072 x 4096 x 32 in tiles of 192 x 256 took 317 us, now 296.)
+// Of products written in 32 bits (ACROSS) it is column 16 y + 4 q + e.
 //
 // Steps of 64 values of k (128 bytes, a line) go from memory straight to LDS
 // (buffer_load ... lds) into rings of buffers, NS steps ahead of the one that is
@@ -353,10 +353,12 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
       uint32_t from_a = base_a + at_a[h], from_b = base_b + (T::kAcross ? 0 : at_b[h]);
       asm("" : "+v"(from_a));
       asm("" : "+v"(from_b));
-#pragma unroll
-      for (int y = 0; y < kNT; ++y) fb[y] = read_b(from_b, h, y);
+      // (a first: with ACROSS's reads of b, two for each of a's, in front dx's product of
+      // 4096 x 4096 x 32768 was 2% slower; others do not tell)
 #pragma unroll
       for (int x = 0; x < kMT; ++x) fa[x] = lds_read16(from_a + x * 16 * kStepBytes);
+#pragma unroll
+      for (int y = 0; y < kNT; ++y) fb[y] = read_b(from_b, h, y);
       __builtin_amdgcn_sched_barrier(0);
     };
     // the reads are done, and values past k cut from both operands (what stands there may
