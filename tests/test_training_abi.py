@@ -111,12 +111,16 @@ def test_layer_norm_backward_refusals():
     assert back(cols=0, dy=None, h=None, dw=None, db=None) == 0
 
 
-def test_layer_norm_workspace_is_twice_the_rms_norms():
-    for rows, cols in [(1, 64), (1000, 64), (2000, 64), (8192, 4096), (513, 16385), (0, 64)]:
-        assert armx.workspace_bytes(armx.OP_LAYER_NORM_BACKWARD, rows, cols) == \
-            2 * armx.workspace_bytes(armx.OP_RMS_BACKWARD, rows, cols)
+def test_layer_norm_workspace_is_two_rows_of_sums_a_block():
+    for rows, cols in [(1, 64), (1000, 64), (2000, 64), (8192, 4096), (8192, 3000), (513, 16385),
+                       (0, 64)]:
         plan = armx.launch_plan(armx.OP_LAYER_NORM_BACKWARD, rows, cols)
-        assert plan["launches"] == (2 if plan["workspace_bytes"] else 1)
+        need = armx.workspace_bytes(armx.OP_LAYER_NORM_BACKWARD, rows, cols)
+        assert plan["workspace_bytes"] == need
+        assert need in (0, plan["grid_blocks"] * 2 * ((cols + 63) // 64 * 64) * 4)
+        # few rows, and rows that the registers do not hold beside the sums, need none
+        assert (need == 0) == ((rows <= 1024 and rows * cols <= 1 << 23) or cols > 16384)
+        assert plan["launches"] == (2 if need else 1)
 
 
 BAD_LOSS_SIZES = [dict(vocab=0), dict(cols=0), dict(cols=(1 << 21) + 1, rows=1, vocab=1),
