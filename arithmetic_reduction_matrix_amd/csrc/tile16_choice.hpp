@@ -34,7 +34,7 @@ constexpr uint64_t kLargestTile = 256;   // rows and columns
     }                             \
   } while (0)
 
-inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // The first row of the product that a lane of a wavefront holds, in its tile, and the first
 // column of the wavefront.
