@@ -312,12 +312,15 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
 
 // The part of dx that a piece of the vocabulary makes: dz (rows x k) times the piece's rows
 // of w (k x cols), k in `splits` parts of `per` whose products stand apart; added to what
-// is there after the first piece.  `to` has whole tiles of room for columns.
+// is there after the first piece.  `to` has whole tiles of room for columns.  With `dx` the
+// piece is the last and its only product the whole of it: dx itself, times the rows'
+// factors, instead.  (By way of the sums and a join: gradients of 2046 x 1216 x 192 36.4 us,
+// now 31.9; of 4096 x 131072 x 4096 9663, now 9631.)
 template <class T, int TYPE>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
     Matrix16 dz, Matrix16 w, uint64_t cols, uint32_t k, uint32_t per, float* to, uint64_t ldd,
-    bool more,
-    unsigned tiles_m, unsigned tiles_n) {
+    bool more, uint16_t* dx, uint64_t lddx, const RowScale* rows, unsigned tiles_m,
+    unsigned tiles_n) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   const unsigned id = unsigned(xcd_block_id()), split = id / (tiles_m * tiles_n);
   unsigned ti, tj;
@@ -350,11 +353,39 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
 #pragma unroll
         for (int y = 0; y < T::kNT; ++y) acc[i0 + i][y] += old[i][y];
     }
+    float back[kTogether];
+    uint32_t skip[kTogether];
+    if (dx) {
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const RowScale& r = rows[row0 + i0 + i < dz.rows ? row0 + i0 + i : dz.rows - 1];
+        back[i] = r.back;
+        skip[i] = r.skip;
+      }
+    }
 #pragma unroll
     for (int i = i0; i < i0 + kTogether; ++i) {
       if (row0 + i >= dz.rows) continue;
+      if (!dx) {
 #pragma unroll
-      for (int y = 0; y < T::kNT; ++y) at(i)[4 * y] = acc[i][y];
+        for (int y = 0; y < T::kNT; ++y) at(i)[4 * y] = acc[i][y];
+        continue;
+      }
+      uint16_t* out = dx + (row0 + i) * lddx;
+#pragma unroll
+      for (int y = 0; y < T::kNT; ++y) {
+        const uint64_t c = j0 + wave_col<T>() + 16 * y + 4 * q;
+        const floatx4 v = acc[i][y] * back[i - i0];
+        u32x2 h = {narrow2<TYPE>(v[0], v[1]), narrow2<TYPE>(v[2], v[3])};
+        if (skip[i - i0]) h = u32x2{0, 0};
+        if (c + 4 <= cols) {
+          *reinterpret_cast<u32x2*>(out + c) = h;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < cols) out[c + e] = uint16_t(h[e / 2] >> (16 * (e % 2)));
+        }
+      }
     }
   }
 }
@@ -551,12 +582,16 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
       uint64_t across = a.cols;
       uint32_t per = uint32_t(round_up(ceil_div(count, plan.splits), kStepValues));
       bool more = v0 != 0;
-      void* args[] = {&mz, &mw, &across, &k, &per, &sums, &ldd, &more, &tiles_m, &tiles_n};
+      uint16_t* out = last && plan.splits == 1 ? grads.dx : nullptr;
+      uint64_t lddx = grads.lddx;
+      void* args[] = {&mz, &mw, &across, &k, &per, &sums, &ldd, &more, &out, &lddx, &rows,
+                      &tiles_m, &tiles_n};
 #define ARMX_TILE_CASE(T)                                                      \
   tiles_m = unsigned(ceil_div(a.rows, uint64_t(T::kBM)));                      \
   tiles_n = unsigned(ceil_div(a.cols, uint64_t(T::kBN)));                      \
   e = steps.run(reinterpret_cast<const void*>(&loss_dx_kernel<T::Across, TYPE>), \
-                dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args)
+                dim3(tiles_m * tiles_n * unsigned(plan.splits)), T::kThreads, args,       \
+                out && !dzt)
       ARMX_OF_TILE(plan.dx_tile, ARMX_TILE_CASE);
 #undef ARMX_TILE_CASE
       if (e != hipSuccess) return e;
@@ -574,13 +609,13 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   e = steps.run(grads.dweight_type == ARMX_F32                                              \
                     ? reinterpret_cast<const void*>(&loss_dweight_kernel<T, TYPE, ARMX_F32>) \
                     : reinterpret_cast<const void*>(&loss_dweight_kernel<T, TYPE, TYPE>),   \
-                dim3(tiles_m * tiles_n), T::kThreads, args, last && !dz)
+                dim3(tiles_m * tiles_n), T::kThreads, args, last && !(dz && plan.splits > 1))
       ARMX_OF_TILE(choose_tile16(count, a.cols, k, cu_count), ARMX_TILE_CASE);
 #undef ARMX_TILE_CASE
       if (e != hipSuccess) return e;
     }
   }
-  if (!dz) return hipSuccess;
+  if (!dz || plan.splits == 1) return hipSuccess;
   const float* from = sums;
   uint64_t splits = plan.splits, count = a.rows, all = a.cols, lddx = grads.lddx;
   const RowScale* scales = rows;
@@ -629,7 +664,7 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   take(p.rows, rows * sizeof(RowScale));
   if (dx) {
     take(p.dz, rows * p.ldz * 2);
-    take(p.dx, p.splits * rows * p.ldd * 4);
+    if (p.splits > 1 || p.piece < vocab) take(p.dx, p.splits * rows * p.ldd * 4);
   }
   if (dweight) {
     take(p.dzt, p.piece * p.ldt * 2);

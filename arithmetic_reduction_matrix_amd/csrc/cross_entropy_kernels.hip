@@ -214,6 +214,7 @@ double tile16_time(int index, uint64_t tiles, uint64_t k, int cu_count) {
 }
 
 constexpr uint64_t kLeastSplit = 512;   // values of k in a part
+constexpr double kJoinLaunch = 4;       // us
 
 }  // namespace
 
@@ -230,8 +231,9 @@ Split16 choose_split16(uint64_t m, uint64_t n, uint64_t k, int cu_count, uint64_
     for (uint64_t splits = 1; splits <= most; splits *= 2) {
       if (tiles * splits > 0x7FFFFFFFu / 1024) break;  // the grid's limit
       if (splits > 1 && k / splits < kLeastSplit) break;
-      // (a product is written and read again to be joined, at 4.9 TB/s)
-      const double join = most > 1 ? double(splits) * double(m) * double(n) * 8 / 4.9e6 : 0;
+      // (products are written and read again to be joined, at 4.9 TB/s, by another launch)
+      const double join =
+          splits > 1 ? kJoinLaunch + double(splits) * double(m) * double(n) * 8 / 4.9e6 : 0;
       const double t = tile16_time(i, tiles * splits, ceil_div(k, splits), cu_count) + join;
       if (least < 0 || t < least) best = Split16{i, splits}, least = t;
     }
