@@ -329,6 +329,7 @@ int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
   if (sum_out && sum_out == out && rows && cols) return ARMX_ERR_CONFIG;
   if (!aligned(mean, 4) || !aligned(inv_std, 4)) return ARMX_ERR_ALIGN;
   if (rows == 0) return ARMX_OK;
+  if (mean && mean == inv_std) return ARMX_ERR_CONFIG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (cols == 0) {
     for (float* zeros : {mean, inv_std}) {
@@ -387,6 +388,7 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
     if (!aligned(ws, 256)) return ARMX_ERR_ALIGN;
     if (ws_bytes < plan.ws_bytes) return ARMX_ERR_WORKSPACE;
   }
+  if (dweight == dbias) return ARMX_ERR_CONFIG;
   a.dy = static_cast<const uint16_t*>(dy);
   a.h = static_cast<const uint16_t*>(h);
   a.weight = static_cast<const uint16_t*>(weight);
@@ -432,6 +434,7 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
   const armx::CrossEntropyPlan plan = armx::plan_cross_entropy(rows, vocab);
   st = check_space(ws, ws_bytes, plan.ws_bytes);
   if (st != ARMX_OK) return st;
+  if (loss == lse) return ARMX_ERR_CONFIG;
   const int cus = armx::current_cu_count();
   log_loss("cross_entropy_rows", a, plan.ws_bytes, cus);
   return hip_status(armx::launch_cross_entropy(a, plan, loss, lse, ws, cus, cfg,
@@ -472,6 +475,7 @@ int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
       armx::plan_cross_entropy_backward(rows, vocab, cols, dx != nullptr, dweight != nullptr, cus);
   st = check_space(ws, ws_bytes, plan.ws_bytes);
   if (st != ARMX_OK) return st;
+  if (dx == dweight) return ARMX_ERR_CONFIG;
   log_loss("cross_entropy_rows_backward", a, plan.ws_bytes, cus);
   return hip_status(armx::launch_cross_entropy_backward(a, plan, g, ws, cus, cfg, s));
 }

@@ -597,7 +597,7 @@ int dropout_rows(const void* x, size_t ldx, const void* residual, size_t ldr, in
  * 2^-63) lose bits or count as 0, which counts where eps is below 2^-100.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,SHAPE,HIP}; a type other than the
  * two, an eps that is negative or NaN, a p outside 0 .. 1, or an out that starts where
- * sum_out does is ARMX_ERR_CONFIG.
+ * sum_out does (or mean where inv_std) is ARMX_ERR_CONFIG.
  */
 int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
                     const void* weight, const void* bias, int type, size_t rows, size_t cols,
@@ -630,7 +630,8 @@ int layer_norm_rows(const void* x, size_t ldx, const void* residual, size_t ldr,
  * ws       device workspace of armx_workspace_bytes(ARMX_OP_LAYER_NORM_BACKWARD, rows,
  *          cols, NULL) bytes; it needs no zeros and none are left (it has no
  *          counter region).  NULL when that is 0.
- * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}; dx where dresidual
+ * starts, or dweight where dbias does, is ARMX_ERR_CONFIG.
  */
 int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t ldh,
                              const void* weight, const float* mean, const float* inv_std,
@@ -646,7 +647,8 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
  *   loss[r] = lse[r] - z[r][targets[r]], or 0 where targets[r] == ignore_index
  * all in binary32 (products of 16-bit values are exact, the sums are those of the matrix
  * units).  No z is stored: a tile of them at a time is made and summed up.  A row's loss
- * does not depend on how many rows there are (batch invariance).
+ * does not depend on how many rows there are (batch invariance).  An infinite z counts as
+ * it is where it is -infinity; +infinity or a NaN makes NaNs of its row's lse and loss.
  *
  * x        device, rows x cols, ARMX_F16 or ARMX_BF16 (hidden states).
  * weight   device, vocab x cols of the same type (the output layer's).
@@ -661,7 +663,8 @@ int layer_norm_rows_backward(const void* dy, size_t ldy, const void* h, size_t l
  * vocab and cols are at least 1 (ARMX_ERR_SHAPE), cols at most 2^21, rows 2^21, vocab
  * 2^28, pitches 2^22, and ceil(rows / 256) * ceil(vocab / 256) at most 2097151.
  * Rows that all start at multiples of 128 bytes are read fastest.
- * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}.
+ * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}; loss where lse
+ * starts is ARMX_ERR_CONFIG.
  */
 int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw,
                        const int64_t* targets, int type, size_t rows, size_t vocab, size_t cols,
@@ -694,7 +697,7 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
  * 2097151.  A row of dx, and of dweight, may depend in its last bit on the row count and
  * the device's compute-unit count; nothing depends on timing.
  * Returns ARMX_OK or ARMX_ERR_{NULL,ALIGN,CONFIG,WORKSPACE,SHAPE,HIP}; dx and dweight
- * both NULL is ARMX_ERR_NULL.
+ * both NULL is ARMX_ERR_NULL, in one place ARMX_ERR_CONFIG.
  */
 int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
                                 const void* weight, size_t ldw, const int64_t* targets,

@@ -163,6 +163,15 @@ def test_cross_entropy_backward_refusals():
     assert grad(rows=0, g=None, x=None, w=None, t=None, lse=None, dx=None, dw=None, ws=None) == 0
 
 
+def test_two_results_in_one_place_are_refused():
+    assert norm(mean=P, inv=P) == -3 and norm(mean=P, inv=P, cols=0) == -3
+    assert back(dw=P, db=P) == -3
+    assert loss(out=P, lse=P) == -3
+    assert grad(dx=P, dw=P) == -3
+    # which is said last: what else is wrong has its own status
+    assert loss(out=P, lse=P, ws_bytes=0) == -4 and grad(dx=P, dw=P, ws_bytes=0) == -4
+
+
 def test_cross_entropy_workspaces():
     size = lib.armx_cross_entropy_backward_workspace_bytes
     both, dx, dw = (size(4096, 131072, 4096, *w) for w in ((1, 1), (1, 0), (0, 1)))
