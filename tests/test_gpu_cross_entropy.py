@@ -287,6 +287,34 @@ def test_several_pieces():
     assert np.all(np.abs(f64(g.dweight) - dw) <= tol * (2.0 ** -11 + 2.0 ** -13 + 2 * U * rows))
 
 
+def test_pieces_in_parts():
+    # two pieces of 2^27 values of dz and a little more, each with its product for dx in
+    # parts, the last of them shorter or empty in the second piece
+    rng = np.random.default_rng(10)
+    rows, vocab, cols = 3000, 50001, 72
+    x, w, t = inputs(rng, rows, vocab, cols, torch.bfloat16)
+    got = armx.cross_entropy_rows(x, w, t)
+    dloss = torch.from_numpy(rng.uniform(0.5, 1.5, rows).astype(np.float32)).cuda()
+    g = armx.cross_entropy_rows_backward(dloss, x, w, t, got.lse, dweight_dtype=torch.float32)
+    some = torch.from_numpy(np.r_[0:60, rows - 60:rows]).cuda()
+    check_grads(armx.CrossEntropyGrads(g.dx[some], None), dloss[some], x[some], w, t[some],
+                got.lse[some])
+    # dweight's rows at the pieces' ends and those of some targets, with check_grads' bound
+    tn, lse, xs = t.cpu().numpy(), f64(got.lse), f64(x)
+    live = tn != -100
+    words = np.unique(np.r_[0:40, 25000:25200, vocab - 40:vocab, tn[live][:40]])
+    ws = f64(w)[words]
+    z, ag = xs @ ws.T, (f64(dloss) * live)[:, None]
+    p = np.exp(z - lse[:, None])
+    dz = (p - (tn[:, None] == words)) * ag
+    e_z = 2 * U * 1.02 * (cols + 8) * (np.abs(xs) @ np.abs(ws).T)
+    e_p = p * (e_z + U * (3 * np.abs(z) + 3 * np.abs(lse)[:, None] + 5))
+    e_dz = np.abs(dz) * (HALF[x.dtype] + 4 * U) + ag * e_p + FLOOR[x.dtype] * ag.max() * 2.0 ** -15
+    tol = e_dz.T @ np.abs(xs) + 2 * U * (2 * rows + 40) * (np.abs(dz).T @ np.abs(xs))
+    want = dz.T @ xs
+    assert np.all(np.abs(f64(g.dweight)[words] - want) <= (tol + U * np.abs(want)) * 1.02)
+
+
 def test_places_past_32_bits():
     vocab, cols = (1 << 19) + 13, 4096 + 8   # 2^31 values and more
     w = torch.empty(vocab, cols, dtype=torch.bfloat16, device="cuda")
