@@ -180,7 +180,7 @@ def cross_entropy_rows_backward(dloss: torch.Tensor, x: torch.Tensor, weight: to
     row's loss, ``lse`` as it returned them.  Returns dx (of x's type; ``out`` receives
     it) and dweight (x's type, or float32 by ``dweight_dtype`` or by ``dweight``), each
     None if not wanted.  The logits are made again, a piece of the vocabulary at a time;
-    without ``workspace`` one is taken from the allocator for this call (about 0.6 GB of
+    without ``workspace`` one is taken from the allocator for this call (about 0.7 GB of
     pieces and transposes at 4096 rows of 4096 values)."""
     code = None if dweight_dtype is None else _TYPES.get(dweight_dtype, 3)
     return _done(_binding.cross_entropy_rows_backward(dloss, x, weight, targets, lse,
