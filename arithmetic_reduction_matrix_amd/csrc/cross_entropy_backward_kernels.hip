@@ -226,7 +226,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
     uint16_t* dzt, uint64_t ldt, uint64_t terms, unsigned tiles_m, unsigned tiles_n) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   unsigned ti, tj;
-  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  tile_of<T>(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
   const float all = top ? top_scale(*top) : 0.0f;
   floatx4 z[T::kMT][T::kNT];
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   const unsigned id = unsigned(xcd_block_id()), split = id / (tiles_m * tiles_n);
   unsigned ti, tj;
-  tile_of(id % (tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
+  tile_of<T>(id % (tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
   const uint32_t k0 = split * per;
   const uint32_t part = k0 >= k ? 0 : k - k0 < per ? k - k0 : per;
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dweight_kernel(
     unsigned tiles_m, unsigned tiles_n) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   unsigned ti, tj;
-  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  tile_of<T>(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
   const float back = 1.0f / top_scale(*top);
   floatx4 acc[T::kMT][T::kNT];

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void cross_entropy_kernel
   static_assert(T::kNT == 4, "a wavefront's columns are one piece");
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kLdsBytes];
   unsigned ti, tj;
-  tile_of(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
+  tile_of<T>(unsigned(xcd_block_id()), tiles_m, tiles_n, ti, tj);
   const uint64_t i0 = uint64_t(ti) * T::kBM, j0 = uint64_t(tj) * T::kBN;
   floatx4 z[T::kMT][T::kNT];
   multiply_tile<T, TYPE>(x, w, cols, i0, j0, lds, z);

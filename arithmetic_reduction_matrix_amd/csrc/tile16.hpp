@@ -94,6 +94,7 @@ using Yes = Int<1>;
 using No = Int<0>;
 
 constexpr int kStepBytes = 128, kStepValues = 64;
+constexpr unsigned kGroupRows = 1024;   // tile_of
 
 // A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of an operand
 // have a buffer, and of one of the two (b with MORE_B) one step more, so that its loads
@@ -106,6 +107,7 @@ struct Tile16 {
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
   static constexpr bool kMoreB = MORE_B, kTurns = TURNS, kAcross = ACROSS;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr unsigned kGroup = kGroupRows / BM;   // rows of tiles
   static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
   static constexpr int kNT = BN / WN / 16;
   static constexpr int kRows = kMT, kCols = 4 * kNT;   // a lane's part of the product
@@ -176,13 +178,16 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Which tile a block makes: every XCD takes a contiguous range of ids, and ids run down
-// kTileGroup rows of tiles before the next column, so that blocks running at the same
-// time on one XCD share operand rows in its L2.
-constexpr unsigned kTileGroup = 4;
+// kGroup rows of tiles, 1024 of the product, before the next column, so that blocks running
+// at the same time on one XCD share operand rows in its L2.  (Us, 4 rows of tiles / 1024 rows
+// of any: 777 x 50001 x 2056 of 192 x 256 196 / 181, 131072 x 4096 x 256 of 128 x 128 459 /
+// 423; 768, 1536, 2048 and 4096 rows over the shapes where each tile is chosen are 1% slower
+// on average, 32768 x 4096 x 4096 of 256 x 256 727 with 1024 rows, 756 with 1536.)
+template <class T>
 __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned tiles_n,
                                         unsigned& ti, unsigned& tj) {
-  const unsigned per = kTileGroup * tiles_n, grp = id / per, first = grp * kTileGroup;
-  const unsigned rows = tiles_m - first < kTileGroup ? tiles_m - first : kTileGroup;
+  const unsigned per = T::kGroup * tiles_n, grp = id / per, first = grp * T::kGroup;
+  const unsigned rows = tiles_m - first < T::kGroup ? tiles_m - first : T::kGroup;
   const unsigned in = id - grp * per;
   ti = first + in % rows;
   tj = in / rows;
