@@ -15,8 +15,8 @@
 //   (kTwoTerms), multiplied by the same row of x.
 // Powers of two keep both in binary16's range: 2^14 for dx, 2^15 for dweight.
 //
-// Of 4096 x 131072 x 4096 bf16 (9.6 ms) a piece of 32768 takes 839 us for logits and dz,
-// whose second copy is 2% of them, 807 for dx and 767 for dweight, where a library's products
+// Of 4096 x 131072 x 4096 bf16 (9.6 ms) a piece of 32768 takes 840 us for logits and dz,
+// whose second copy is 2% of them, 805 for dx and 767 for dweight, where a library's products
 // alone take 740, 680 and 718: the matrix units are busy in 69, 73 and 78% of cycles, at a
 // clock of 1.7 to 1.8 GHz.  Pieces of 2^24 to 2^28 values take the same time.
 #include <hip/hip_runtime.h>

@@ -4,7 +4,7 @@
 // As in the root-mean-square norm a row lies in the registers of the threads that
 // share it and every value is read and written once: HBM is the bound.  (8192 x 4096 bf16
 // with residual and dropout 47 us, 5.7 TB/s read and written; its gradients with all that
-// flows 71, 4.7 TB/s, 5 of them the join of the blocks' sums; dropout of 16384 x 8192 88,
+// flows 72, 4.7 TB/s, 5 of them the join of the blocks' sums; dropout of 16384 x 8192 87,
 // 6.1 TB/s; a large copy reaches 4.9.  The bits of dropout cost 120 vector instructions for
 // 8 values, which hide under the loads of other wavefronts.)
 //
