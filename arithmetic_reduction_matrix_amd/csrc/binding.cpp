@@ -7,8 +7,8 @@
 // 1 / rms 11.0 / 6.3, product 1 x 4096 x 4096 8.5 / 4.7, backward 515 x 2056
 // 15.6 / 9.5).
 //
-// Every function takes positional arguments (layer.py gives them names, defaults
-// and documentation) and returns a tuple of tensors, or the library's status as an
+// Every function takes positional arguments (layer.py and training.py give them names,
+// defaults and documentation) and returns a tuple of tensors, or the library's status as an
 // int when it is not ARMX_OK.  Wrong types raise TypeError, anything else that the
 // tensors get wrong ValueError; exceptions of PyTorch (out of memory) pass through.
 #include <torch/csrc/Exceptions.h>

@@ -193,12 +193,12 @@ namespace {
 //
 // The constants are fitted to times of each tile on MI355X over 335 products of 1 to 131072
 // rows, 256 to 131072 columns and lengths of 16 to 32064 with 16-bit results; over those the
-// tile that they choose is 2.5% behind the fastest on average, and 32% at worst
+// tile that they choose is 2.3% behind the fastest on average, and 32% at worst
 // (33 x 16384 x 2056).  Each pays where it is chosen (us, it and the best of the others):
 // 256 x 256 at 1024 x 32003 x 2056 132 (163); 192 x 256 at 384 x 32003 x 1000 37 (41);
 // 256 x 128 at 777 x 8192 x 8192 104 (119); 128 x 128 at 2048 x 32003 x 128 41 (52);
-// 64 x 128 at 256 x 8192 x 4096 35 (41); 32 x 128 at 128 x 8192 x 512 6.2 (6.2); 16 x 128 at 1024 x 1000 x 64 4.5 (4.9); 16 x 64 at
-// 16 x 4096 x 8192 29 (43).
+// 64 x 128 at 256 x 8192 x 4096 35 (41); 16 x 128 at 16 x 131072 x 512 27 (29); 16 x 64 at
+// 16 x 4096 x 8192 29 (43).  (One of 32 x 128 was chosen more often than it paid.)
 double tile16_time(int index, uint64_t tiles, uint64_t k, int cu_count) {
   struct Time {
     int resident;
@@ -206,8 +206,8 @@ double tile16_time(int index, uint64_t tiles, uint64_t k, int cu_count) {
   };
   constexpr Time times[kTile16s] = {
       {1, 7.25f, 1.21f, 1.21f}, {1, 4.66f, 1.07f, 1.07f}, {1, 3.74f, 0.73f, 0.73f},
-      {2, 2.66f, 0.36f, 0.52f}, {2, 1.81f, 0.31f, 0.37f}, {2, 1.46f, 0.38f, 0.30f},
-      {2, 1.16f, 0.28f, 0.24f}, {3, 1.08f, 0.27f, 0.12f}};
+      {2, 2.66f, 0.36f, 0.52f}, {2, 1.81f, 0.31f, 0.37f}, {2, 1.16f, 0.28f, 0.24f},
+      {3, 1.08f, 0.27f, 0.12f}};
   const Time t = times[index];
   const uint64_t per_cu = ceil_div(tiles, uint64_t(cu_count));
   const double steps = double(ceil_div(k, uint64_t(kStepValues)));

@@ -19,15 +19,16 @@
 // (buffer_load ... lds) into rings of buffers, NS steps ahead of the one that is
 // multiplied.  The half of a step (32 values) that is multiplied next is read from LDS
 // under the products of the one before, so a step's buffers are free again in its middle;
-// there one operand's loads of the step NS on are sent, and the other's, whose ring has
-// one buffer more, already under the first half: loads are spread over the whole step.
+// there a's loads of the step NS on are sent, and b's, whose ring has one buffer more,
+// already under the first half: loads are spread over the whole step.
 // (256 x 256, both operands' loads in the second half of a step: 4096 x 32768 x 4096 806
 // us, 4096 x 4096 x 32768 763; spread 779 and 744; and with the two wavefronts of a SIMD
-// taking turns, TURNS, 763 and 715.)  LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand
-// tile keeps its piece c in slot c ^ swizzle(r), so that the 16 lanes of a 16-byte LDS
-// read, whose rows are 128 bytes apart, meet no bank twice.  The load writes LDS in
-// lane order, so the swizzle is made on the memory side: the lane that fills slot s of
-// row r fetches piece s ^ swizzle(r).
+// taking turns, TURNS, 763 and 715.)
+//
+// LDS rows are in operand order, 8 slots of 16 bytes; row r of an operand tile keeps its
+// piece c in slot c ^ swizzle(r), so that the 16 lanes of a 16-byte LDS read, whose rows are
+// 128 bytes apart, meet no bank twice.  The load writes LDS in lane order, so the swizzle is
+// made on the memory side: the lane that fills slot s of row r fetches piece s ^ swizzle(r).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -94,27 +95,24 @@ using Yes = Int<1>;
 using No = Int<0>;
 
 constexpr int kStepBytes = 128, kStepValues = 64;
-constexpr unsigned kGroupRows = 1024;   // tile_of
 
-// A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of an operand
-// have a buffer, and of one of the two (b with MORE_B) one step more, so that its loads
-// need not wait for the middle of a step.
+// A block makes BM x BN of the product with WM x WN wavefronts.  NS steps of a have a
+// buffer, and of b one step more, so that its loads need not wait for the middle of a step.
 // ACROSS: b's rows lie across the sum, so that its transpose is multiplied.
-template <int BM, int BN, int WM, int WN, int NS, bool MORE_B = true, bool TURNS = false,
-          bool ACROSS = false>
+template <int BM, int BN, int WM, int WN, int NS, bool TURNS = false, bool ACROSS = false>
 struct Tile16 {
-  typedef Tile16<BM, BN, WM, WN, NS, MORE_B, TURNS, true> Across;
+  typedef Tile16<BM, BN, WM, WN, NS, TURNS, true> Across;
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN, kNS = NS;
-  static constexpr bool kMoreB = MORE_B, kTurns = TURNS, kAcross = ACROSS;
+  static constexpr bool kTurns = TURNS, kAcross = ACROSS;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr unsigned kGroup = kGroupRows / BM;   // rows of tiles
+  static constexpr unsigned kGroup = BM < 128 ? 4 : 1024 / BM;   // tile_of
   static constexpr int kMT = BM / WM / 16;  // 16-row operand tiles per wavefront
   static constexpr int kNT = BN / WN / 16;
   static constexpr int kRows = kMT, kCols = 4 * kNT;   // a lane's part of the product
   static constexpr int kLoadsA = BM / 8 / kWaves;  // wavefront loads per step
   static constexpr int kLoadsB = BN / 8 / kWaves;
   static constexpr int kStageA = BM * kStepBytes, kStageB = BN * kStepBytes;
-  static constexpr int kNA = NS + (MORE_B ? 0 : 1), kNB = NS + (MORE_B ? 1 : 0);
+  static constexpr int kNA = NS, kNB = NS + 1;
   static constexpr int kLdsBytes = kNA * kStageA + kNB * kStageB;
   // wavefronts per SIMD that the LDS leaves room for, at most 2 (of 256 registers)
   static constexpr int kResident = 160 * 1024 / kLdsBytes * kWaves / 4;
@@ -126,7 +124,7 @@ struct Tile16 {
   static_assert(kMT <= 16, "operand tiles");
   static_assert(kNT == 4, "lane_column");
   static_assert(BN == 256 || BN == 128 || BN == 64, "across_swizzle");
-  static_assert(!TURNS || (kWaves == 8 && NS == 2 && MORE_B), "two wavefronts a SIMD, in turns");
+  static_assert(!TURNS || (kWaves == 8 && NS == 2), "two wavefronts a SIMD, in turns");
 };
 
 typedef __attribute__((address_space(3))) int8_t tile_lds_byte;
@@ -166,7 +164,8 @@ __device__ __forceinline__ uint64_t lds_read_across(uint32_t at) {
 template <class T>
 __device__ __forceinline__ uint32_t across_swizzle(uint32_t row) {
   const uint32_t third = (row >> 3) & 1;
-  if constexpr (T::kBN == 64) return (((row >> 1) & 1) | third << 1) << 1;   // two rows in 256 bytes
+  if constexpr (T::kBN == 64)   // two rows in 256 bytes
+    return (((row >> 1) & 1) | third << 1) << 1;
   return ((row & 3) | third << 2) << 1;
 }
 
@@ -178,10 +177,11 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Which tile a block makes: every XCD takes a contiguous range of ids, and ids run down
-// kGroup rows of tiles, 1024 of the product, before the next column, so that blocks running
-// at the same time on one XCD share operand rows in its L2.  (Us, 4 rows of tiles / 1024 rows
-// of any: 777 x 50001 x 2056 of 192 x 256 196 / 181, 131072 x 4096 x 256 of 128 x 128 459 /
-// 423; 768, 1536, 2048 and 4096 rows over the shapes where each tile is chosen are 1% slower
+// kGroup rows of tiles before the next column, so that blocks running at the same time on
+// one XCD share operand rows in its L2: 1024 rows of the product, or 4 of the small tiles.
+// (Us, 4 rows of tiles / 1024 rows: 777 x 50001 x 2056 of 192 x 256 196 / 181, 131072 x 4096
+// x 256 of 128 x 128 459 / 423, but logits and dz of 2046 x 1216 x 192, of 64 x 128, 9.3 /
+// 12.0; 768, 1536, 2048 and 4096 rows over the shapes where each tile is chosen are 1% slower
 // on average, 32768 x 4096 x 4096 of 256 x 256 727 with 1024 rows, 756 with 1536.)
 template <class T>
 __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned tiles_n,
@@ -195,8 +195,9 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned 
 
 // acc = the tile at (i0, j0) of a b^T over k values, rows and columns past the
 // matrices' undefined.  ACROSS: of a b over the rows of b, of which there are at least k
-// or that end where zeros are to be read, and whose columns are `across`.  `lds`: T::kLdsBytes, at a multiple of 1024, free again after a
-// barrier.  Every thread of the block takes part.
+// or that end where zeros are to be read, and whose columns are `across`.  `lds`:
+// T::kLdsBytes, at a multiple of 1024, free again after a barrier.  Every thread of the
+// block takes part.
 template <class T, int TYPE>
 __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16& mb, uint32_t k,
                                               uint64_t i0, uint64_t j0, int8_t* lds,
@@ -271,19 +272,6 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     }
   };
   constexpr int kLoads = T::kLoadsA + T::kLoadsB;
-  constexpr int kFirst = T::kMoreB ? T::kLoadsB : T::kLoadsA, kSecond = kLoads - kFirst;
-  auto send_first = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
-    if constexpr (T::kMoreB)
-      send_b(to, k0, x);
-    else
-      send_a(to, k0, x);
-  };
-  auto send_second = [&](uint32_t to, uint32_t k0, int x) ARMX_INLINE {
-    if constexpr (T::kMoreB)
-      send_a(to, k0, x);
-    else
-      send_b(to, k0, x);
-  };
   auto stage = [&](uint32_t t) ARMX_INLINE {
 #pragma unroll
     for (int x = 0; x < T::kLoadsA; ++x) send_a(ring_a + t * T::kStageA, t * kStepBytes, x);
@@ -497,24 +485,22 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
   };
   // A step but the last (its first half's operands already in registers): the second
   // half's are read while the first is multiplied, and with SEND the step NS on is sent
-  // for into the spare buffer of the ring that has one; then, after the barrier that ends
-  // all reading of this step's buffers and finds the next one's filled (all but `out`
-  // loads), into this one's of the other ring, while the next step's first half is read
-  // under the second half's products.
-  uint32_t spare = T::kMoreB ? ring_b + (T::kNB - 1) * T::kStageB
-                             : ring_a + (T::kNA - 1) * T::kStageA;
+  // for into b's spare buffer; then, after the barrier that ends all reading of this
+  // step's buffers and finds the next one's filled (all but `out` loads), into a's of this
+  // step, while the next step's first half is read under the second half's products.
+  uint32_t spare_b = ring_b + (T::kNB - 1) * T::kStageB;
   auto step = [&](auto send, auto out, uint32_t s) ARMX_INLINE {
     constexpr bool kSend = decltype(send)::value;
     const uint32_t k0 = (s + NS) * kStepBytes;
-    multiply_and_fetch(1, place(base_a, base_b, 1), Int<kSend ? kFirst : 0>{},
-                       [&](int x) ARMX_INLINE { send_first(spare, k0, x); });
+    multiply_and_fetch(1, place(base_a, base_b, 1), Int<kSend ? T::kLoadsB : 0>{},
+                       [&](int x) ARMX_INLINE { send_b(spare_b, k0, x); });
     sync(out);
     const uint32_t old_a = base_a, old_b = base_b;
     base_a = after_a(base_a);
     base_b = after_b(base_b);
-    spare = T::kMoreB ? old_b : old_a;
-    multiply_and_fetch(0, place(base_a, base_b, 0), Int<kSend ? kSecond : 0>{},
-                       [&](int x) ARMX_INLINE { send_second(T::kMoreB ? old_a : old_b, k0, x); });
+    spare_b = old_b;
+    multiply_and_fetch(0, place(base_a, base_b, 0), Int<kSend ? T::kLoadsA : 0>{},
+                       [&](int x) ARMX_INLINE { send_a(old_a, k0, x); });
   };
   uint32_t s = 0;
   if (steps >= NS) {
@@ -526,7 +512,7 @@ __device__ __forceinline__ void multiply_tile(const Matrix16& ma, const Matrix16
     sync(No{});
   }
   fetch_half(0);
-  for (; steps - s > NS; ++s) step(Yes{}, Int<(NS - 2) * kLoads + kFirst>{}, s);
+  for (; steps - s > NS; ++s) step(Yes{}, Int<(NS - 2) * kLoads + T::kLoadsB>{}, s);
   // the last steps; what is still out shrinks with them
   if constexpr (NS > 3)
     if (steps - s > 3) step(No{}, Int<2 * kLoads>{}, s), ++s;

@@ -8,15 +8,14 @@
 namespace armx {
 namespace {
 
-typedef Tile16<256, 256, 2, 4, 2, true, true> Tile0;
+typedef Tile16<256, 256, 2, 4, 2, true> Tile0;
 typedef Tile16<192, 256, 2, 4, 2> Tile1;
 typedef Tile16<256, 128, 4, 2, 3> Tile2;
 typedef Tile16<128, 128, 2, 2, 2> Tile3;
 typedef Tile16<64, 128, 2, 2, 2> Tile4;
-typedef Tile16<32, 128, 1, 2, 3> Tile5;
-typedef Tile16<16, 128, 1, 2, 3> Tile6;
-typedef Tile16<16, 64, 1, 1, 4> Tile7;
-constexpr int kTile16s = 8;
+typedef Tile16<16, 128, 1, 2, 3> Tile5;
+typedef Tile16<16, 64, 1, 1, 4> Tile6;
+constexpr int kTile16s = 7;
 constexpr uint64_t kLargestTile = 256;   // rows and columns
 
 // Calls CASE(T) for tile number `index`.
@@ -30,7 +29,6 @@ constexpr uint64_t kLargestTile = 256;   // rows and columns
       case 4: CASE(Tile4); break; \
       case 5: CASE(Tile5); break; \
       case 6: CASE(Tile6); break; \
-      case 7: CASE(Tile7); break; \
     }                             \
   } while (0)
 
