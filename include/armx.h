@@ -678,8 +678,9 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
  *   dx[r][c]      = sum over v of dz[r][v] * weight[v][c], rounded once to `type`
  *   dweight[v][c] = sum over r of dz[r][v] * x[r][c], rounded once to `dweight_type`.
  * A piece of the vocabulary at a time its z is made again and its dz kept as 16-bit
- * values in the workspace, scaled by rows so that neither binary16's range nor a row's
- * largest value costs accuracy; sums are in binary32.
+ * values in the workspace, scaled so that neither binary16's range nor a row's largest
+ * value costs accuracy; sums are in binary32.  (In binary16 a value counts to the next
+ * multiple of 2^-39 of the largest |dloss| for dweight, of 2^-38 of its row's for dx.)
  *
  * dloss    device, rows binary32 (the mean over rows: 1 / rows each, say, times a loss
  *          scale where 16-bit gradients need one).  What it holds for ignored rows
