@@ -9,8 +9,8 @@
 // 8 values, which hide under the loads of other wavefronts.)
 //
 // Mean and squared deviations are taken by a wavefront of its own part of the row
-// first: its mean m, then the sum q of (h - m)^2 and the sum e of h - m, which is what
-// m's rounding left, so that the part's mean is m + e / n and its squared deviations
+// first: its mean m (to 16 bits), then the sum q of (h - m)^2 and the sum e of h - m, which
+// is what m's rounding left, so that the part's mean is m + e / n and its squared deviations
 // q - e^2 / n.  Parts are joined by
 //   mean = sum n_w mean_w / n,   M = sum (M_w + n_w (mean_w - mean)^2),
 // sums of numbers of one sign, with one barrier a row.  Nothing cancels, whatever the
@@ -74,13 +74,28 @@ __device__ __forceinline__ u32x4 add8(u32x4 x, u32x4 r) {
   return narrow8<TYPE>(a);
 }
 
+// m to 16 significant bits, so that differences of 16-bit values from it are exact (from one
+// of 24 a row's round alike, and their sum is off by that many times the rounding).
+__device__ __forceinline__ float coarse(float m) {
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, m) + 0x80u) & 0xFFFFFF00u);
+}
+
+// The mean of a row.  Of one below a quarter of the deviations the values' own sum is the
+// more exact, of others what is made of the deviations.  (Off by, rms, rows of 4096 values
+// around 0: 1.7e-8 without either, now 4.4e-10, for 4% of the time of a norm of 16384 x 2048.)
+__device__ __forceinline__ float mean_of(float mean, float m2, float sum, uint32_t cols,
+                                         float inv_cols) {
+  const float n = float(cols), m = sum * inv_cols;
+  return m * m * (16.0f * n) < m2 ? __builtin_fmaf(__builtin_fmaf(-m, n, sum), inv_cols, m) : mean;
+}
+
 // Mean and sum of squared deviations of a row, in each of its threads.
 template <class L>
 struct Moments {
   static constexpr int kWaves = L::kTpr ? 1 : L::kMax / 64;
   static constexpr int kLevels = log2_of(L::kTpr ? L::kTpr : 64);
   struct Lds {
-    float mean[kWaves], m2[kWaves];
+    float mean[kWaves], m2[kWaves], sum[kWaves];
   };
   // values of wavefront `w`'s part of the row
   __device__ __forceinline__ static float part(uint32_t cols, int w) {
@@ -108,7 +123,8 @@ struct Moments {
     }
     // (m is near the mean and no more, so the quick reciprocal does)
     const float n = part(cols, wave), each = __builtin_amdgcn_rcpf(n);
-    const float m = lane_tree(s, kLevels) * each;
+    s = lane_tree(s, kLevels);
+    const float m = coarse(s * each);
     float q = 0.0f, e = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
@@ -141,13 +157,18 @@ struct Moments {
       if (lane_id() == 0) {
         l.mean[wave] = mean;
         l.m2[wave] = m2;
+        l.sum[wave] = s;
       }
       __syncthreads();
       const int waves = num_waves();
       const float first = l.mean[0];
       float off = 0.0f;
+      s = l.sum[0];
 #pragma unroll 4
-      for (int w = 1; w < waves; ++w) off = __builtin_fmaf(part(cols, w), l.mean[w] - first, off);
+      for (int w = 1; w < waves; ++w) {
+        off = __builtin_fmaf(part(cols, w), l.mean[w] - first, off);
+        s += l.sum[w];
+      }
       mean = first + off * inv_cols;
       m2 = 0.0f;
 #pragma unroll 4
@@ -156,6 +177,7 @@ struct Moments {
         m2 += __builtin_fmaf(part(cols, w) * d, d, l.m2[w]);
       }
     }
+    mean = mean_of(mean, m2, s, cols, inv_cols);
   }
 };
 
@@ -293,7 +315,7 @@ __global__ __launch_bounds__(1024) void layer_norm_loop_kernel(LayerNormArgs k) 
   const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
   const Dropper drop(k.dropout);
   for (uint64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
-    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
+    float n = 0.0f, mean = 0.0f, m2 = 0.0f, sum = 0.0f;
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
       const u32x4 h = load_sum_chunk<TYPE, IN>(k, drop, row, c);
       if (IN != kPlain && k.sum_out) store_chunk8<false>(k.sum_out + row * k.lds, c, cols, h);
@@ -312,15 +334,18 @@ __global__ __launch_bounds__(1024) void layer_norm_loop_kernel(LayerNormArgs k) 
       const float d = m - mean, all = n + float(in);
       m2 += __builtin_fmaf(d * d, n * (float(in) / all), q);
       mean = __builtin_fmaf(d, float(in) / all, mean);
+      sum += s;
       n = all;
     }
-    const float first = block_sum(n * mean, part[0]) * k.inv_cols;
+    sum = block_sum(sum, part[0]);
+    const float first = sum * k.inv_cols;
     const float d = mean - first;
     m2 = block_sum(__builtin_fmaf(n * d, d, m2), part[1]);
     // what the first mean's rounding left
     const float e = block_sum(n * d, part[2]);
     mean = first + e * k.inv_cols;
     m2 -= e * (e * k.inv_cols);
+    mean = mean_of(mean, m2, sum, cols, k.inv_cols);
     const float inv = inv_std_of(m2, k.inv_cols, k.eps);
     for (uint32_t c = threadIdx.x; c < chunks; c += 1024) {
       // from sum_out (where this thread wrote it), so that outputs may stand where

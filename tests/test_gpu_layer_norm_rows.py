@@ -136,6 +136,25 @@ def check_backward(got, dy, h, w, mean, inv, ds, drop, place=None):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("cols", [24, 100, 512, 1000, 4096, 5000, 16384, 40000])
+def test_means_beside_large_deviations(cols, dtype):
+    # values of one grid, whose every sum is exact in binary32, in pairs that cancel but for
+    # one: what is left is the division, within a unit of the mean
+    rng = np.random.default_rng(cols)
+    a = rng.integers(-120, 121, (50, cols // 2))
+    h = np.concatenate([a, -a, np.zeros((50, cols % 2), int)], 1)[:, rng.permutation(cols)]
+    h[:, 3] = 0
+    h[np.arange(50), 3] = np.arange(50) - 25 - (h.sum(1) - h[:, 3])
+    x = torch.zeros(50, -(-cols // 8) * 8, dtype=dtype, device="cuda")[:, :cols]
+    x.copy_(torch.from_numpy(h / 32.0))
+    assert np.array_equal(f64(x), h / 32.0)
+    w = torch.ones(cols, dtype=dtype, device="cuda")
+    got = f64(armx.layer_norm_rows(x, w, keep_stats=True).mean)
+    want = f64(x).sum(1) / cols
+    assert np.all(np.abs(got - want) <= 2 * U * np.abs(want)), np.abs(got - want).max()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (2, 64), (3, 8), (1000, 64), (4099, 136),
                                        (513, 2056), (300, 8192), (70000, 16), (33, 33000),
                                        (512, 1001), (513, 1024), (1024, 2049), (1025, 4100),
