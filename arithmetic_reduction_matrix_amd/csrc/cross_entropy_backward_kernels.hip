@@ -241,7 +241,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
   for (int i = 0; i < T::kMT; ++i) {
     const uint64_t row = row0 + i < x.rows ? row0 + i : x.rows - 1;
     row_scale[i] = rows[row];
-    row_lse[i] = lse[row] * kLog2E;
+    row_lse[i] = lse[row];
     row_at[i] = column_index(targets[row] - first - int64_t(col));
   }
   float each[T::kMT];
@@ -250,11 +250,11 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
     const RowScale s = row_scale[i];
     const float l = row_lse[i];
     each[i] = s.dloss * all;
-    // (the product's rounding, 2^-24 of lse, is far below the 16 bits to come)
+    // (the difference first, which is exact where p is near 1: a rounding of lse log2 e is
+    // 2^-24 of lse in p, which counts in the p - 1 of a row nearly sure of its target)
 #pragma unroll
     for (int c = 0; c < T::kCols; ++c)
-      z[i][c / 4][c % 4] =
-          __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][c / 4][c % 4], kLog2E, -l));
+      z[i][c / 4][c % 4] = exp_of(z[i][c / 4][c % 4] - l);
     // few wavefronts have a row's target among their columns, or an ignored row
     const uint32_t at = row_at[i];
     if (at < T::kCols) {
