@@ -9,7 +9,8 @@
 // dz is rounded to 16 bits twice, with a scale of its own each time:
 // - for dx, a row is divided by 1 - exp(z[target] - lse), its target's magnitude, which
 //   then is a whole power of two and is not rounded at all (it outweighs the others of
-//   its row together), and the row of dx is multiplied by it and by dloss in 32 bits;
+//   its row together), and the row of dx is multiplied by it and by dloss in 32 bits.  Of a
+//   row surer of its target than the roundings of its logits (least_rest) it is rounded;
 // - for dweight, by dloss over the largest |dloss|; of a few rows, whose roundings do
 //   not average out, the rest that the rounding leaves is a second 16-bit term
 //   (kTwoTerms), multiplied by the same row of x.
@@ -57,57 +58,106 @@ __device__ __forceinline__ float top_scale(uint32_t top_bits) {
   return top < 0x1p-105f ? 0x1p120f : kTopScale / top;
 }
 
-// Rows' scales, kRowsEach for each wavefront of block `block`.
-constexpr int kRowsEach = 4;
+// The least that a row's scale counts as 1 - p of its target, from sum |x w| over the target's
+// logit.  Where p is near 1, lse is about that logit, and what it is off by, d, moves all of
+// the row's p by a factor e^d: the others may then add up to e^d - p, above 1 - p by d.
+// Scaled by 2^14 / rest, four times below binary16's largest value, they stay in its range
+// while d is up to three times `rest`: 48 roundings of the magnitudes that were summed.  An
+// lse of cross_entropy_rows, made of the logits as they are here, is off by two, and another
+// sum in binary32 by fewer than that as well.  (Where p is below 2/3 no value of a row can
+// leave the range.)
+__device__ __forceinline__ float least_rest(float size) {
+  return __builtin_fminf(__builtin_fmaxf(size * 0x1p-20f, 0x1p-14f), 1.0f);
+}
+
+// Scales of 16 rows by block `block`.  Their targets' logits are the diagonal of 16 rows of x
+// times the targets' 16 rows of the weight, by the instructions of multiply_tile over the same
+// values in the same order (products of zeros past the rows left out), and so with the bits
+// that loss_grad_kernel's have: another sum of them may differ by more than the 1 - p that it
+// is to scale.  Beside it, by the same on magnitudes, what is summed.
+//
+// The wavefronts' loads are in flight together; then each multiplies its own in its turn and
+// hands the sum on (hand[0]).  Magnitudes are summed by each wavefront apart.  (16 rows by one
+// wavefront: gradients of 515 x 32003 x 1000 6 us more, of 8 x 32768 x 4096 6.5.)
+constexpr int kScaleRows = 16;
 template <int TYPE>
 __device__ __forceinline__ void scale_rows(const CrossEntropyArgs& k, const float* dloss,
-                                           const float* lse, RowScale* rows, uint64_t block) {
-  const uint32_t cols = uint32_t(k.cols), chunks = (cols + 7) / 8;
-#pragma unroll 1
-  for (int i = 0; i < kRowsEach; ++i) {
-    const uint64_t row = (block * 4 + wave_id()) * kRowsEach + i;
-    if (row >= k.rows) break;
-    const uint64_t bits = uint64_t(k.targets[row]);   // the same in all lanes
-    const int64_t t = int64_t(
-        uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(bits >> 32)))) << 32 |
-        uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(bits)))));
-    RowScale s = {0.0f, 0.0f, 0.0f, 1u};
-    if (t != k.ignore) {
-      s.skip = 0;
-      s.dloss = dloss[row];
-      if (t >= 0 && t < int64_t(k.vocab)) {
-        const RowWords xr(k.x + row * k.ldx, cols), wr(k.weight + uint64_t(t) * k.ldw, cols);
-        float z = 0.0f;
-        for (uint32_t c = lane_id(); c < chunks; c += 256) {
-          u32x4 a[4], b[4];
+                                           const float* lse, RowScale* rows, uint64_t block,
+                                           floatx4 (*hand)[64]) {
+  constexpr uint32_t kHalf = kStepValues / 2;   // a product's values of k
+  constexpr uint32_t kFlight = 8, kWaves = 4;
+  const uint64_t row0 = block * kScaleRows;
+  const uint32_t lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
+  const uint64_t row = row0 + r < k.rows ? row0 + r : k.rows - 1;
+  const int64_t t = k.targets[row];
+  const bool in = t >= 0 && t < int64_t(k.vocab);
+  const uint16_t* xr = k.x + row * k.ldx;
+  const uint16_t* wr = k.weight + uint64_t(in ? t : 0) * k.ldw;
+  const uint32_t cols = uint32_t(k.cols), full = cols / kHalf, all = (cols + kHalf - 1) / kHalf;
+  u32x4 a[kFlight], b[kFlight], cut_a, cut_b;   // (the last product's, cut)
+  auto load = [&](uint32_t first) ARMX_INLINE {
+    if (full) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[j] = xr.load(c + 64 * j);   // zeros past the row
-            b[j] = wr.load(c + 64 * j);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[8], g[8];
-            widen8<TYPE>(a[j], f);
-            widen8<TYPE>(b[j], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              z = (c + 64 * j) * 8 + e < cols ? __builtin_fmaf(f[e], g[e], z) : z;
-          }
-        }
-        z = lane_tree_full(z);
-        // (one that is nearly sure of its target keeps a scale that the logit's own
-        // rounding does not turn over)
-        const float rest = __builtin_fmaxf(1.0f - exp_of(z - lse[row]), 0x1p-14f);
-        s.scale = kRowScale / rest;
-        // (an infinite dloss makes infinities of both signs in dz, whose sums are NaNs)
-        s.back = s.dloss - s.dloss == 0.0f ? s.dloss * (rest / kRowScale) : __builtin_nanf("");
-      } else {
-        s.scale = s.dloss = s.back = __builtin_nanf("");
+      for (uint32_t i = 0; i < kFlight; ++i) {
+        const uint32_t h = first + i < full ? first + i : full - 1;
+        a[i] = *reinterpret_cast<const u32x4*>(xr + h * kHalf + 8 * g);
+        b[i] = *reinterpret_cast<const u32x4*>(wr + h * kHalf + 8 * g);
       }
     }
-    if (lane_id() == 0) rows[row] = s;
+  };
+  floatx4 size = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add_size = [&](u32x4 x, u32x4 w) ARMX_INLINE {
+    size = mfma16<TYPE>(w & 0x7FFF7FFFu, x & 0x7FFF7FFFu, size);
+  };
+  load(wave * kFlight);
+  for (uint32_t h0 = 0; h0 < all; h0 += kWaves * kFlight) {
+    const uint32_t first = h0 + wave * kFlight;
+    const bool cut = full < all && first <= full && full - first < kFlight;
+    if (cut) {
+      cut_a = load8_masked(xr, full * kHalf + 8 * g, cols, 0);
+      cut_b = load8_masked(wr, full * kHalf + 8 * g, cols, 0);
+      add_size(cut_a, cut_b);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kFlight; ++i)
+      if (first + i < full) add_size(a[i], b[i]);
+    for (uint32_t w = 0; w < kWaves && h0 + w * kFlight < all; ++w) {
+      if (wave == w) {
+        floatx4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (first) z = hand[0][lane];
+#pragma unroll
+        for (uint32_t i = 0; i < kFlight; ++i)
+          if (first + i < full) z = mfma16<TYPE>(b[i], a[i], z);
+        if (cut) z = mfma16<TYPE>(cut_b, cut_a, z);
+        hand[0][lane] = z;
+        if (first + kWaves * kFlight < all) load(first + kWaves * kFlight);
+      }
+      __syncthreads();
+    }
   }
+  hand[1 + wave][lane] = size;
+  __syncthreads();
+  // row r's is with lane r of 16 number r / 4, value r % 4
+  if (wave != 0 || g != r / 4 || row0 + r >= k.rows) return;
+  auto mine = [&](int i) ARMX_INLINE {
+    return reinterpret_cast<const float*>(&hand[i][lane])[r % 4];
+  };
+  RowScale s = {0.0f, 0.0f, 0.0f, 1u};
+  if (t != k.ignore) {
+    s.skip = 0;
+    s.dloss = dloss[row];
+    if (in) {
+      const float left = __builtin_fabsf(1.0f - exp_of(mine(0) - lse[row]));
+      const float least = least_rest((mine(1) + mine(2)) + (mine(3) + mine(4)));
+      const float rest = __builtin_fmaxf(left, least);
+      s.scale = kRowScale / rest;
+      // (an infinite dloss makes infinities of both signs in dz, whose sums are NaNs)
+      s.back = s.dloss - s.dloss == 0.0f ? s.dloss * (rest / kRowScale) : __builtin_nanf("");
+    } else {
+      s.scale = s.dloss = s.back = __builtin_nanf("");
+    }
+  }
+  rows[row] = s;
 }
 
 // The largest |dloss| of rows that count (its bits, NaNs largest), by one block: 8 rows a
@@ -202,9 +252,9 @@ __global__ __launch_bounds__(256) void loss_prepare_kernel(CrossEntropyArgs k, c
                                                            const float* lse, RowScale* rows,
                                                            uint32_t* top, uint16_t* xt,
                                                            uint64_t ldt, unsigned scales) {
-  __shared__ uint32_t tile[64][33];
+  __shared__ __attribute__((aligned(16))) uint32_t tile[64][33];
   if (blockIdx.x < scales) {
-    scale_rows<TYPE>(k, dloss, lse, rows, blockIdx.x);
+    scale_rows<TYPE>(k, dloss, lse, rows, blockIdx.x, reinterpret_cast<floatx4(*)[64]>(tile));
   } else if (blockIdx.x == scales) {
     top_of_rows(k, dloss, top, tile[0]);
   } else {
@@ -545,7 +595,7 @@ hipError_t launch_grads(const CrossEntropyArgs& a, const CrossEntropyGradPlan& p
   const float *dloss = grads.dloss, *lse = grads.lse;
   hipError_t e;
   {
-    unsigned scales = unsigned(ceil_div(a.rows, 4 * kRowsEach));
+    unsigned scales = unsigned(ceil_div(a.rows, kScaleRows));
     uint64_t blocks = scales, ldt = plan.ldt;
     if (dzt) {
       const uint64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);

@@ -680,7 +680,9 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
  * A piece of the vocabulary at a time its z is made again and its dz kept as 16-bit
  * values in the workspace, scaled so that neither binary16's range nor a row's largest
  * value costs accuracy; sums are in binary32.  (In binary16 a value counts to the next
- * multiple of 2^-39 of the largest |dloss| for dweight, of 2^-38 of its row's for dx.)
+ * multiple of 2^-39 of the largest |dloss| for dweight, and for dx of 2^-38 of |dloss[r]|
+ * times 1 - p of the row's target, which counts as no less than 2^-14 and 2^-20 of the sum
+ * of |x * weight| over the target's logit.)
  *
  * dloss    device, rows binary32 (the mean over rows: 1 / rows each, say, times a loss
  *          scale where 16-bit gradients need one).  What it holds for ignored rows

@@ -84,3 +84,13 @@ def cross_entropy_backward(dloss, x, w, targets, lse, ignore=-100):
     dz[rows, t[rows]] -= 1.0
     dz = np.where(live[:, None], dz * np.where(live, dloss, 0.0)[:, None], 0.0)
     return dz @ w, dz.T @ x, dz
+
+
+def row_scale(z, size, lse):
+    """What a row of exp(z - lse) - onehot(target) is multiplied by before binary16 holds
+    it, in binary32: z and lse as the kernel has them, size = sum |x w| of the target's
+    logit."""
+    z, size, lse = (np.float32(v) for v in (z, size, lse))
+    least = np.minimum(np.maximum(size * np.float32(2.0 ** -20), np.float32(2.0 ** -14)), np.float32(1))
+    rest = np.maximum(np.abs(np.float32(1) - np.exp(z - lse, dtype=np.float32)), least)
+    return np.float32(2.0 ** 14) / rest

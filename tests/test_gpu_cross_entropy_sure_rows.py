@@ -1,5 +1,6 @@
-"""cross_entropy_rows_backward on rows that are nearly sure of their target: probabilities
-beside a large log of the sum of exponentials."""
+"""cross_entropy_rows_backward on rows that are nearly sure of their target: large logits
+whose sums cancel, where 1 - p is close to what the logits' own rounding leaves, and
+probabilities beside a large log of the sum of exponentials."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +9,7 @@ import arithmetic_reduction_matrix_amd as armx
 
 from _layer import FLOOR, HALF, TYPES, U, f64, ids
 from _parity import require_gpu
+from test_gpu_cross_entropy import check_grads, check_loss
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +25,54 @@ def put(values, dtype):
     m = torch.empty(rows, -(-cols // 8) * 8, dtype=dtype, device="cuda")[:, :cols]
     m.copy_(torch.from_numpy(values))
     return m
+
+
+def nearly_sure(rng, cols, logit, dtype, rows=120):
+    """Row r's target is word 2 r, and word 2 r + 1 is the only other one near it: half the
+    rows have 1 - p from 1e-5 to 1e-2, the others from 2.4e-4 to 4e-4.  What the words
+    have beside the row's own direction cancels in its logits, and is many times them."""
+    x = rng.standard_normal((rows, cols))
+    along = x / (x * x).sum(1, keepdims=True)
+    noise = rng.standard_normal((rows, cols)) * logit / (6.25 * cols ** 0.5)
+    noise -= (noise * x).sum(1, keepdims=True) * along
+    rest = np.where(np.arange(rows) % 2, 10.0 ** rng.uniform(-5, -2, rows),
+                    rng.uniform(2.4e-4, 4e-4, rows))
+    w = np.empty((2 * rows, cols))
+    w[::2] = noise + logit * along
+    w[1::2] = w[::2] + np.log(rest / (1 - rest))[:, None] * along
+    return put(x, dtype), put(w, dtype), torch.arange(0, 2 * rows, 2, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("cols", [1001, 4096, 8192])
+@pytest.mark.parametrize("logit", [100, 400, 1000, 4000])
+def test_large_logits_of_rows_nearly_sure(logit, cols, dtype):
+    rng = np.random.default_rng(logit + cols)
+    x, w, t = nearly_sure(rng, cols, logit, dtype)
+    rows, vocab = x.shape[0], w.shape[0]
+    got = armx.cross_entropy_rows(x, w, t)
+    check_loss(got, x, w, t)
+    # (a loss scale of 1024, so that binary16's results keep their bits)
+    dloss = torch.from_numpy(rng.uniform(512, 1536, rows).astype(np.float32)).cuda()
+    g = armx.cross_entropy_rows_backward(dloss, x, w, t, got.lse, dweight_dtype=torch.float32)
+    assert torch.isfinite(g.dx).all() and torch.isfinite(g.dweight).all()
+    check_grads(g, dloss, x, w, t, got.lse)
+    # Both gradients are made of the same dz, which dweight (two terms up to 128 rows)
+    # shows: word v's row of it is dz[r][v] x[r] of its one row r, as every other word is
+    # 0.3 logits and more behind.  dx has a rounding of each of its two dz, floors at the
+    # smallest step of what is scaled to 2^14 over at most 1, and its own rounding.
+    xs, ws, dw = f64(x), f64(w), f64(g.dweight)
+    half, floor, ag = HALF[dtype], FLOOR[dtype], f64(dloss)[:, None]
+    mine = np.repeat(xs, 2, 0)
+    dz = ((dw * mine).sum(1) / (mine * mine).sum(1)).reshape(rows, 2)
+    want = dz[:, :1] * ws[::2] + dz[:, 1:] * ws[1::2]
+    size = np.abs(dz[:, :1] * ws[::2]) + np.abs(dz[:, 1:] * ws[1::2])
+    floors = floor * ag.max() * (2.0 ** -14 + 2.0 ** -15)
+    far = ag * vocab * np.exp(-0.2 * logit)
+    tol = size * (half + half ** 2 + (2 * (vocab + 40) + 30) * U) + (floors + far) * (
+        np.abs(ws).sum(0) + np.abs(ws).max())
+    bad = ~(np.abs(f64(g.dx) - want) <= (tol + half * (np.abs(want) + tol)) * 1.02 + floor)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], f64(g.dx)[bad][:4], want[bad][:4])
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
