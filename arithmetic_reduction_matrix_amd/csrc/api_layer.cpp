@@ -164,13 +164,35 @@ int check_space(const void* ws, size_t got, size_t need) {
   return got < need ? ARMX_ERR_WORKSPACE : ARMX_OK;
 }
 
-void log_loss(const char* entry, const armx::CrossEntropyArgs& a, size_t ws, int cu_count) {
+void log_loss(const armx::CrossEntropyArgs& a, size_t ws, int cu_count) {
   if (!log_enabled()) return;
   const armx::Tile16Size t = armx::tile16_size(
       armx::choose_tile16(a.rows, a.vocab, a.cols, cu_count));
-  std::fprintf(stderr, "armx: %s rows=%llu vocab=%llu cols=%llu type=%d tile=%dx%d ws=%zu\n", entry,
+  std::fprintf(stderr,
+               "armx: cross_entropy_rows rows=%llu vocab=%llu cols=%llu type=%d tile=%dx%d "
+               "ws=%zu\n",
                (unsigned long long)a.rows, (unsigned long long)a.vocab,
                (unsigned long long)a.cols, a.type, t.bm, t.bn, ws);
+}
+
+// The tiles of a first piece's products (a last one that is shorter may take others for its
+// logits and dweight); dx's and dweight's are as they would be where one is not wanted.
+void log_loss_backward(const armx::CrossEntropyArgs& a, const armx::CrossEntropyGradPlan& plan,
+                       int cu_count) {
+  if (!log_enabled()) return;
+  const uint64_t count = a.vocab < plan.piece ? a.vocab : plan.piece;
+  const armx::Tile16Size z = armx::tile16_size(
+      armx::choose_tile16(a.rows, count, a.cols, cu_count));
+  const armx::Tile16Size dx = armx::tile16_size(plan.dx_tile);
+  const armx::Tile16Size dw = armx::tile16_size(
+      armx::choose_tile16(count, a.cols, a.rows * plan.terms, cu_count));
+  std::fprintf(stderr,
+               "armx: cross_entropy_rows_backward rows=%llu vocab=%llu cols=%llu type=%d "
+               "piece=%llu logits=%dx%d dx=%dx%d parts=%llu dweight=%dx%d terms=%llu ws=%zu\n",
+               (unsigned long long)a.rows, (unsigned long long)a.vocab,
+               (unsigned long long)a.cols, a.type, (unsigned long long)plan.piece, z.bm, z.bn,
+               dx.bm, dx.bn, (unsigned long long)plan.splits, dw.bm, dw.bn,
+               (unsigned long long)plan.terms, plan.ws_bytes);
 }
 
 }  // namespace
@@ -436,7 +458,7 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
   if (st != ARMX_OK) return st;
   if (loss == lse) return ARMX_ERR_CONFIG;
   const int cus = armx::current_cu_count();
-  log_loss("cross_entropy_rows", a, plan.ws_bytes, cus);
+  log_loss(a, plan.ws_bytes, cus);
   return hip_status(armx::launch_cross_entropy(a, plan, loss, lse, ws, cus, cfg,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -476,7 +498,7 @@ int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
   st = check_space(ws, ws_bytes, plan.ws_bytes);
   if (st != ARMX_OK) return st;
   if (dx == dweight) return ARMX_ERR_CONFIG;
-  log_loss("cross_entropy_rows_backward", a, plan.ws_bytes, cus);
+  log_loss_backward(a, plan, cus);
   return hip_status(armx::launch_cross_entropy_backward(a, plan, g, ws, cus, cfg, s));
 }
 
