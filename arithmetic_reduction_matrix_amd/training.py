@@ -179,7 +179,9 @@ def cross_entropy_rows_backward(dloss: torch.Tensor, x: torch.Tensor, weight: to
     """Gradients of ``cross_entropy_rows``: ``dloss`` (float32) is the gradient of every
     row's loss, ``lse`` as it returned them.  Returns dx (of x's type; ``out`` receives
     it) and dweight (x's type, or float32 by ``dweight_dtype`` or by ``dweight``), each
-    None if not wanted.  The logits are made again, a piece of the vocabulary at a time;
+    None if not wanted.  The logits are made again, a piece of the vocabulary at a time, and
+    their gradients enter both products as values of x's type: of more than 128 rows, a row
+    of dweight that one token alone makes has the accuracy of that type, as float32 too;
     without ``workspace`` one is taken from the allocator for this call (about 0.7 GB of
     pieces and transposes at 4096 rows of 4096 values)."""
     code = None if dweight_dtype is None else _TYPES.get(dweight_dtype, 3)

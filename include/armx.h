@@ -678,11 +678,16 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
  *   dx[r][c]      = sum over v of dz[r][v] * weight[v][c], rounded once to `type`
  *   dweight[v][c] = sum over r of dz[r][v] * x[r][c], rounded once to `dweight_type`.
  * A piece of the vocabulary at a time its z is made again and its dz kept as 16-bit
- * values in the workspace, scaled so that neither binary16's range nor a row's largest
- * value costs accuracy; sums are in binary32.  (In binary16 a value counts to the next
- * multiple of 2^-39 of the largest |dloss| for dweight, and for dx of 2^-38 of |dloss[r]|
- * times 1 - p of the row's target, which counts as no less than 2^-14 and 2^-20 of the sum
- * of |x * weight| over the target's logit.)
+ * values of `type` in the workspace, scaled so that binary16's range costs nothing; sums are
+ * in binary32.  So a value of dz counts with an error of up to half a step of `type` (2^-11
+ * of it in binary16, 2^-8 in bfloat16), except for dx its row's target's, which is exact as
+ * far as the logits are, and for dweight, where rows <= 128, all of them (two terms: 2^-22 and
+ * 2^-16).  Over the words of a row and the rows of a frequent word these errors average out.
+ * The row of dweight of a word that matters to one row of x only has that row's in full,
+ * whatever `dweight_type`: ARMX_F32 spares the last rounding and no other.  (In binary16 a
+ * value counts to the next multiple of 2^-39 of the largest |dloss| for dweight, and for dx of
+ * 2^-38 of |dloss[r]| times 1 - p of the row's target, which counts as no less than 2^-14 and
+ * 2^-20 of the sum of |x * weight| over the target's logit.)
  *
  * dloss    device, rows binary32 (the mean over rows: 1 / rows each, say, times a loss
  *          scale where 16-bit gradients need one).  What it holds for ignored rows

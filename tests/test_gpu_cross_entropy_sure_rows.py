@@ -110,3 +110,37 @@ def test_probabilities_beside_a_large_lse(dtype):
     tol = tol + 1e-14 * np.abs(w).sum(0)
     off = np.abs(f64(g.dx) - want)
     assert np.all(off <= (tol + half * (np.abs(want) + tol)) * 1.02 + floor)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows", [100, 128, 129, 4096])
+def test_a_word_of_one_token(rows, dtype):
+    # Its row of dweight is one value of dz times that token's x, and no other rounding
+    # averages with its own: half a step of the 16-bit type on either side of 128 rows, and
+    # up to them two terms' square of it.
+    rng = np.random.default_rng(rows)
+    vocab, cols, token = 500, 64, rows // 3
+    x = rng.integers(-3, 4, (rows, cols)) / 4   # logits that are exact
+    w = rng.integers(-1, 2, (vocab, cols)) / 4
+    x[:, 0] = 3
+    x[token, 0] = -0.75
+    w[vocab - 1] = 0
+    w[vocab - 1, 0] = -8        # 24 behind for the others, 6 before for its token
+    t = rng.integers(0, vocab - 1, rows)
+    t[token] = vocab - 1
+    xd, wd, td = put(x, dtype), put(w, dtype), torch.from_numpy(t).cuda()
+    lse = armx.cross_entropy_rows(xd, wd, td).lse
+    dloss = torch.from_numpy(rng.uniform(0.5, 1.5, rows).astype(np.float32)).cuda()
+    g = armx.cross_entropy_rows_backward(dloss, xd, wd, td, lse, dweight_dtype=torch.float32)
+    d = x @ w[vocab - 1] - f64(lse)
+    p = np.exp(d)
+    dz = (p - (np.arange(rows) == token)) * f64(dloss)
+    assert np.abs(np.delete(dz, token)).max() < 1e-6 * abs(dz[token])
+    want = dz @ x
+    e_p = (p * U * (3 * np.abs(d) + 4)) * f64(dloss) + FLOOR[dtype] * 1.5 * 2.0 ** -15
+    size = np.abs(dz) @ np.abs(x)
+    rest = e_p @ np.abs(x) + (2 * (2 * rows + 40) + 4) * U * size
+    err = np.abs(f64(g.dweight)[vocab - 1] - want)
+    assert np.all(err <= (HALF[dtype] * size + rest) * 1.02)
+    if rows <= 128:
+        assert np.all(err <= (HALF[dtype] ** 2 * size + rest) * 1.02)
