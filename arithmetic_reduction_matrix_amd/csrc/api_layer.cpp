@@ -123,7 +123,7 @@ int check_dropout(const armx_dropout* d, uint64_t rows, armx::DropoutArgs* out) 
 
 // Sizes of the cross entropy: 32-bit offsets in a tile's rows, and grids.
 constexpr uint64_t kMaxLossRows = uint64_t(1) << 21, kMaxLossCols = uint64_t(1) << 21;
-constexpr uint64_t kMaxLossVocab = uint64_t(1) << 28, kMaxLossLd = uint64_t(1) << 22;
+constexpr uint64_t kMaxLossVocab = uint64_t(1) << 28;
 
 int check_loss_sizes(uint64_t rows, uint64_t vocab, uint64_t cols, bool backward) {
   if (rows > kMaxLossRows || vocab > kMaxLossVocab || cols > kMaxLossCols) return ARMX_ERR_SHAPE;
@@ -144,7 +144,8 @@ int check_loss(const void* x, size_t ldx, const void* weight, size_t ldw, const 
        check_matrix(x, rows, cols, ldx, 16, 8),
        rows ? check_matrix(weight, vocab, cols, ldw, 16, 8) : ARMX_OK});
   if (st != ARMX_OK || rows == 0) return st;
-  if ((rows > 1 && ldx > kMaxLossLd) || (vocab > 1 && ldw > kMaxLossLd)) return ARMX_ERR_SHAPE;
+  if ((rows > 1 && ldx > armx::kMaxTileLd) || (vocab > 1 && ldw > armx::kMaxTileLd))
+    return ARMX_ERR_SHAPE;
   if (!targets) return ARMX_ERR_NULL;
   if (!aligned(targets, 8)) return ARMX_ERR_ALIGN;
   a->x = static_cast<const uint16_t*>(x);
@@ -495,6 +496,7 @@ int cross_entropy_rows_backward(const float* dloss, const void* x, size_t ldx,
   const int cus = armx::current_cu_count();
   const armx::CrossEntropyGradPlan plan =
       armx::plan_cross_entropy_backward(rows, vocab, cols, dx != nullptr, dweight != nullptr, cus);
+  if (plan.ws_bytes == size_t(-1)) return ARMX_ERR_SHAPE;
   st = check_space(ws, ws_bytes, plan.ws_bytes);
   if (st != ARMX_OK) return st;
   if (dx == dweight) return ARMX_ERR_CONFIG;

@@ -21,6 +21,17 @@ struct CrossEntropyArgs {
   int type = ARMX_F16;
 };
 
+// The products reach a tile's rows, at most 256 of them, by 32-bit byte offsets from its
+// first: those of x and of the weight by a limit on their pitches, those made in the
+// workspace by their plan (tile_reaches).
+constexpr uint64_t kMaxTileLd = uint64_t(1) << 22, kMostTileRows = 256;
+constexpr bool tile_reaches(uint64_t rows, uint64_t ld, uint64_t k) {
+  // (whole steps of 64 values, 2 bytes each)
+  return ((rows < kMostTileRows ? rows : kMostTileRows) - 1) * ld * 2 + (k + 63) / 64 * 128 <=
+         0xFFFFFFF0u;
+}
+static_assert(tile_reaches(kMostTileRows, kMaxTileLd, kMaxTileLd), "pitches of x and the weight");
+
 // The sums of a tile's 64 columns, a piece, stand apart until they are joined in order.
 constexpr uint64_t kLossPiece = 64;
 
@@ -40,7 +51,7 @@ struct CrossEntropyGradPlan {
   uint64_t ldd = 0;       // floats between rows of those products
   // byte offsets in the workspace
   size_t top = 0, rows = 0, dz = 0, dzt = 0, xt = 0, dx = 0;
-  size_t ws_bytes = 0;
+  size_t ws_bytes = 0;   // size_t(-1): sizes that the products do not reach
 };
 
 CrossEntropyPlan plan_cross_entropy(uint64_t rows, uint64_t vocab);

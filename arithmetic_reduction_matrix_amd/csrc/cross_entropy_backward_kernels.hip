@@ -708,6 +708,13 @@ CrossEntropyGradPlan plan_cross_entropy_backward(uint64_t rows, uint64_t vocab, 
   p.terms = rows <= kTwoTerms ? 2 : 1;
   // with one term a tile's rows past the last are written too
   p.ldt = round_up(p.terms == 2 ? 2 * rows : rows + kRoom - 1, kStepValues) + kStepValues;
+  // (rows * piece is at most 2^27 values or a piece kLeastPiece, and ldt little more than the
+  // rows: all sizes that the calls take hold this, which their products rest on)
+  if (!tile_reaches(rows, p.ldz, p.piece) || !tile_reaches(p.piece, p.ldt, rows * p.terms) ||
+      !tile_reaches(cols, p.ldt, rows * p.terms)) {
+    p.ws_bytes = size_t(-1);
+    return p;
+  }
   p.ldd = round_up(cols, kRoom);
   // Of few tiles, parts of the piece in blocks of their own: tile and parts are chosen
   // together.  (Parts up to a block of 128 x 128 for every compute unit, and their tile after

@@ -56,9 +56,8 @@ __device__ __forceinline__ floatx4 mfma16(u32x4 x, u32x4 y, floatx4 acc) {
                                                    __builtin_bit_cast(bf16x8, y), acc, 0, 0, 0);
 }
 
-// A matrix of 16-bit values, `k` of each row counting.  `ld` (values, a multiple of 8)
-// is at most kMaxTileLd, so that a tile's rows are reached by 32-bit offsets.
-constexpr uint64_t kMaxTileLd = uint64_t(1) << 22;
+// A matrix of 16-bit values, `k` of each row counting.  `ld` (values, a multiple of 8) lets
+// a tile's rows be reached by 32-bit byte offsets (tile_reaches of cross_entropy.h).
 struct Matrix16 {
   const uint16_t* p;
   uint64_t rows, ld;
