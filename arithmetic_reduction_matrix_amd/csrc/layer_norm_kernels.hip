@@ -9,7 +9,7 @@
 // 8 values, which hide under the loads of other wavefronts.)
 //
 // Mean and squared deviations are taken by a wavefront of its own part of the row
-// first: its mean m (to 16 bits), then the sum q of (h - m)^2 and the sum e of h - m, which
+// first: its mean m (to 16 bits: coarse), then the sum q of (h - m)^2 and the sum e of h - m, which
 // is what m's rounding left, so that the part's mean is m + e / n and its squared deviations
 // q - e^2 / n.  Parts are joined by
 //   mean = sum n_w mean_w / n,   M = sum (M_w + n_w (mean_w - mean)^2),
@@ -74,15 +74,18 @@ __device__ __forceinline__ u32x4 add8(u32x4 x, u32x4 r) {
   return narrow8<TYPE>(a);
 }
 
-// m to 16 significant bits, so that differences of 16-bit values from it are exact (from one
-// of 24 a row's round alike, and their sum is off by that many times the rounding).
+// m to 16 significant bits: a 16-bit value's difference from it is exact unless the value is
+// more than 2^8 times m, or less than 2^-13 of it, where it is rounded (from an m of 24 bits
+// most are, a row's alike, and their sum is off by that many times the rounding).
 __device__ __forceinline__ float coarse(float m) {
   return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, m) + 0x80u) & 0xFFFFFF00u);
 }
 
-// The mean of a row.  Of one below a quarter of the deviations the values' own sum is the
-// more exact, of others what is made of the deviations.  (Off by, rms, rows of 4096 values
-// around 0: 1.7e-8 without either, now 4.4e-10, for 4% of the time of a norm of 16384 x 2048.)
+// The mean of a row.  Of one below a quarter of the deviations, many of whose differences are
+// rounded, the values' own sum is the more exact, of others what is made of the deviations.
+// (Off by, rms, rows of 4096 values around 0: 1.7e-8 without either, now 4.4e-10, for 4% of the
+// time of a norm of 16384 x 2048.  The squared deviations take each difference's rounding as
+// it comes, 2^-24 of it.)
 __device__ __forceinline__ float mean_of(float mean, float m2, float sum, uint32_t cols,
                                          float inv_cols) {
   const float n = float(cols), m = sum * inv_cols;
