@@ -193,12 +193,13 @@ namespace {
 //
 // The constants are fitted to times of each tile on MI355X over 335 products of 1 to 131072
 // rows, 256 to 131072 columns and lengths of 16 to 32064 with 16-bit results; over those the
-// tile that they choose is 2.3% behind the fastest on average, and 32% at worst
-// (33 x 16384 x 2056).  Each pays where it is chosen (us, it and the best of the others):
-// 256 x 256 at 1024 x 32003 x 2056 132 (163); 192 x 256 at 384 x 32003 x 1000 37 (41);
-// 256 x 128 at 777 x 8192 x 8192 104 (119); 128 x 128 at 2048 x 32003 x 128 41 (52);
-// 64 x 128 at 256 x 8192 x 4096 35 (41); 16 x 128 at 16 x 131072 x 512 27 (29); 16 x 64 at
-// 16 x 4096 x 8192 29 (43).  (One of 32 x 128 was chosen more often than it paid.)
+// tile that they choose is 2.3% behind the fastest on average, more than 20% at 7 and 30% at
+// worst (8192 x 1000 x 384).  Each pays where it is chosen (us, it and the best of the
+// others): 256 x 256 at 1024 x 32003 x 2056 130 (166); 192 x 256 at 384 x 32003 x 1000 35 (38);
+// 256 x 128 at 777 x 8192 x 8192 105 (122); 128 x 128 at 2048 x 32003 x 128 34 (42); 64 x 128
+// at 256 x 8192 x 4096 35 (41); 16 x 128 at 1000 x 1000 x 32 4.1 (4.3), and its times at larger
+// ones are those of the best (16 x 131072 x 512 27 (27)); 16 x 64 at 16 x 4096 x 8192 29 (43).
+// (One of 32 x 128 was chosen more often than it paid.)
 double tile16_time(int index, uint64_t tiles, uint64_t k, int cu_count) {
   struct Time {
     int resident;
