@@ -18,10 +18,10 @@
 //   in full.
 // Powers of two keep both in binary16's range: 2^14 for dx, 2^15 for dweight.
 //
-// Of 4096 x 131072 x 4096 bf16 (9.6 ms) a piece of 32768 takes 840 us for logits and dz,
-// whose second copy is 2% of them, 805 for dx and 767 for dweight, where a library's products
-// alone take 740, 680 and 718: the matrix units are busy in 69, 73 and 78% of cycles, at a
-// clock of 1.7 to 1.8 GHz.  Pieces of 2^24 to 2^28 values take the same time.
+// Of 4096 x 131072 x 4096 bf16 (9.4 to 9.9 ms by card) a piece of 32768 takes 833 us for logits
+// and dz, whose second copy is 2% of them, 794 for dx and 760 for dweight, where a library's
+// products alone take 740, 680 and 718 with operands laid out for them: the matrix units are
+// busy in 69, 73 and 78% of cycles, at a clock of 1.7 to 1.8 GHz.  Pieces of 2^24 to 2^28 values take the same time.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -248,7 +248,8 @@ __device__ __forceinline__ void transpose_tile(const CrossEntropyArgs& k, uint64
 // What the products need before the first of them, in one launch: rows' scales by the first
 // `scales` blocks, and for dweight (xt not null) the largest |dloss| by the next one and x's
 // transpose, a tile at a time, by the others.  (In launches of their own, with an atomic
-// maximum: gradients of 300 x 1000 x 64 27.3 us, now 24.7; of 2046 x 1216 x 192 41.0, now 36.0.)
+// maximum, against one: gradients of 300 x 1000 x 64 27.3 us / 24.7, of 2046 x 1216 x 192 41.0 /
+// 36.0.)
 template <int TYPE, int COPIES>
 __global__ __launch_bounds__(256) void loss_prepare_kernel(CrossEntropyArgs k, const float* dloss,
                                                            const float* lse, RowScale* rows,
@@ -371,8 +372,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_grad_kernel(
 // of w (k x cols), k in `splits` parts of `per` whose products stand apart; added to what
 // is there after the first piece.  `to` has whole tiles of room for columns.  With `dx` the
 // piece is the last and its only product the whole of it: dx itself, times the rows'
-// factors, instead.  (By way of the sums and a join: gradients of 2046 x 1216 x 192 36.4 us,
-// now 31.9; of 4096 x 131072 x 4096 9663, now 9631.)
+// factors, instead.  (By way of the sums and a join / so: gradients of 2046 x 1216 x 192 36.4 us
+// / 31.9, of 4096 x 131072 x 4096 9663 / 9631.)
 template <class T, int TYPE>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
     Matrix16 dz, Matrix16 w, uint64_t cols, uint32_t k, uint32_t per, float* to, uint64_t ldd,
@@ -448,8 +449,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void loss_dx_kernel(
 }
 
 // dx = the splits' products added in order, times the rows' factors; 8 columns a thread,
-// whose products of 4 splits are in flight at once.  (One block for all of a row: dx of
-// 1 x 32768 x 1024 43.6 us, now 37.8.)
+// whose products of 4 splits are in flight at once.  (One block for all of a row / so: dx
+// of 1 x 32768 x 1024 43.6 us / 37.8.)
 constexpr int kJoinChunks = 64;
 template <int TYPE>
 __global__ __launch_bounds__(kJoinChunks) void loss_dx_join_kernel(

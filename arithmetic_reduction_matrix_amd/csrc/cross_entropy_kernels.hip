@@ -5,9 +5,9 @@
 // kept, and those are joined in order by a second kernel.
 //
 // Many rows are bound by the matrix units and the clock that their power leaves (8192 x
-// 131072 x 4096 bf16 6.0 ms, 1460 TFLOP/s, the rate of a library's product alone; units busy
-// in 80% of cycles at 1.7 GHz), few by reading the weight (8 x 32768 x 1024 14.7 us, 12 of
-// them at 5.4 TB/s).
+// 131072 x 4096 bf16 5.9 to 6.3 ms by card, 1390 to 1500 TFLOP/s, 97 to 99% of the rate of a
+// library's product alone; units busy in 80% of cycles at 1.7 GHz), few by reading the weight
+// (8 x 32768 x 1024 14.7 us, 12 of them at 5.4 TB/s).
 //
 // A row's sums do not depend on the tile that makes them: k runs in order in every
 // tile, a wavefront has 64 columns, and their sum is one tree over them.
