@@ -21,7 +21,8 @@
 // Of 4096 x 131072 x 4096 bf16 (9.4 to 9.9 ms by card) a piece of 32768 takes 833 us for logits
 // and dz, whose second copy is 2% of them, 794 for dx and 760 for dweight, where a library's
 // products alone take 740, 680 and 718 with operands laid out for them: the matrix units are
-// busy in 69, 73 and 78% of cycles, at a clock of 1.7 to 1.8 GHz.  Pieces of 2^24 to 2^28 values take the same time.
+// busy in 69, 73 and 78% of cycles, at a clock of 1.7 to 1.8 GHz.  Pieces of 2^24 to 2^28
+// values take the same time.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

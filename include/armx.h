@@ -693,6 +693,9 @@ int cross_entropy_rows(const void* x, size_t ldx, const void* weight, size_t ldw
  *          scale where 16-bit gradients need one).  What it holds for ignored rows
  *          reaches nothing, nor does their x.
  * lse      device, rows binary32, as cross_entropy_rows wrote them.
+ *          (Another's may be off from the logits as they are here by 2^-13 and 2^-19 of
+ *          the sum of |x * weight| over the target's logit; of one that is off by more,
+ *          binary16's dx may leave its range.)
  * dx       device, rows x cols of `type`, or NULL (not wanted).
  * dweight  device, vocab x cols, or NULL; rows 16-byte aligned in pitches of a
  *          multiple of 8; zeros when rows == 0.
