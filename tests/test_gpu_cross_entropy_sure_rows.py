@@ -27,15 +27,15 @@ def put(values, dtype):
     return m
 
 
-def nearly_sure(rng, cols, logit, dtype, rows=120):
+def nearly_sure(rng, cols, logit, dtype, rows=120, most=-2):
     """Row r's target is word 2 r, and word 2 r + 1 is the only other one near it: half the
-    rows have 1 - p from 1e-5 to 1e-2, the others from 2.4e-4 to 4e-4.  What the words
+    rows have 1 - p from 1e-5 to 10^most, the others from 2.4e-4 to 4e-4.  What the words
     have beside the row's own direction cancels in its logits, and is many times them."""
     x = rng.standard_normal((rows, cols))
     along = x / (x * x).sum(1, keepdims=True)
     noise = rng.standard_normal((rows, cols)) * logit / (6.25 * cols ** 0.5)
     noise -= (noise * x).sum(1, keepdims=True) * along
-    rest = np.where(np.arange(rows) % 2, 10.0 ** rng.uniform(-5, -2, rows),
+    rest = np.where(np.arange(rows) % 2, 10.0 ** rng.uniform(-5, most, rows),
                     rng.uniform(2.4e-4, 4e-4, rows))
     w = np.empty((2 * rows, cols))
     w[::2] = noise + logit * along
@@ -144,3 +144,32 @@ def test_a_word_of_one_token(rows, dtype):
     assert np.all(err <= (HALF[dtype] * size + rest) * 1.02)
     if rows <= 128:
         assert np.all(err <= (HALF[dtype] ** 2 * size + rest) * 1.02)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("cols", [600, 1001, 4096])
+@pytest.mark.parametrize("logit", [100, 400])
+def test_a_target_s_value_is_exact_in_dx(logit, cols, dtype):
+    # A column that no logit sees and in which targets' words have 1: dx there is dz of the
+    # row's target, which is a power of two in 16 bits if its scale is made of the same
+    # logit, bit for bit: it has dx's own rounding and no other.  dweight, where x is 1, has
+    # that dz in two terms.
+    rng = np.random.default_rng(logit * cols)
+    x, w, t = nearly_sure(rng, cols, logit, dtype, most=-0.5)
+    x[:, 0], x[:, 1], w[:, 0] = 0, 1, 0
+    w[::2, 0] = 1
+    rows = x.shape[0]
+    z = f64(x) @ f64(w).T
+    far = np.arange(2 * rows) // 2 != np.arange(rows)[:, None]
+    assert (z - np.diag(z[:, ::2])[:, None])[far].max() < -20   # no other row's words
+    lse = armx.cross_entropy_rows(x, w, t).lse
+    dloss = torch.from_numpy(rng.uniform(512, 1536, rows).astype(np.float32)).cuda()
+    g = armx.cross_entropy_rows_backward(dloss, x, w, t, lse, dweight_dtype=torch.float32)
+    dz, got, half = f64(g.dweight)[::2, 1], f64(g.dx)[:, 0], HALF[dtype]
+    # rows no surer than the magnitudes that are summed allow
+    size = (np.abs(f64(x)) * np.abs(f64(w)[::2])).sum(1)
+    clear = np.abs(dz) > 1.01 * f64(dloss) * np.maximum(2.0 ** -14, 2.0 ** -20 * size)
+    assert clear.sum() > 10
+    tol = np.abs(dz) * (half * (1 + half) + half ** 2 + 16 * U) + FLOOR[dtype] * 1536 * 2.0 ** -14
+    assert np.all((np.abs(got - dz) <= tol + FLOOR[dtype])[clear]), \
+        (np.abs(got - dz) / np.abs(dz) / half)[clear].max()
